@@ -79,7 +79,8 @@ typedef enum pa_device_error {
     PA_DEV_BAD_BLOCK_ID = 2,    /* block id outside [0, num_blocks) (tile read as zeros) */
     PA_DEV_BAD_SEQ_LEN = 3,     /* seq_len < 1, > max_seq_len or > max_blocks_per_seq * block_size */
     PA_DEV_BAD_QUERY_LEN = 4,   /* q_len > seq_len, > max_query_len, or rows beyond total_q */
-    PA_DEV_WAIT_TIMEOUT = 5     /* a pipeline wait gave up (internal error); the CTA stopped */
+    PA_DEV_WAIT_TIMEOUT = 5,    /* a pipeline wait gave up (internal error); the CTA stopped */
+    PA_DEV_BAD_POSITION = 6     /* rotation position outside the cos / sin table (token skipped) */
 } pa_device_error;
 
 /* Human-readable name of a pa_status value (static string, never NULL). */
@@ -182,6 +183,73 @@ pa_status pa_append_tokens(const void* key, const void* value, int64_t key_strid
                            int32_t num_seqs, int32_t total_tokens, int32_t num_kv_heads,
                            int32_t head_dim, int32_t block_size, int32_t num_blocks,
                            int64_t* slot_mapping, int32_t* device_status, void* stream);
+
+/*
+ * pa_qk_norm_rope_append -- this step's new tokens made ready for attention in
+ * one launch: the norm of every q and k head, the position rotation, and the
+ * cache write of pa_append_tokens.  (The pages start from K and V that are
+ * already rotated and have no counterpart of this call; it stands in front of
+ * write_to_paged_cache for models that norm and rotate their heads.)
+ *
+ * For each head x of q and of key at rotation position p, in fp32:
+ *   y = x * w / sqrt(mean(x^2) + eps)        (weight NULL: y = x)
+ *   (y_a, y_b) <- (y_a cos - y_b sin, y_b cos + y_a sin)
+ * for the rot_dim / 2 pairs of its first rot_dim values: pair i is
+ * (i, i + rot_dim / 2), or (2 i, 2 i + 1) if `interleaved` is non-zero.  The
+ * result is rounded once to bf16.  value is copied.
+ *
+ *   q_out          [total_tokens, num_heads, head_dim] bf16 (written); may be
+ *                  q itself when q's token rows are contiguous, and else may
+ *                  not overlap the inputs
+ *   q, key, value  bf16, heads of one token contiguous, token rows q_stride /
+ *                  key_stride / value_stride elements apart (multiples of 8,
+ *                  at least one row): views of one fused projection will do
+ *   q_weight, k_weight  [head_dim] float, or NULL: that side is not normed
+ *   eps            added to the mean square; finite and >= 0
+ *   cos_sin        [max_position, rot_dim] float: row p holds the rot_dim / 2
+ *                  cosines, then as many sines, of position p's pairs
+ *   rot_dim        a multiple of 16, 16 .. head_dim; values past it are not rotated
+ *   positions      optional [total_tokens] int32 rotation positions (NULL: a
+ *                  token's position in its request, as in pa_append_tokens)
+ *   key_cache, value_cache, block_tables, query_start_loc, seq_lens,
+ *   slot_mapping, device_status  as pa_append_tokens
+ * head_dim 64 or 128, any positive block_size.  A token whose slot is out of
+ * range is not written to the cache (its q_out row is); a token whose rotation
+ * position lies outside the table is skipped altogether (slot -1,
+ * PA_DEV_BAD_POSITION).  Rows behind query_start_loc[num_seqs] are left as
+ * they are in q_out and slot_mapping.  num_seqs == 0 or total_tokens == 0 is
+ * a no-op.  A head with a NaN or an infinity norms to NaN.
+ */
+pa_status pa_qk_norm_rope_append(void* q_out, const void* q, const void* key, const void* value,
+                                 int64_t q_stride, int64_t key_stride, int64_t value_stride,
+                                 const float* q_weight, const float* k_weight, float eps,
+                                 const float* cos_sin, int32_t max_position, int32_t rot_dim,
+                                 int32_t interleaved, const int32_t* positions, void* key_cache,
+                                 void* value_cache, const int32_t* block_tables,
+                                 int32_t max_blocks_per_seq, const int32_t* query_start_loc,
+                                 const int32_t* seq_lens, int32_t num_seqs, int32_t total_tokens,
+                                 int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                                 int32_t block_size, int32_t num_blocks, int64_t* slot_mapping,
+                                 int32_t* device_status, void* stream);
+
+/*
+ * pa_qk_norm_rope_append_fp8 -- pa_qk_norm_rope_append into e4m3 caches: the
+ * rotated fp32 key values (not rounded to bf16 in between) and the values are
+ * stored as e4m3(x / scale), rounded as in pa_reshape_and_cache_fp8.  k_scale
+ * and v_scale finite and > 0 (else PA_ERR_INVALID).
+ */
+pa_status pa_qk_norm_rope_append_fp8(void* q_out, const void* q, const void* key, const void* value,
+                                     int64_t q_stride, int64_t key_stride, int64_t value_stride,
+                                     const float* q_weight, const float* k_weight, float eps,
+                                     const float* cos_sin, int32_t max_position, int32_t rot_dim,
+                                     int32_t interleaved, const int32_t* positions, void* key_cache,
+                                     void* value_cache, const int32_t* block_tables,
+                                     int32_t max_blocks_per_seq, const int32_t* query_start_loc,
+                                     const int32_t* seq_lens, int32_t num_seqs, int32_t total_tokens,
+                                     int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                                     int32_t block_size, int32_t num_blocks, float k_scale,
+                                     float v_scale, int64_t* slot_mapping, int32_t* device_status,
+                                     void* stream);
 
 /*
  * pa_map_to_kernel_blocks -- block tables of KV-manager blocks expanded into

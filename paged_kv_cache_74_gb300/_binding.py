@@ -21,13 +21,14 @@ _lib = None
 
 PA_OK, PA_ERR_INVALID, PA_ERR_UNSUPPORTED, PA_ERR_WORKSPACE, PA_ERR_CUDA = range(5)
 DEVICE_ERRORS = {0: "ok", 1: "bad slot", 2: "bad block id", 3: "bad seq_len",
-                 4: "bad query length", 5: "wait timeout"}
+                 4: "bad query length", 5: "wait timeout", 6: "bad rotation position"}
 ABI_SYMBOLS = ("pa_status_string", "pa_abi_version", "pa_reshape_and_cache",
                "pa_compute_slot_mapping", "pa_decode_workspace_size", "pa_decode",
                "pa_prefill_workspace_size", "pa_prefill_varlen", "pa_decode_noalloc",
                "pa_map_to_kernel_blocks", "pa_reshape_and_cache_fp8", "pa_decode_fp8",
                "pa_reshape_and_cache_xsplit", "pa_decode_xsplit", "pa_append_tokens",
-               "pa_reshape_and_cache_xsplit_fp8", "pa_decode_xsplit_fp8", "pa_prefill_varlen_fp8")
+               "pa_reshape_and_cache_xsplit_fp8", "pa_decode_xsplit_fp8", "pa_prefill_varlen_fp8",
+               "pa_qk_norm_rope_append", "pa_qk_norm_rope_append_fp8")
 
 
 class PAError(RuntimeError):
@@ -72,6 +73,12 @@ def _declare(lib):
     lib.pa_append_tokens.restype = ctypes.c_int
     lib.pa_append_tokens.argtypes = [_vp, _vp, _i64, _i64, _vp, _vp, _vp, _i32, _vp, _vp, _i32,
                                      _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp]
+    rope = [_vp] * 4 + [_i64] * 3 + [_vp, _vp, _f32, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _i32,
+                                     _vp, _vp] + [_i32] * 7
+    lib.pa_qk_norm_rope_append.restype = ctypes.c_int
+    lib.pa_qk_norm_rope_append.argtypes = rope + [_vp, _vp, _vp]
+    lib.pa_qk_norm_rope_append_fp8.restype = ctypes.c_int
+    lib.pa_qk_norm_rope_append_fp8.argtypes = rope + [_f32, _f32, _vp, _vp, _vp]
     lib.pa_map_to_kernel_blocks.restype = ctypes.c_int
     lib.pa_map_to_kernel_blocks.argtypes = [_vp, _vp, _i32, _i32, _i32, _vp, _vp]
     lib.pa_decode_workspace_size.restype = _sz
@@ -284,6 +291,93 @@ def append_tokens(key, value, key_cache, value_cache, block_tables, query_start_
         _ptr(block_tables), block_tables.shape[1], _ptr(query_start_loc), _ptr(seq_lens),
         seq_lens.shape[0], T, hkv, d, bs, nb, _ptr(slot_mapping), _ptr(status), _stream()))
     return slot_mapping
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _heads(name, t, T, heads, d):
+    _cuda(name, t, torch.bfloat16)
+    if tuple(t.shape) != (T, heads, d) or t.stride(2) != 1 or t.stride(1) != d:
+        raise ValueError(f"{name} must be [{T}, {heads}, {d}] with contiguous heads")
+
+
+def _qk_norm_rope(fn, cache_dtype, scales, q, key, value, key_cache, value_cache, block_tables,
+                  query_start_loc, seq_lens, cos_sin, q_weight, k_weight, eps, interleaved, positions,
+                  out, slot_mapping, status):
+    _contig("key_cache", key_cache, cache_dtype)
+    _contig("value_cache", value_cache, cache_dtype)
+    _contig("block_tables", block_tables, torch.int32)
+    _contig("query_start_loc", query_start_loc, torch.int32)
+    _contig("seq_lens", seq_lens, torch.int32)
+    _contig("cos_sin", cos_sin, torch.float32)
+    nb, bs, hkv, d = key_cache.shape
+    if value_cache.shape != key_cache.shape:
+        raise ValueError("key_cache and value_cache shapes differ")
+    if q.dim() != 3:
+        raise ValueError("q must be [T, heads, head_dim]")
+    T, hq = q.shape[0], q.shape[1]
+    _heads("q", q, T, hq, d)
+    _heads("key", key, T, hkv, d)
+    _heads("value", value, T, hkv, d)
+    S = seq_lens.shape[0]
+    if block_tables.dim() != 2 or block_tables.shape[0] != S or query_start_loc.shape[0] != S + 1:
+        raise ValueError("block_tables must be [num_seqs, max_blocks] and query_start_loc [num_seqs + 1]")
+    for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if t is not None and tuple(_contig(name, t, torch.float32).shape) != (d,):
+            raise ValueError(f"{name} must be [{d}]")
+    if cos_sin.dim() != 2:
+        raise ValueError("cos_sin must be [max_position, rot_dim]")
+    if positions is not None and _contig("positions", positions, torch.int32).numel() != T:
+        raise ValueError(f"positions must be [{T}]")
+    if slot_mapping is not None and _contig("slot_mapping", slot_mapping, torch.int64).numel() != T:
+        raise ValueError(f"slot_mapping must be [{T}]")
+    if status is not None and _contig("status", status, torch.int32).numel() < 4:
+        raise ValueError("status must hold 4 values")
+    if out is None:
+        out = torch.empty((T, hq, d), dtype=torch.bfloat16, device=q.device)
+    if tuple(_contig("out", out, torch.bfloat16).shape) != (T, hq, d):
+        raise ValueError(f"out must be [{T}, {hq}, {d}]")
+    _same_device(q.device, key=key, value=value, key_cache=key_cache, value_cache=value_cache,
+                 block_tables=block_tables, query_start_loc=query_start_loc, seq_lens=seq_lens,
+                 cos_sin=cos_sin, q_weight=q_weight, k_weight=k_weight, positions=positions, out=out,
+                 slot_mapping=slot_mapping, status=status)
+    with torch.cuda.device(q.device):
+        _check(fn, getattr(load_library(), fn)(
+            _ptr(out), _ptr(q), _ptr(key), _ptr(value), q.stride(0), key.stride(0), value.stride(0),
+            _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(cos_sin), cos_sin.shape[0],
+            cos_sin.shape[1], int(bool(interleaved)), _ptr(positions), _ptr(key_cache),
+            _ptr(value_cache), _ptr(block_tables), block_tables.shape[1], _ptr(query_start_loc),
+            _ptr(seq_lens), S, T, hq, hkv, d, bs, nb, *scales, _ptr(slot_mapping), _ptr(status),
+            _stream()))
+    return out
+
+
+def qk_norm_rope_append(q, key, value, key_cache, value_cache, block_tables, query_start_loc, seq_lens,
+                        cos_sin, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
+                        positions=None, out=None, slot_mapping=None, status=None):
+    """Norm of every q and k head (float weights [d]; None: not normed), rotation
+    by the rows of cos_sin [max_position, rot_dim] (rot_dim / 2 cosines, then
+    sines), and the cache write of append_tokens, in one launch.  Returns the
+    normed, rotated q [T, Hq, d] (out may be q itself if q is contiguous).
+    positions: rotation positions [T] int32 (None: the tokens' positions in
+    their requests)."""
+    return _qk_norm_rope("pa_qk_norm_rope_append", torch.bfloat16, (), q, key, value, key_cache,
+                         value_cache, block_tables, query_start_loc, seq_lens, cos_sin, q_weight,
+                         k_weight, eps, interleaved, positions, out, slot_mapping, status)
+
+
+def qk_norm_rope_append_fp8(q, key, value, key_cache, value_cache, block_tables, query_start_loc,
+                            seq_lens, cos_sin, k_scale, v_scale, q_weight=None, k_weight=None, eps=1e-6,
+                            interleaved=False, positions=None, out=None, slot_mapping=None, status=None):
+    """qk_norm_rope_append into e4m3 caches (uint8 [nb, bs, Hkv, d]): e4m3(x / scale)."""
+    return _qk_norm_rope("pa_qk_norm_rope_append_fp8", torch.uint8, (float(k_scale), float(v_scale)), q,
+                         key, value, key_cache, value_cache, block_tables, query_start_loc, seq_lens,
+                         cos_sin, q_weight, k_weight, eps, interleaved, positions, out, slot_mapping,
+                         status)
 
 
 def map_to_kernel_blocks(block_tables, blocks_per_kv_block, out=None, status=None):

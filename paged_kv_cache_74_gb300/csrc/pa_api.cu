@@ -468,6 +468,84 @@ pa_status launch_decode_rows(void* out, const void* q, const void* key_cache, co
   return err == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
+// Validation and launch of pa_qk_norm_rope_append and its e4m3 form.
+pa_status qk_norm_rope_impl(NormRopeArgs a, int32_t head_dim, bool interleaved, bool kv8, void* stream) {
+  if (a.num_seqs < 0 || a.total_tokens < 0 || a.num_heads < 1 || a.num_kv_heads < 1 ||
+      a.num_blocks < 1 || a.block_size < 1 || a.max_blocks_per_seq < 1 || a.max_position < 1)
+    return PA_ERR_INVALID;
+  if (!std::isfinite(a.eps) || a.eps < 0.f) return PA_ERR_INVALID;
+  if (kv8 && !(std::isfinite(a.k_scale) && a.k_scale > 0.f && std::isfinite(a.v_scale) && a.v_scale > 0.f))
+    return PA_ERR_INVALID;
+  if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+  if (a.rot_dim < 16 || a.rot_dim > head_dim || a.rot_dim % 16 != 0) return PA_ERR_UNSUPPORTED;
+  const int64_t qrow = static_cast<int64_t>(a.num_heads) * head_dim;
+  const int64_t row = static_cast<int64_t>(a.num_kv_heads) * head_dim;
+  if (qrow > (1 << 20) || row > (1 << 20)) return PA_ERR_UNSUPPORTED;
+  if (a.num_seqs == 0 || a.total_tokens == 0) return PA_OK;
+  if (!a.q_out || !a.q || !a.key || !a.value || !a.cos_sin || !a.key_cache || !a.value_cache ||
+      !a.block_tables || !a.query_start_loc || !a.seq_lens)
+    return PA_ERR_INVALID;
+  const void* wide[] = {a.q_out, a.q, a.key, a.value, a.cos_sin, a.key_cache, a.value_cache,
+                        a.q_weight, a.k_weight};
+  for (const void* p : wide)
+    if (!aligned(p, 16)) return PA_ERR_INVALID;
+  if (!aligned(a.block_tables, 4) || !aligned(a.query_start_loc, 4) || !aligned(a.seq_lens, 4) ||
+      !aligned(a.positions, 4) || !aligned(a.slot_mapping, 8) || !aligned(a.status, 4))
+    return PA_ERR_INVALID;
+  if (a.q_stride < qrow || a.key_stride < row || a.value_stride < row || a.q_stride % 8 != 0 ||
+      a.key_stride % 8 != 0 || a.value_stride % 8 != 0)
+    return PA_ERR_INVALID;
+  if (a.q_out == a.q && a.q_stride != qrow) return PA_ERR_INVALID;
+  return launch_qk_norm_rope(a, head_dim, kv8, interleaved, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
+}
+
+NormRopeArgs norm_rope_args(void* q_out, const void* q, const void* key, const void* value,
+                            int64_t q_stride, int64_t key_stride, int64_t value_stride,
+                            const float* q_weight, const float* k_weight, float eps,
+                            const float* cos_sin, int32_t max_position, int32_t rot_dim,
+                            const int32_t* positions, void* key_cache, void* value_cache,
+                            const int32_t* block_tables, int32_t max_blocks_per_seq,
+                            const int32_t* query_start_loc, const int32_t* seq_lens, int32_t num_seqs,
+                            int32_t total_tokens, int32_t num_heads, int32_t num_kv_heads,
+                            int32_t block_size, int32_t num_blocks, float k_scale, float v_scale,
+                            int64_t* slot_mapping, int32_t* device_status) {
+  NormRopeArgs a;
+  a.q_out = static_cast<__nv_bfloat16*>(q_out);
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.key = static_cast<const __nv_bfloat16*>(key);
+  a.value = static_cast<const __nv_bfloat16*>(value);
+  a.q_stride = q_stride;
+  a.key_stride = key_stride;
+  a.value_stride = value_stride;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.cos_sin = cos_sin;
+  a.positions = positions;
+  a.key_cache = key_cache;
+  a.value_cache = value_cache;
+  a.block_tables = block_tables;
+  a.query_start_loc = query_start_loc;
+  a.seq_lens = seq_lens;
+  a.slot_mapping = slot_mapping;
+  a.status = device_status;
+  a.eps = eps;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.max_position = max_position;
+  a.rot_dim = rot_dim;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.num_seqs = num_seqs;
+  a.total_tokens = total_tokens;
+  a.num_heads = num_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.block_size = block_size;
+  a.num_blocks = num_blocks;
+  a.warps_per_token = 1;
+  return a;
+}
+
 }  // namespace
 }  // namespace pa
 
@@ -592,6 +670,45 @@ pa_status pa_append_tokens(const void* key, const void* value, int64_t key_strid
       num_blocks, static_cast<int>(row), slot_mapping, device_status,
       static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+pa_status pa_qk_norm_rope_append(void* q_out, const void* q, const void* key, const void* value,
+                                 int64_t q_stride, int64_t key_stride, int64_t value_stride,
+                                 const float* q_weight, const float* k_weight, float eps,
+                                 const float* cos_sin, int32_t max_position, int32_t rot_dim,
+                                 int32_t interleaved, const int32_t* positions, void* key_cache,
+                                 void* value_cache, const int32_t* block_tables,
+                                 int32_t max_blocks_per_seq, const int32_t* query_start_loc,
+                                 const int32_t* seq_lens, int32_t num_seqs, int32_t total_tokens,
+                                 int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                                 int32_t block_size, int32_t num_blocks, int64_t* slot_mapping,
+                                 int32_t* device_status, void* stream) {
+  return qk_norm_rope_impl(
+      norm_rope_args(q_out, q, key, value, q_stride, key_stride, value_stride, q_weight, k_weight, eps,
+                     cos_sin, max_position, rot_dim, positions, key_cache, value_cache, block_tables,
+                     max_blocks_per_seq, query_start_loc, seq_lens, num_seqs, total_tokens, num_heads,
+                     num_kv_heads, block_size, num_blocks, 1.f, 1.f, slot_mapping, device_status),
+      head_dim, interleaved != 0, false, stream);
+}
+
+pa_status pa_qk_norm_rope_append_fp8(void* q_out, const void* q, const void* key, const void* value,
+                                     int64_t q_stride, int64_t key_stride, int64_t value_stride,
+                                     const float* q_weight, const float* k_weight, float eps,
+                                     const float* cos_sin, int32_t max_position, int32_t rot_dim,
+                                     int32_t interleaved, const int32_t* positions, void* key_cache,
+                                     void* value_cache, const int32_t* block_tables,
+                                     int32_t max_blocks_per_seq, const int32_t* query_start_loc,
+                                     const int32_t* seq_lens, int32_t num_seqs, int32_t total_tokens,
+                                     int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                                     int32_t block_size, int32_t num_blocks, float k_scale,
+                                     float v_scale, int64_t* slot_mapping, int32_t* device_status,
+                                     void* stream) {
+  return qk_norm_rope_impl(
+      norm_rope_args(q_out, q, key, value, q_stride, key_stride, value_stride, q_weight, k_weight, eps,
+                     cos_sin, max_position, rot_dim, positions, key_cache, value_cache, block_tables,
+                     max_blocks_per_seq, query_start_loc, seq_lens, num_seqs, total_tokens, num_heads,
+                     num_kv_heads, block_size, num_blocks, k_scale, v_scale, slot_mapping, device_status),
+      head_dim, interleaved != 0, true, stream);
 }
 
 pa_status pa_map_to_kernel_blocks(int32_t* kernel_tables, const int32_t* block_tables,

@@ -198,4 +198,31 @@ cudaError_t launch_slot_mapping(int64_t* slot_mapping, int total_tokens, const i
                                 const int32_t* seq_lens, int num_seqs, int block_size,
                                 int num_blocks, int32_t* status, cudaStream_t stream);
 
+// Norm, rotation and cache write of the new tokens (qk_norm_rope.cu).
+struct NormRopeArgs {
+  __nv_bfloat16* q_out;             // [total_tokens, num_heads, D]
+  const __nv_bfloat16* q;           // token rows q_stride elements apart (may be q_out)
+  const __nv_bfloat16* key;
+  const __nv_bfloat16* value;
+  int64_t q_stride, key_stride, value_stride;
+  const float* q_weight;            // [D] or nullptr: q heads are not normed
+  const float* k_weight;
+  const float* cos_sin;             // [max_position, rot_dim]: rot_dim / 2 cos, then as many sin
+  const int32_t* positions;         // [total_tokens] rotation positions, or nullptr: the cache positions
+  void* key_cache;                  // token-major, bf16 or e4m3
+  void* value_cache;
+  const int32_t* block_tables;
+  const int32_t* query_start_loc;
+  const int32_t* seq_lens;
+  int64_t* slot_mapping;            // optional output
+  int32_t* status;
+  float eps, k_scale, v_scale;
+  int max_position, rot_dim;
+  int max_blocks_per_seq, num_seqs, total_tokens;
+  int num_heads, num_kv_heads, block_size, num_blocks;
+  int warps_per_token;              // set by the launcher
+};
+cudaError_t launch_qk_norm_rope(NormRopeArgs a, int head_dim, bool kv8, bool interleaved,
+                                cudaStream_t stream);
+
 }  // namespace pa
