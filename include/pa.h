@@ -392,6 +392,59 @@ pa_status pa_decode_fp8(void* out, const void* q, const void* key_cache, const v
                         size_t workspace_bytes, void* stream);
 
 /*
+ * pa_decode_masked -- pa_decode with modified scores: capped by a tanh, biased
+ * by distance, and masked to a prefix and a run of keys ending at the row's
+ * own position.  (The pages' kernels take alibi_slopes but no cap or mask;
+ * the call is pa_decode's neighbour for models that need them.)
+ *
+ *   softcap       0: none; else finite > 0
+ *   slopes        optional [num_heads] float distance slopes (NULL = none)
+ *   key_starts    optional int32, one per query row (here [num_seqs]): the
+ *                 first key of the row's run (NULL = 0 for every row)
+ *   prefix_lens   optional int32 [num_seqs]: the keys of each request that all
+ *                 its rows see (NULL = 0)
+ * The row at position p (here seq_lens[r] - 1) scores key j
+ *   s = scale * (q . k);  s = softcap * tanh(s / softcap);  s -= slopes[h] * |p - j|
+ * and sees it if j < prefix_lens[r] or key_starts[row] <= j <= p; out is the
+ * softmax over the seen keys, exact in fp32 as in pa_decode (the tanh to 1e-6
+ * of the score).  A sliding window of w keys is key_starts = p - w + 1, with the
+ * first n tokens kept in sight by prefix_lens = n; documents packed into one
+ * request have key_starts = the first token of the row's document.  Any values
+ * are allowed: prefix_lens and key_starts are clipped to [0, seq_len]; a row
+ * that sees no key gives zeros.
+ * Keys that the row does not see may hold anything (NaN and infinities
+ * included), and blocks (of 16 tokens, whatever block_size) without a seen key
+ * are not read, nor are their block_tables entries: blocks that have left a
+ * window may be reused.
+ * Other arguments, workspace (pa_decode_workspace_size), sizes and errors as
+ * pa_decode; always the warp-level tensor-core decode: groups of more than 4
+ * q heads are cut into units of at most 4 as in pa_decode_xsplit.
+ */
+pa_status pa_decode_masked(void* out, const void* q, const void* key_cache, const void* value_cache,
+                           const int32_t* block_tables, int32_t max_blocks_per_seq,
+                           const int32_t* seq_lens, int32_t num_seqs, int32_t max_seq_len,
+                           int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                           int32_t block_size, int32_t num_blocks, float scale, float softcap,
+                           const float* slopes, const int32_t* key_starts, const int32_t* prefix_lens,
+                           int32_t partition_tokens, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/*
+ * pa_decode_masked_fp8 -- pa_decode_masked over an e4m3 cache, as pa_decode_fp8
+ * is to pa_decode (scores and values scaled by k_scale and v_scale before the
+ * cap and the bias).
+ */
+pa_status pa_decode_masked_fp8(void* out, const void* q, const void* key_cache, const void* value_cache,
+                               const int32_t* block_tables, int32_t max_blocks_per_seq,
+                               const int32_t* seq_lens, int32_t num_seqs, int32_t max_seq_len,
+                               int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                               int32_t block_size, int32_t num_blocks, float scale, float k_scale,
+                               float v_scale, float softcap, const float* slopes,
+                               const int32_t* key_starts, const int32_t* prefix_lens,
+                               int32_t partition_tokens, void* workspace, size_t workspace_bytes,
+                               void* stream);
+
+/*
  * The x-split cache layout ("vLLM 深度解析（二）", section 3.2.1: the
  * layout of the pages' own CUDA-core decode kernel), for drop-in use of
  * caches laid out that way:

@@ -28,7 +28,8 @@ ABI_SYMBOLS = ("pa_status_string", "pa_abi_version", "pa_reshape_and_cache",
                "pa_map_to_kernel_blocks", "pa_reshape_and_cache_fp8", "pa_decode_fp8",
                "pa_reshape_and_cache_xsplit", "pa_decode_xsplit", "pa_append_tokens",
                "pa_reshape_and_cache_xsplit_fp8", "pa_decode_xsplit_fp8", "pa_prefill_varlen_fp8",
-               "pa_qk_norm_rope_append", "pa_qk_norm_rope_append_fp8")
+               "pa_qk_norm_rope_append", "pa_qk_norm_rope_append_fp8", "pa_decode_masked",
+               "pa_decode_masked_fp8")
 
 
 class PAError(RuntimeError):
@@ -86,6 +87,11 @@ def _declare(lib):
     lib.pa_decode.restype = ctypes.c_int
     lib.pa_decode.argtypes = [_vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32,
                               _i32, _i32, _f32, _i32, _vp, _sz, _vp]
+    dec = [_vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _f32]
+    lib.pa_decode_masked.restype = ctypes.c_int
+    lib.pa_decode_masked.argtypes = dec + [_f32, _vp, _vp, _vp, _i32, _vp, _sz, _vp]
+    lib.pa_decode_masked_fp8.restype = ctypes.c_int
+    lib.pa_decode_masked_fp8.argtypes = dec + [_f32, _f32, _f32, _vp, _vp, _vp, _i32, _vp, _sz, _vp]
     lib.pa_decode_noalloc.restype = ctypes.c_int
     lib.pa_decode_noalloc.argtypes = [_vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32,
                                       _i32, _i32, _i32, _f32, _i32, _vp, _vp]
@@ -534,6 +540,79 @@ def decode_noalloc(q, key_cache, value_cache, block_tables, seq_lens, max_seq_le
         block_tables.shape[1], _ptr(seq_lens), S, int(max_seq_len), hq, hkv, d, bs, nb,
         float(scale), int(partition_tokens), _ptr(status), _stream()))
     return out
+
+
+def _masks(q, rows, num_seqs, slopes, key_starts, prefix_lens):
+    if slopes is not None and _contig("slopes", slopes, torch.float32).numel() != q.shape[1]:
+        raise ValueError(f"slopes must be [{q.shape[1]}]")
+    if key_starts is not None and _contig("key_starts", key_starts, torch.int32).numel() != rows:
+        raise ValueError(f"key_starts must be [{rows}]")
+    if prefix_lens is not None and _contig("prefix_lens", prefix_lens, torch.int32).numel() != num_seqs:
+        raise ValueError(f"prefix_lens must be [{num_seqs}]")
+
+
+def _attention_args(q, key_cache, value_cache, cache_dtype, block_tables, seq_lens, out):
+    """Checks shared by the masked attention calls; returns out."""
+    _contig("q", q, torch.bfloat16)
+    _contig("key_cache", key_cache, cache_dtype)
+    _contig("value_cache", value_cache, cache_dtype)
+    _contig("block_tables", block_tables, torch.int32)
+    _contig("seq_lens", seq_lens, torch.int32)
+    if q.dim() != 3 or key_cache.dim() != 4 or key_cache.shape[3] != q.shape[2] or \
+            value_cache.shape != key_cache.shape:
+        raise ValueError("cache shapes do not match q")
+    if block_tables.dim() != 2 or block_tables.shape[0] != seq_lens.shape[0]:
+        raise ValueError("block_tables must be [num_seqs, max_blocks]")
+    if out is None:
+        out = torch.empty_like(q)
+    if _contig("out", out, torch.bfloat16).shape != q.shape:
+        raise ValueError("out must have q's shape")
+    return out
+
+
+def _decode_masked(fn, cache_dtype, scales, q, key_cache, value_cache, block_tables, seq_lens,
+                   max_seq_len, scale, softcap, slopes, key_starts, prefix_lens, out, workspace,
+                   partition_tokens):
+    out = _attention_args(q, key_cache, value_cache, cache_dtype, block_tables, seq_lens, out)
+    S, hq, d = q.shape
+    nb, bs, hkv, _ = key_cache.shape
+    if seq_lens.shape[0] != S:
+        raise ValueError(f"seq_lens must be [{S}]")
+    _masks(q, S, S, slopes, key_starts, prefix_lens)
+    _same_device(q.device, key_cache=key_cache, value_cache=value_cache, block_tables=block_tables,
+                 seq_lens=seq_lens, slopes=slopes, key_starts=key_starts, prefix_lens=prefix_lens,
+                 out=out, workspace=workspace)
+    with torch.cuda.device(q.device):
+        if workspace is None:
+            workspace = new_workspace(
+                decode_workspace_size(S, hq, hkv, d, max_seq_len, partition_tokens), q.device)
+        _check(fn, getattr(load_library(), fn)(
+            _ptr(out), _ptr(q), _ptr(key_cache), _ptr(value_cache), _ptr(block_tables),
+            block_tables.shape[1], _ptr(seq_lens), S, int(max_seq_len), hq, hkv, d, bs, nb,
+            float(scale), *scales, float(softcap), _ptr(slopes), _ptr(key_starts), _ptr(prefix_lens),
+            int(partition_tokens), _ptr(workspace), workspace.numel(), _stream()))
+    return out
+
+
+def decode_masked(q, key_cache, value_cache, block_tables, seq_lens, max_seq_len, scale, softcap=0.0,
+                  slopes=None, key_starts=None, prefix_lens=None, out=None, workspace=None,
+                  partition_tokens=0):
+    """Paged decode with modified scores: s = scale q.k, then softcap tanh(s /
+    softcap) (0: none), then - slopes[h] |p - j| (float [Hq]); a row sees keys
+    j < prefix_lens[r] (int32 [S]) and key_starts[row] <= j <= p (int32 [S]).
+    A row that sees no key gives zeros."""
+    return _decode_masked("pa_decode_masked", torch.bfloat16, (), q, key_cache, value_cache, block_tables,
+                          seq_lens, max_seq_len, scale, softcap, slopes, key_starts, prefix_lens, out,
+                          workspace, partition_tokens)
+
+
+def decode_masked_fp8(q, key_cache, value_cache, block_tables, seq_lens, max_seq_len, scale, k_scale,
+                      v_scale, softcap=0.0, slopes=None, key_starts=None, prefix_lens=None, out=None,
+                      workspace=None, partition_tokens=0):
+    """decode_masked over e4m3 caches (uint8 [nb, bs, Hkv, d]) with their scales."""
+    return _decode_masked("pa_decode_masked_fp8", torch.uint8, (float(k_scale), float(v_scale)), q,
+                          key_cache, value_cache, block_tables, seq_lens, max_seq_len, scale, softcap,
+                          slopes, key_starts, prefix_lens, out, workspace, partition_tokens)
 
 
 def prefill_workspace_size(num_seqs, total_q, num_heads, num_kv_heads, head_dim, max_seq_len):

@@ -1,0 +1,30 @@
+// decode_masked.cu -- the streaming paged decode with modified scores (tanh
+// cap, distance bias, prefix and first-key masks): launchers of the MOD
+// instantiations of decode_kernel.cuh.
+//
+// The kernel is bound by the K/V bytes of the visible keys, as the plain
+// decode is; tiles without a visible key are not loaded.  Groups of more than 4
+// q heads are cut into units of at most 4 that each read their kv head's K/V
+// (the units of a kv head are neighbours in the tile order, so the repeated
+// reads mostly hit L2).
+#include "decode_kernel.cuh"
+
+namespace pa {
+
+cudaError_t launch_decode_masked(const DecodeArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                                 int head_dim, bool kv8, cudaStream_t stream) {
+  // e4m3 units of two kv heads (8 q heads, head_dim 128).
+  if (kv8 && a.group == 8 && head_dim == 128)
+    return launch_decode_impl<128, 8, true, false, false, true>(a, kmap, vmap, stream);
+  const int gmax = decode_gmax(a.group);
+#define PA_DECODE_CASE(DD, GG)                                                            \
+  if (head_dim == DD && gmax == GG)                                                       \
+    return kv8 ? launch_decode_impl<DD, GG, true, false, false, true>(a, kmap, vmap, stream) \
+               : launch_decode_impl<DD, GG, false, false, false, true>(a, kmap, vmap, stream);
+  PA_DECODE_CASE(128, 1) PA_DECODE_CASE(128, 2) PA_DECODE_CASE(128, 4)
+  PA_DECODE_CASE(64, 1) PA_DECODE_CASE(64, 2) PA_DECODE_CASE(64, 4)
+#undef PA_DECODE_CASE
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace pa

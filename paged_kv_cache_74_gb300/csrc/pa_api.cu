@@ -400,13 +400,14 @@ pa_status launch_decode_rows(void* out, const void* q, const void* key_cache, co
                              int32_t num_blocks, int32_t block_size, float scale,
                              const DecodeLayout& L, void* workspace, cudaStream_t stream,
                              const KvFormat& kv = KvFormat(), bool after_prefill = false,
-                             int tile_sms = 0, int max_query_len = 0) {
+                             int tile_sms = 0, int max_query_len = 0,
+                             const ScoreMods* mods = nullptr) {
   // The TMA views address the cache in 16-token tiles.
   const int num_tiles16 = num_blocks * (block_size / kBlockSize);
   const int group = num_heads / num_kv_heads;
-  const bool tc = !kv.xsplit && decode_uses_tc(head_dim, group);
-  // x-split: units of up to 4 q heads (see xsplit_heads_per_unit).
-  const int unit_heads = kv.xsplit ? xsplit_heads_per_unit(group) : group;
+  const bool tc = !kv.xsplit && mods == nullptr && decode_uses_tc(head_dim, group);
+  // x-split and modified scores: units of up to 4 q heads (see xsplit_heads_per_unit).
+  const int unit_heads = kv.xsplit || mods != nullptr ? xsplit_heads_per_unit(group) : group;
   const int kv_div = group / unit_heads;
   const bool pair = kv.pair && kv.e4m3 && !kv.xsplit && !tc && decode_fp8_pairs(head_dim, num_heads, num_kv_heads);
   if (kv.pair && !pair) return PA_ERR_INVALID;
@@ -463,9 +464,59 @@ pa_status launch_decode_rows(void* out, const void* q, const void* key_cache, co
   a.tile_sms = tile_sms;
   a.ctas_per_sm = tile_sms > 0 ? static_cast<int>(L.num_ctas / tile_sms) : 0;
   a.max_query_len = max_query_len;
-  const cudaError_t err = tc ? launch_decode_tc(a, qmap, kmap, vmap, head_dim, kv.e4m3, stream)
-                            : launch_decode(a, kmap, vmap, head_dim, kv.e4m3, kv.xsplit, stream);
+  if (mods != nullptr) a.mods = *mods;
+  const cudaError_t err = mods != nullptr ? launch_decode_masked(a, kmap, vmap, head_dim, kv.e4m3, stream)
+                          : tc            ? launch_decode_tc(a, qmap, kmap, vmap, head_dim, kv.e4m3, stream)
+                                          : launch_decode(a, kmap, vmap, head_dim, kv.e4m3, kv.xsplit, stream);
   return err == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+// The score modifications of a masked call; false if they are invalid.
+bool make_mods(ScoreMods* m, float scale, float k_scale, float softcap, const float* slopes,
+               const int32_t* key_starts, const int32_t* prefix_lens) {
+  if (!std::isfinite(softcap) || softcap < 0.f) return false;
+  if (!aligned(slopes, 4) || !aligned(key_starts, 4) || !aligned(prefix_lens, 4)) return false;
+  m->slopes = slopes;
+  m->key_starts = key_starts;
+  m->prefix_lens = prefix_lens;
+  if (softcap > 0.f) {
+    m->cap_in = scale * k_scale / softcap;
+    m->cap_log2 = softcap * 1.4426950408889634f;
+    if (!std::isfinite(m->cap_in) || !std::isfinite(m->cap_log2)) return false;
+  }
+  return true;
+}
+
+// pa_decode_masked and its e4m3 form.
+pa_status decode_masked_impl(void* out, const void* q, const void* key_cache, const void* value_cache,
+                             const int32_t* block_tables, int32_t max_blocks_per_seq,
+                             const int32_t* seq_lens, int32_t num_seqs, int32_t max_seq_len,
+                             int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                             int32_t block_size, int32_t num_blocks, float scale, float softcap,
+                             const float* slopes, const int32_t* key_starts, const int32_t* prefix_lens,
+                             int32_t partition_tokens, void* workspace, size_t workspace_bytes,
+                             void* stream, KvFormat kv) {
+  const pa_status st = check_decode_args(out, q, key_cache, value_cache, block_tables, max_blocks_per_seq,
+                                         seq_lens, num_seqs, max_seq_len, num_heads, num_kv_heads,
+                                         head_dim, block_size, num_blocks, scale);
+  if (st != PA_OK) return st;
+  ScoreMods mods;
+  if (!make_mods(&mods, scale, kv.k_scale, softcap, slopes, key_starts, prefix_lens)) return PA_ERR_INVALID;
+  if (partition_tokens < 0 || partition_tokens % kBlockSize != 0) return PA_ERR_INVALID;
+  if (num_seqs == 0) return PA_OK;
+  kv.pair = kv.e4m3 && decode_fp8_pairs(head_dim, num_heads, num_kv_heads);
+  const int group = num_heads / num_kv_heads;
+  const int units = kv.pair ? num_kv_heads / 2 : num_kv_heads * (group / xsplit_heads_per_unit(group));
+  if (units > 65535) return PA_ERR_UNSUPPORTED;
+  const DecodeLayout L =
+      decode_layout(num_seqs, num_heads, units, head_dim, max_seq_len, partition_tokens, kv.pair);
+  if (L.num_ctas > kMaxDecodeCtas) return PA_ERR_UNSUPPORTED;
+  if (!workspace || workspace_bytes < L.total) return PA_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return PA_ERR_INVALID;
+  return launch_decode_rows(out, q, key_cache, value_cache, block_tables, max_blocks_per_seq, seq_lens,
+                            nullptr, num_seqs, num_seqs, max_seq_len, num_heads, num_kv_heads, head_dim,
+                            num_blocks, block_size, scale, L, workspace,
+                            static_cast<cudaStream_t>(stream), kv, false, 0, 0, &mods);
 }
 
 // Validation and launch of pa_qk_norm_rope_append and its e4m3 form.
@@ -802,6 +853,41 @@ pa_status pa_decode_fp8(void* out, const void* q, const void* key_cache, const v
                             seq_lens, nullptr, num_seqs, num_seqs, max_seq_len, num_heads,
                             num_kv_heads, head_dim, num_blocks, block_size, scale, L, workspace,
                             static_cast<cudaStream_t>(stream), kv);
+}
+
+pa_status pa_decode_masked(void* out, const void* q, const void* key_cache, const void* value_cache,
+                           const int32_t* block_tables, int32_t max_blocks_per_seq,
+                           const int32_t* seq_lens, int32_t num_seqs, int32_t max_seq_len,
+                           int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                           int32_t block_size, int32_t num_blocks, float scale, float softcap,
+                           const float* slopes, const int32_t* key_starts, const int32_t* prefix_lens,
+                           int32_t partition_tokens, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  return decode_masked_impl(out, q, key_cache, value_cache, block_tables, max_blocks_per_seq, seq_lens,
+                            num_seqs, max_seq_len, num_heads, num_kv_heads, head_dim, block_size,
+                            num_blocks, scale, softcap, slopes, key_starts, prefix_lens, partition_tokens,
+                            workspace, workspace_bytes, stream, KvFormat());
+}
+
+pa_status pa_decode_masked_fp8(void* out, const void* q, const void* key_cache, const void* value_cache,
+                               const int32_t* block_tables, int32_t max_blocks_per_seq,
+                               const int32_t* seq_lens, int32_t num_seqs, int32_t max_seq_len,
+                               int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                               int32_t block_size, int32_t num_blocks, float scale, float k_scale,
+                               float v_scale, float softcap, const float* slopes,
+                               const int32_t* key_starts, const int32_t* prefix_lens,
+                               int32_t partition_tokens, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+  if (!(std::isfinite(k_scale) && k_scale > 0.f && std::isfinite(v_scale) && v_scale > 0.f))
+    return PA_ERR_INVALID;
+  KvFormat kv;
+  kv.e4m3 = true;
+  kv.k_scale = k_scale;
+  kv.v_scale = v_scale;
+  return decode_masked_impl(out, q, key_cache, value_cache, block_tables, max_blocks_per_seq, seq_lens,
+                            num_seqs, max_seq_len, num_heads, num_kv_heads, head_dim, block_size,
+                            num_blocks, scale, softcap, slopes, key_starts, prefix_lens, partition_tokens,
+                            workspace, workspace_bytes, stream, kv);
 }
 
 pa_status pa_reshape_and_cache_xsplit(const void* key, const void* value, int64_t key_stride,

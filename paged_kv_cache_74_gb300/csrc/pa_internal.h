@@ -19,6 +19,16 @@ namespace pa {
 constexpr int kBlockSize = 16;
 constexpr int kWorkspaceHeader = 256; // status record + padding at the start of a workspace
 
+// Modified scores of the masked attention calls (score_mods.cuh).  All zero:
+// plain causal attention.
+struct ScoreMods {
+  const float* slopes = nullptr;         // [num_heads] distance bias, or none
+  const int32_t* key_starts = nullptr;   // [q rows] first key of the causal part, or none (0)
+  const int32_t* prefix_lens = nullptr;  // [num_seqs] keys every row sees, or none (0)
+  float cap_in = 0.f;                    // softmax scale (* k_scale) / cap
+  float cap_log2 = 0.f;                  // cap * log2(e); 0: no cap
+};
+
 // Decode work.  The tiles (request, kv head, block) of all decode rows are
 // numbered request-major, then kv head, then block; the W tiles are split
 // into num_ctas contiguous, equal ranges, one per CTA of a persistent grid.
@@ -64,6 +74,7 @@ struct DecodeArgs {
   int tile_sms;
   int ctas_per_sm;
   int max_query_len;                // of the call (the tile kernel's row checks)
+  ScoreMods mods;                   // masked calls only
 };
 
 // Launch `kernel` on `stream` with programmatic stream serialization: the
@@ -97,6 +108,9 @@ cudaError_t launch_overlapped(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
 // head_dim, 1, 1}, 32-byte swizzled.
 cudaError_t launch_decode(const DecodeArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
                           int head_dim, bool kv8, bool xsplit, cudaStream_t stream);
+// The same kernel with modified scores (decode_masked.cu), token-major caches.
+cudaError_t launch_decode_masked(const DecodeArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                                 int head_dim, bool kv8, cudaStream_t stream);
 // Tensor-core decode (decode_tc.cu): qmap = q as {head_dim, heads, rows}
 // with a {64, group, 1} box; kmap, vmap = bf16 caches as {64, 8, head_dim /
 // 64, slots / 8, kv heads} with a {64, 8, head_dim / 64, 2, 1} box (one

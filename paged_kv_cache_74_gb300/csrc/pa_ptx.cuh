@@ -447,6 +447,13 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
+// Hardware reciprocal (PTX rcp.approx, 1 ulp); 1 / infinity = 0.
+__device__ __forceinline__ float fast_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 __device__ __forceinline__ float2 ld_shared_f2(uint32_t addr) {
   float2 v;
   asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
