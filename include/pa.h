@@ -597,6 +597,58 @@ pa_status pa_prefill_varlen_fp8(void* out, const void* q, const void* key_cache,
                                 float k_scale, float v_scale, void* workspace,
                                 size_t workspace_bytes, void* stream);
 
+/*
+ * pa_prefill_masked_workspace_size -- bytes of workspace
+ * pa_prefill_varlen_masked needs (pa_prefill_workspace_size and the plan of its
+ * query tiles).  Returns 0 for invalid arguments.
+ */
+size_t pa_prefill_masked_workspace_size(int32_t num_seqs, int32_t total_q, int32_t num_heads,
+                                        int32_t num_kv_heads, int32_t head_dim, int32_t max_seq_len);
+
+/*
+ * pa_prefill_varlen_masked -- pa_prefill_varlen with the modified scores of
+ * pa_decode_masked: softcap, slopes [num_heads], key_starts [total_q] (one per
+ * query row, in any order within a request) and prefix_lens [num_seqs].  The
+ * row at position p sees key j if j < prefix_lens[r] or key_starts[row] <= j <= p:
+ * a prefix is seen by all rows of its request, those before its end included
+ * (its keys must be in the cache: prefix_lens is clipped to seq_lens), and the
+ * distance bias of a key behind the row is by |p - j| as well.
+ * Keys that no row of a request's 128-row query tile sees may hold anything,
+ * and 16-token blocks without a seen key are not read; V of a key that some
+ * row of the tile sees must be finite (a weight of 0 does not cancel an
+ * infinity in the tile's product).  Rows that see no key give zeros.
+ * When max_query_len > 1 a first kernel plans the query tiles (which keys each
+ * needs), then the tile kernel and the decode kernel follow as in
+ * pa_prefill_varlen, without the split of the SMs between them.  Other
+ * arguments, sizes and errors as pa_prefill_varlen; rows with q_len == 1 run as
+ * in pa_decode_masked.
+ */
+pa_status pa_prefill_varlen_masked(void* out, const void* q, const void* key_cache,
+                                   const void* value_cache, const int32_t* query_start_loc,
+                                   const int32_t* seq_lens, int32_t num_seqs, int32_t total_q,
+                                   int32_t max_query_len, int32_t max_seq_len,
+                                   const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                   int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                                   int32_t block_size, int32_t num_blocks, float scale, float softcap,
+                                   const float* slopes, const int32_t* key_starts,
+                                   const int32_t* prefix_lens, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
+/*
+ * pa_prefill_varlen_masked_fp8 -- pa_prefill_varlen_masked over e4m3 caches, as
+ * pa_prefill_varlen_fp8 is to pa_prefill_varlen.
+ */
+pa_status pa_prefill_varlen_masked_fp8(void* out, const void* q, const void* key_cache,
+                                       const void* value_cache, const int32_t* query_start_loc,
+                                       const int32_t* seq_lens, int32_t num_seqs, int32_t total_q,
+                                       int32_t max_query_len, int32_t max_seq_len,
+                                       const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                       int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                                       int32_t block_size, int32_t num_blocks, float scale,
+                                       float k_scale, float v_scale, float softcap, const float* slopes,
+                                       const int32_t* key_starts, const int32_t* prefix_lens,
+                                       void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

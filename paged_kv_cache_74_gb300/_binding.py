@@ -29,7 +29,8 @@ ABI_SYMBOLS = ("pa_status_string", "pa_abi_version", "pa_reshape_and_cache",
                "pa_reshape_and_cache_xsplit", "pa_decode_xsplit", "pa_append_tokens",
                "pa_reshape_and_cache_xsplit_fp8", "pa_decode_xsplit_fp8", "pa_prefill_varlen_fp8",
                "pa_qk_norm_rope_append", "pa_qk_norm_rope_append_fp8", "pa_decode_masked",
-               "pa_decode_masked_fp8")
+               "pa_decode_masked_fp8", "pa_prefill_masked_workspace_size", "pa_prefill_varlen_masked",
+               "pa_prefill_varlen_masked_fp8")
 
 
 class PAError(RuntimeError):
@@ -104,6 +105,13 @@ def _declare(lib):
     lib.pa_prefill_varlen_fp8.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp,
                                           _i32, _i32, _i32, _i32, _i32, _i32, _f32, _f32, _f32, _vp,
                                           _sz, _vp]
+    lib.pa_prefill_masked_workspace_size.restype = _sz
+    lib.pa_prefill_masked_workspace_size.argtypes = [_i32, _i32, _i32, _i32, _i32, _i32]
+    pre = [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _f32]
+    lib.pa_prefill_varlen_masked.restype = ctypes.c_int
+    lib.pa_prefill_varlen_masked.argtypes = pre + [_f32, _vp, _vp, _vp, _vp, _sz, _vp]
+    lib.pa_prefill_varlen_masked_fp8.restype = ctypes.c_int
+    lib.pa_prefill_varlen_masked_fp8.argtypes = pre + [_f32, _f32, _f32, _vp, _vp, _vp, _vp, _sz, _vp]
     return lib
 
 
@@ -672,6 +680,58 @@ def prefill_varlen_fp8(q, key_cache, value_cache, query_start_loc, seq_lens, blo
         block_tables.shape[1], hq, hkv, d, bs, nb, float(scale), float(k_scale), float(v_scale),
         _ptr(workspace), workspace.numel(), _stream()))
     return out
+
+
+def prefill_masked_workspace_size(num_seqs, total_q, num_heads, num_kv_heads, head_dim, max_seq_len):
+    return int(load_library().pa_prefill_masked_workspace_size(num_seqs, total_q, num_heads,
+                                                               num_kv_heads, head_dim, max_seq_len))
+
+
+def _prefill_masked(fn, cache_dtype, scales, q, key_cache, value_cache, query_start_loc, seq_lens,
+                    block_tables, max_query_len, max_seq_len, scale, softcap, slopes, key_starts,
+                    prefix_lens, out, workspace):
+    out = _attention_args(q, key_cache, value_cache, cache_dtype, block_tables, seq_lens, out)
+    tq, hq, d = q.shape
+    nb, bs, hkv, _ = key_cache.shape
+    S = seq_lens.shape[0]
+    if _contig("query_start_loc", query_start_loc, torch.int32).numel() != S + 1:
+        raise ValueError(f"query_start_loc must be [{S + 1}]")
+    _masks(q, tq, S, slopes, key_starts, prefix_lens)
+    _same_device(q.device, key_cache=key_cache, value_cache=value_cache, query_start_loc=query_start_loc,
+                 seq_lens=seq_lens, block_tables=block_tables, slopes=slopes, key_starts=key_starts,
+                 prefix_lens=prefix_lens, out=out, workspace=workspace)
+    with torch.cuda.device(q.device):
+        if workspace is None:
+            workspace = new_workspace(prefill_masked_workspace_size(S, tq, hq, hkv, d, max_seq_len),
+                                      q.device)
+        _check(fn, getattr(load_library(), fn)(
+            _ptr(out), _ptr(q), _ptr(key_cache), _ptr(value_cache), _ptr(query_start_loc),
+            _ptr(seq_lens), S, tq, int(max_query_len), int(max_seq_len), _ptr(block_tables),
+            block_tables.shape[1], hq, hkv, d, bs, nb, float(scale), *scales, float(softcap),
+            _ptr(slopes), _ptr(key_starts), _ptr(prefix_lens), _ptr(workspace), workspace.numel(),
+            _stream()))
+    return out
+
+
+def prefill_varlen_masked(q, key_cache, value_cache, query_start_loc, seq_lens, block_tables,
+                          max_query_len, max_seq_len, scale, softcap=0.0, slopes=None, key_starts=None,
+                          prefix_lens=None, out=None, workspace=None):
+    """prefill_varlen with the modified scores of decode_masked: softcap, slopes
+    [Hq], key_starts [total_q] (one per query row) and prefix_lens [S], whose
+    keys every row of the request sees, also the rows before them."""
+    return _prefill_masked("pa_prefill_varlen_masked", torch.bfloat16, (), q, key_cache, value_cache,
+                           query_start_loc, seq_lens, block_tables, max_query_len, max_seq_len, scale,
+                           softcap, slopes, key_starts, prefix_lens, out, workspace)
+
+
+def prefill_varlen_masked_fp8(q, key_cache, value_cache, query_start_loc, seq_lens, block_tables,
+                              max_query_len, max_seq_len, scale, k_scale, v_scale, softcap=0.0,
+                              slopes=None, key_starts=None, prefix_lens=None, out=None, workspace=None):
+    """prefill_varlen_masked over e4m3 caches (uint8 [nb, bs, Hkv, d]) with their scales."""
+    return _prefill_masked("pa_prefill_varlen_masked_fp8", torch.uint8, (float(k_scale), float(v_scale)), q,
+                           key_cache, value_cache, query_start_loc, seq_lens, block_tables,
+                           max_query_len, max_seq_len, scale, softcap, slopes, key_starts, prefix_lens,
+                           out, workspace)
 
 
 def device_status(workspace_or_status):

@@ -332,6 +332,24 @@ PrefillLayout prefill_layout(size_t base, int num_seqs, int total_q, int num_hea
   return P;
 }
 
+// The plan of a masked prefill, after the tile kernel's part (PrefillPlan).
+// A request of q_len rows has ceil(q_len / 128) query tiles.
+struct PlanLayout {
+  int max_tiles = 0;
+  size_t head_offset = 0, first_offset = 0, cum_offset = 0, tiles_offset = 0, total = 0;
+};
+
+PlanLayout plan_layout(size_t base, int num_seqs, int total_q) {
+  PlanLayout P;
+  P.max_tiles = static_cast<int>(static_cast<int64_t>(total_q) / 128 + num_seqs);
+  P.head_offset = align_up(base, 256);
+  P.first_offset = align_up(P.head_offset + sizeof(PlanHead), 256);
+  P.cum_offset = align_up(P.first_offset + (static_cast<size_t>(num_seqs) + 1) * 4, 256);
+  P.tiles_offset = align_up(P.cum_offset + static_cast<size_t>(P.max_tiles) * 8, 256);
+  P.total = align_up(P.tiles_offset + static_cast<size_t>(P.max_tiles) * sizeof(PlanTile), 256);
+  return P;
+}
+
 // A distinct non-zero tag per decode launch (see the pair counters).
 unsigned next_epoch() {
   static std::atomic<unsigned> epoch{0};
@@ -511,7 +529,9 @@ pa_status decode_masked_impl(void* out, const void* q, const void* key_cache, co
   const DecodeLayout L =
       decode_layout(num_seqs, num_heads, units, head_dim, max_seq_len, partition_tokens, kv.pair);
   if (L.num_ctas > kMaxDecodeCtas) return PA_ERR_UNSUPPORTED;
-  if (!workspace || workspace_bytes < L.total) return PA_ERR_WORKSPACE;
+  if (!workspace || workspace_bytes < pa_decode_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim,
+                                                               max_seq_len, partition_tokens))
+    return PA_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return PA_ERR_INVALID;
   return launch_decode_rows(out, q, key_cache, value_cache, block_tables, max_blocks_per_seq, seq_lens,
                             nullptr, num_seqs, num_seqs, max_seq_len, num_heads, num_kv_heads, head_dim,
@@ -1004,6 +1024,13 @@ pa_status pa_decode_xsplit_fp8(void* out, const void* q, const void* key_cache,
                             static_cast<cudaStream_t>(stream), kv);
 }
 
+size_t pa_prefill_masked_workspace_size(int32_t num_seqs, int32_t total_q, int32_t num_heads,
+                                        int32_t num_kv_heads, int32_t head_dim, int32_t max_seq_len) {
+  const size_t base =
+      pa_prefill_workspace_size(num_seqs, total_q, num_heads, num_kv_heads, head_dim, max_seq_len);
+  return base == 0 ? 0 : plan_layout(base, num_seqs, total_q).total;
+}
+
 size_t pa_prefill_workspace_size(int32_t num_seqs, int32_t total_q, int32_t num_heads,
                                  int32_t num_kv_heads, int32_t head_dim, int32_t max_seq_len) {
   if (total_q < 0) return 0;
@@ -1025,7 +1052,7 @@ pa_status prefill_varlen_impl(void* out, const void* q, const void* key_cache,
                               int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
                               int32_t block_size, int32_t num_blocks, float scale,
                               void* workspace, size_t workspace_bytes, void* stream,
-                              const KvFormat& kv) {
+                              KvFormat kv, const ScoreMods* mods = nullptr) {
   pa_status st = check_decode_args(out, q, key_cache, value_cache, block_tables, max_blocks_per_seq,
                                    seq_lens, num_seqs, max_seq_len, num_heads, num_kv_heads,
                                    head_dim, block_size, num_blocks, scale);
@@ -1034,12 +1061,23 @@ pa_status prefill_varlen_impl(void* out, const void* q, const void* key_cache,
       max_query_len > max_seq_len)
     return PA_ERR_INVALID;
   if (num_seqs == 0 || total_q == 0) return PA_OK;
-  const DecodeLayout L = decode_layout(num_seqs, num_heads, num_kv_heads, head_dim, max_seq_len, 0);
+  // The decode rows' work units (masked: as in pa_decode_masked).
+  const int group = num_heads / num_kv_heads;
+  kv.pair = mods != nullptr && kv.e4m3 && decode_fp8_pairs(head_dim, num_heads, num_kv_heads);
+  const int units = mods == nullptr ? num_kv_heads
+                    : kv.pair       ? num_kv_heads / 2
+                                    : num_kv_heads * (group / xsplit_heads_per_unit(group));
+  if (units > 65535) return PA_ERR_UNSUPPORTED;
+  const DecodeLayout L = decode_layout(num_seqs, num_heads, units, head_dim, max_seq_len, 0, kv.pair);
   if (L.num_ctas > kMaxDecodeCtas) return PA_ERR_UNSUPPORTED;
   const PrefillLayout PL =
       prefill_layout(L.total, num_seqs, total_q, num_heads, num_kv_heads, head_dim);
-  if (!workspace || workspace_bytes < (max_query_len > 1 ? PL.total : L.total))
-    return PA_ERR_WORKSPACE;
+  const PlanLayout plan = plan_layout(PL.total, num_seqs, total_q);
+  const size_t need = mods != nullptr ? pa_prefill_masked_workspace_size(num_seqs, total_q, num_heads, num_kv_heads,
+                                                                         head_dim, max_seq_len)
+                      : max_query_len > 1 ? PL.total
+                                          : L.total;
+  if (!workspace || workspace_bytes < need) return PA_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return PA_ERR_INVALID;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if (max_query_len > 1) {
@@ -1085,32 +1123,83 @@ pa_status prefill_varlen_impl(void* out, const void* q, const void* key_cache,
     // exactly ctas-per-SM CTAs on every SM: the two kernels split the SMs between
     // them (tile_kernel_sms()), so that the decode rows start at once on the
     // SMs the tiles leave instead of after the tile CTAs.
-    const int group = num_heads / num_kv_heads;
     const bool split_sms =
-        head_dim == 128 && !decode_uses_tc(head_dim, group) &&
+        mods == nullptr && head_dim == 128 && !decode_uses_tc(head_dim, group) &&
         L.num_ctas == static_cast<int64_t>(PL.num_ctas) * decode_ctas_per_sm(head_dim, group);
     p.partition = split_sms ? 1 : 0;
     // Both kernels go on the caller's stream.  The tile kernel lets the
     // decode launch start once the kernels before this call are complete;
     // the decode CTAs then take the SMs the tiles leave free, and the decode
     // launch completes only after the tile kernel.
-    if (launch_prefill(p, qmap, kmap, vmap, head_dim, kv.e4m3, cs) != cudaSuccess)
-      return PA_ERR_CUDA;
+    if (mods != nullptr) {
+      p.mods = *mods;
+      p.plan.head = reinterpret_cast<PlanHead*>(ws + plan.head_offset);
+      p.plan.first = reinterpret_cast<int*>(ws + plan.first_offset);
+      p.plan.cum = reinterpret_cast<long long*>(ws + plan.cum_offset);
+      p.plan.tiles = reinterpret_cast<PlanTile*>(ws + plan.tiles_offset);
+      p.plan.max_tiles = plan.max_tiles;
+    }
+    const cudaError_t err = mods != nullptr
+                                ? launch_prefill_masked(p, qmap, kmap, vmap, head_dim, kv.e4m3, cs)
+                                : launch_prefill(p, qmap, kmap, vmap, head_dim, kv.e4m3, cs);
+    if (err != cudaSuccess) return PA_ERR_CUDA;
     return launch_decode_rows(out, q, key_cache, value_cache, block_tables, max_blocks_per_seq,
                               seq_lens, query_start_loc, num_seqs, total_q, max_seq_len,
                               num_heads, num_kv_heads, head_dim, num_blocks, block_size, scale, L,
-                              workspace, cs, kv, true, split_sms ? PL.num_ctas : 0, max_query_len);
+                              workspace, cs, kv, true, split_sms ? PL.num_ctas : 0, max_query_len, mods);
   }
   // Only decode rows: the decode kernel.
   return launch_decode_rows(out, q, key_cache, value_cache, block_tables, max_blocks_per_seq,
                             seq_lens, query_start_loc, num_seqs, total_q, max_seq_len, num_heads,
                             num_kv_heads, head_dim, num_blocks, block_size, scale, L, workspace, cs,
-                            kv);
+                            kv, false, 0, 0, mods);
 }
 
 }  // namespace
 
 extern "C" {
+
+pa_status pa_prefill_varlen_masked(void* out, const void* q, const void* key_cache,
+                                   const void* value_cache, const int32_t* query_start_loc,
+                                   const int32_t* seq_lens, int32_t num_seqs, int32_t total_q,
+                                   int32_t max_query_len, int32_t max_seq_len,
+                                   const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                   int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                                   int32_t block_size, int32_t num_blocks, float scale, float softcap,
+                                   const float* slopes, const int32_t* key_starts,
+                                   const int32_t* prefix_lens, void* workspace, size_t workspace_bytes,
+                                   void* stream) {
+  ScoreMods mods;
+  if (!make_mods(&mods, scale, 1.f, softcap, slopes, key_starts, prefix_lens)) return PA_ERR_INVALID;
+  return prefill_varlen_impl(out, q, key_cache, value_cache, query_start_loc, seq_lens, num_seqs,
+                             total_q, max_query_len, max_seq_len, block_tables, max_blocks_per_seq,
+                             num_heads, num_kv_heads, head_dim, block_size, num_blocks, scale,
+                             workspace, workspace_bytes, stream, KvFormat(), &mods);
+}
+
+pa_status pa_prefill_varlen_masked_fp8(void* out, const void* q, const void* key_cache,
+                                       const void* value_cache, const int32_t* query_start_loc,
+                                       const int32_t* seq_lens, int32_t num_seqs, int32_t total_q,
+                                       int32_t max_query_len, int32_t max_seq_len,
+                                       const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                       int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                                       int32_t block_size, int32_t num_blocks, float scale,
+                                       float k_scale, float v_scale, float softcap, const float* slopes,
+                                       const int32_t* key_starts, const int32_t* prefix_lens,
+                                       void* workspace, size_t workspace_bytes, void* stream) {
+  if (!(std::isfinite(k_scale) && k_scale > 0.f && std::isfinite(v_scale) && v_scale > 0.f))
+    return PA_ERR_INVALID;
+  KvFormat kv;
+  kv.e4m3 = true;
+  kv.k_scale = k_scale;
+  kv.v_scale = v_scale;
+  ScoreMods mods;
+  if (!make_mods(&mods, scale, k_scale, softcap, slopes, key_starts, prefix_lens)) return PA_ERR_INVALID;
+  return prefill_varlen_impl(out, q, key_cache, value_cache, query_start_loc, seq_lens, num_seqs,
+                             total_q, max_query_len, max_seq_len, block_tables, max_blocks_per_seq,
+                             num_heads, num_kv_heads, head_dim, block_size, num_blocks, scale,
+                             workspace, workspace_bytes, stream, kv, &mods);
+}
 
 pa_status pa_prefill_varlen(void* out, const void* q, const void* key_cache,
                             const void* value_cache, const int32_t* query_start_loc,

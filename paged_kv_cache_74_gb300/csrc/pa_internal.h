@@ -124,6 +124,26 @@ int decode_gmax(int group);
 // CTAs per SM the decode kernel for (head_dim, group) is built for.
 int decode_ctas_per_sm(int head_dim, int group);
 
+// The work of a masked prefill (prefill_masked.cu): one record per query tile
+// (128 rows of a request), request-major, the last tile of a request first.
+struct PlanTile {
+  int r, q0, row0, rows;
+  int ctx, kv_end, steps, prefix;   // prefix clipped to the request's keys
+  int lo, hi, n1, gap;              // [lo, hi): the union of the rows' causal runs
+};
+static_assert(sizeof(PlanTile) == 48, "read as three 16-byte words");
+struct PlanHead {
+  int tiles, pad;
+  long long steps;                  // 128-key steps of all tiles (one head pair)
+};
+struct PrefillPlan {
+  PlanHead* head = nullptr;
+  int* first = nullptr;             // [num_seqs + 1] first tile of each request
+  long long* cum = nullptr;         // [max_tiles] steps before each tile
+  PlanTile* tiles = nullptr;        // [max_tiles]
+  int max_tiles = 0;
+};
+
 // Chunked-prefill attention (prefill.cu).  Work unit: 128 query rows of one
 // request with q_len > 1 for two q heads of the same kv head (one head when
 // the group has no partner left), over all the keys those rows see, in
@@ -158,6 +178,8 @@ struct PrefillArgs {
   unsigned epoch;                   // distinct per call (never 0)
   float scale_log2;                 // softmax scale (* k_scale for e4m3) * log2(e)
   float o_scale;                    // 1, or v_scale for e4m3
+  ScoreMods mods;                   // masked calls only, as is the plan
+  PrefillPlan plan;
   // 1: the decode rows of the same call follow in the streaming decode
   // kernel, which takes the SMs this grid leaves (tile_kernel_sms()); only
   // that many CTAs work.  0: every CTA works.
@@ -167,6 +189,10 @@ struct PrefillArgs {
 size_t prefill_partials_bytes(int num_ctas, int head_dim);
 cudaError_t launch_prefill(const PrefillArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
                            const CUtensorMap& vmap, int head_dim, bool kv8, cudaStream_t stream);
+
+// The same with modified scores: the plan, then the tiles (prefill_masked.cu).
+cudaError_t launch_prefill_masked(const PrefillArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
+                                  const CUtensorMap& vmap, int head_dim, bool kv8, cudaStream_t stream);
 
 // Cache writes (cache_write.cu).
 cudaError_t launch_reshape_and_cache(const void* key, const void* value, int64_t key_stride,

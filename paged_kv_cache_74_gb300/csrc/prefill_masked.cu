@@ -1,0 +1,145 @@
+// prefill_masked.cu -- the chunked-prefill kernel with modified scores (tanh
+// cap, distance bias, prefix and first-key masks): the plan of its work, and
+// the launchers of the instantiations of prefill_kernel.cuh.
+//
+// A query tile (128 rows of a request) reads the 128-key steps that hold a key
+// some of its rows sees: those of [0, prefix) and of [lo, hi), where lo is the
+// least first key of its rows and hi its last position + 1.  lo comes from
+// the rows' key_starts, so the tiles' steps have no closed form: one CTA
+// computes them, a warp per tile, and scans them, and the tile kernel finds
+// its range of steps in the scan.  The tile kernel's CTAs start meanwhile and
+// wait for it.
+#include "prefill_kernel.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kPlanThreads = 1024;
+
+// Exclusive prefix sum over the CTA; *total: the sum.  `sums` holds 33 values.
+__device__ __forceinline__ long long block_scan(long long v, long long* sums, long long* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += u;
+  }
+  if (lane == 31) sums[warp] = incl;
+  __syncthreads();
+  if (warp == 0) {
+    const long long w = sums[lane];
+    long long wi = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, wi, o);
+      if (lane >= o) wi += u;
+    }
+    sums[lane] = wi - w;
+    if (lane == 31) sums[32] = wi;
+  }
+  __syncthreads();
+  const long long before = sums[warp] + incl - v;
+  *total = sums[32];
+  __syncthreads();  // sums may be written again
+  return before;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_prefill_kernel(const PrefillArgs a) {
+  __shared__ long long sums[33];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const PrefillPlan& pl = a.plan;
+  // First tile of each request.
+  long long tiles = 0;
+  for (int base = 0; base < a.num_seqs; base += kPlanThreads) {
+    const int r = base + tid;
+    long long total;
+    const long long before = block_scan(prefill_req(a, r).ntq, sums, &total);
+    if (r < a.num_seqs)
+      pl.first[r] = static_cast<int>(min(tiles + before, static_cast<long long>(pl.max_tiles)));
+    tiles += total;
+  }
+  // (requests that share rows, which no valid query_start_loc has, may count more)
+  if (tiles > pl.max_tiles) {
+    if (tid == 0) record_error(a.status, PA_DEV_BAD_QUERY_LEN, a.num_seqs - 1, a.total_q);
+    tiles = pl.max_tiles;
+  }
+  const int n = static_cast<int>(tiles);
+  __syncthreads();
+  for (int t = warp; t < n; t += kPlanThreads / 32) {
+    const int r = warp_search_last(a.num_seqs, lane, [&](int i) { return pl.first[i] <= t; });
+    const PReq p = prefill_req(a, r);
+    const int row0 = max(0, p.ntq - 1 - (t - pl.first[r])) * 128;
+    const int rows = min(128, p.q_len - row0);
+    int lo = 0x7fffffff;
+    for (int i = lane; i < rows; i += 32) {
+      const int start = a.mods.key_starts != nullptr ? max(0, __ldg(a.mods.key_starts + p.q0 + row0 + i)) : 0;
+      if (start <= p.ctx + row0 + i) lo = min(lo, start);
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    if (lane != 0) continue;
+    const int prefix =
+        a.mods.prefix_lens != nullptr ? min(max(__ldg(a.mods.prefix_lens + r), 0), p.seq_len) : 0;
+    const int hi = lo != 0x7fffffff ? p.ctx + row0 + rows : 0;
+    PlanTile w;
+    w.r = r;
+    w.q0 = p.q0;
+    w.row0 = row0;
+    w.rows = rows;
+    w.ctx = p.ctx;
+    w.kv_end = max(prefix, hi);
+    w.prefix = prefix;
+    w.lo = lo;
+    w.hi = hi;
+    // Steps [0, n1) hold the prefix; those of the run that are not among them
+    // follow after a gap.
+    w.n1 = (prefix + 127) / 128;
+    const int second = hi > 0 ? max(w.n1, lo / 128) : w.n1;
+    w.gap = second - w.n1;
+    w.steps = w.n1 + max(0, (hi + 127) / 128 - second);
+    if (w.steps == 0) {  // no row sees a key: one step without data writes the zeros
+      w.steps = 1;
+      w.gap = 0;
+    }
+    pl.tiles[t] = w;
+  }
+  __syncthreads();
+  long long steps = 0;
+  for (int base = 0; base < n; base += kPlanThreads) {
+    const int t = base + tid;
+    long long total;
+    const long long before = block_scan(t < n ? pl.tiles[t].steps : 0, sums, &total);
+    if (t < n) pl.cum[t] = steps + before;
+    steps += total;
+  }
+  if (tid == 0) {
+    pl.head->tiles = n;
+    pl.head->steps = steps;
+  }
+}
+
+template <int MOD>
+cudaError_t launch_tiles(const PrefillArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
+                         const CUtensorMap& vmap, int head_dim, bool kv8, cudaStream_t stream) {
+  if (head_dim == 128)
+    return kv8 ? launch_prefill_impl<128, true, MOD>(a, qmap, kmap, vmap, stream)
+               : launch_prefill_impl<128, false, MOD>(a, qmap, kmap, vmap, stream);
+  if (head_dim == 64)
+    return kv8 ? launch_prefill_impl<64, true, MOD>(a, qmap, kmap, vmap, stream)
+               : launch_prefill_impl<64, false, MOD>(a, qmap, kmap, vmap, stream);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t launch_prefill_masked(const PrefillArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
+                                  const CUtensorMap& vmap, int head_dim, bool kv8, cudaStream_t stream) {
+  const cudaError_t err = launch_overlapped(plan_prefill_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a);
+  if (err != cudaSuccess) return err;
+  return a.mods.cap_log2 > 0.f ? launch_tiles<kModsCap>(a, qmap, kmap, vmap, head_dim, kv8, stream)
+                               : launch_tiles<kMods>(a, qmap, kmap, vmap, head_dim, kv8, stream);
+}
+
+}  // namespace pa

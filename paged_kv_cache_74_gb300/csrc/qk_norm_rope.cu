@@ -23,6 +23,7 @@
 
 #include "pa_internal.h"
 #include "pa_ptx.cuh"
+#include "warp_search.cuh"
 
 namespace pa {
 namespace {
@@ -62,21 +63,10 @@ __device__ __forceinline__ void load_floats8(const float* src, float* dst) {
 
 // The request that owns flattened token t: the largest r with
 // query_start_loc[r] <= t, if t also lies before query_start_loc[r + 1]; -1 for
-// a token of no request.  A 32-way search by the whole warp (one round up to
-// 32 requests, two up to 1024).
+// a token of no request.
 __device__ __forceinline__ int request_of_token(const int32_t* qsl, int num_seqs, int t, int lane,
                                                 int* q0, int* q1) {
-  int lo = 0, n = num_seqs;  // the answer lies in [lo, lo + n)
-  while (n > 1) {
-    const int stride = (n + 31) / 32;
-    const int i = lo + lane * stride;
-    // lane 0 stands for `lo`, which the last round (or the end check) decides
-    const bool below = lane == 0 || (lane * stride < n && __ldg(qsl + i) <= t);
-    // the probes that hold form a prefix when query_start_loc ascends
-    const int last = __popc(__ballot_sync(0xffffffffu, below)) - 1;
-    n = min(stride, n - last * stride);
-    lo += last * stride;
-  }
+  const int lo = warp_search_last(num_seqs, lane, [&](int i) { return __ldg(qsl + i) <= t; });
   *q0 = __ldg(qsl + lo);
   *q1 = __ldg(qsl + lo + 1);
   return *q0 <= t && t < *q1 ? lo : -1;
