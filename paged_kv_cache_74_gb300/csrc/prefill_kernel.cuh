@@ -75,11 +75,6 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-__device__ __forceinline__ float fmin3(float a, float b, float c) {
-  float r;
-  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
 
 // Two floats rounded to bf16 (nearest even), packed low / high.
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
@@ -515,6 +510,171 @@ __device__ __noinline__ bool merge_staged(const float* __restrict__ part_ml,
       (void)mbar_wait(bar_full + 8 * (t % C::MDATA), (t / C::MDATA) & 1);
   }
   return ok;
+}
+
+// ---- the softmax of a step with modified scores
+//
+// Largest cap (log2 units) for which the weights 2^y, |y| <= cap, need no
+// running maximum: sums over 2^31 keys stay below 2^111, and O keeps 2^16 for
+// the values.
+constexpr float kFixedCap = 80.f;
+
+// What one query row sees and how its scores are modified.
+struct RowMask {
+  int pos;      // the row's position
+  int limit;    // its last causal key (rows past the unit's: within the loaded keys)
+  int start;    // first key of its causal run, at most pos + 1
+  int prefix;
+  float slope;  // distance slope * log2(e)
+  bool biased;
+  bool fixed;   // weights 2^y without a reference
+};
+
+// A pair of values in registers.
+__device__ __forceinline__ float2 pair_of(uint32_t a, uint32_t b) {
+  return make_float2(__uint_as_float(a), __uint_as_float(b));
+}
+
+// Holds the registers of an asynchronous TMEM load until its wait.
+__device__ __forceinline__ void pin32(uint32_t (&r)[32]) {
+#pragma unroll
+  for (int e = 0; e < 32; e += 8)
+    asm volatile("" : "+r"(r[e]), "+r"(r[e + 1]), "+r"(r[e + 2]), "+r"(r[e + 3]), "+r"(r[e + 4]),
+                      "+r"(r[e + 5]), "+r"(r[e + 6]), "+r"(r[e + 7]));
+}
+
+// One row's 128 scores of a step, in TMEM at tm_s: m_ref and l_run follow them
+// (lazily, as in the plain step: alpha and rescale say whether O must), and
+// the weights 2^(y - m_ref) replace them, 16 bits each.  The row is walked in
+// four chunks of 32 columns, the next one's load in flight during this one's
+// arithmetic; chunk c's weights go over columns 16 c .., which have been read.
+//
+// Bound by the instructions of the two softmax warps per scheduler: per score
+// about 3.5 issue slots of packed fp32 for the cap's polynomial and 3 for the
+// weight, its rounding and its sum; the exponential alone would need 1 of the
+// 16 special-function lanes' clocks in 16.
+template <int MOD, bool KV8, bool FIXED>
+__device__ __forceinline__ void masked_step(uint32_t tm_s, int key0, const RowMask& rm, const ScoreMods& mods,
+                                            float sl2, float& m_ref, float& l_run, float& alpha,
+                                            bool& rescale) {
+  // The row sees the step's columns [0, np) and [s0, s0 + ns).
+  const int np = rm.prefix - key0;
+  const int nv = rm.limit - key0 + 1;
+  const int s0 = rm.start - key0;
+  const unsigned ns = static_cast<unsigned>(max(0, rm.limit + 1 - rm.start));
+  const bool masked =
+      !__all_sync(0xffffffffu, np >= 128 || (nv >= 128 && (s0 <= 0 || rm.start <= rm.prefix)));
+  // Some visible key lies behind the row's position (the bias is by distance).
+  const bool behind = rm.biased && __any_sync(0xffffffffu, min(np, 128) > max(nv, 0));
+  auto mask = [&](uint32_t (&r)[32], int c) {
+    if (masked) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) {
+        const int col = 32 * c + e;
+        r[e] = col < np || static_cast<unsigned>(col - s0) < ns ? r[e] : 0xff800000u;  // -inf
+      }
+    }
+  };
+  // The scores of chunk c in log2 units, not yet masked.
+  auto scores = [&](uint32_t (&r)[32], int c) {
+    if constexpr (MOD == kModsCap) {
+      float top = 0.f;
+#pragma unroll
+      for (int e = 0; e < 32; e += 2)
+        top = fmax3(top, fabsf(__uint_as_float(r[e])), fabsf(__uint_as_float(r[e + 1])));
+      if (__any_sync(0xffffffffu, top * mods.cap_in > kCapNear)) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(capped_score(__uint_as_float(r[e]), mods));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          const float2 y = capped_near(pair_of(r[e], r[e + 1]), mods);
+          r[e] = __float_as_uint(y.x);
+          r[e + 1] = __float_as_uint(y.y);
+        }
+      }
+    }
+    if (rm.biased) {
+      const float s = MOD == kModsCap ? 1.f : sl2;
+      const float d0 = static_cast<float>(key0 + 32 * c - rm.pos);
+      if (behind) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          r[e] = __float_as_uint(
+              fmaf(__uint_as_float(r[e]), s, -rm.slope * fabsf(d0 + static_cast<float>(e))));
+      } else {
+        const float b0 = rm.slope * d0;
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          const float2 bias = __ffma2_rn(make_float2(rm.slope, rm.slope),
+                                         make_float2(static_cast<float>(e), static_cast<float>(e + 1)),
+                                         make_float2(b0, b0));
+          const float2 y = __ffma2_rn(pair_of(r[e], r[e + 1]), make_float2(s, s), bias);
+          r[e] = __float_as_uint(y.x);
+          r[e + 1] = __float_as_uint(y.y);
+        }
+      }
+    }
+  };
+  // Calls f(r, c) on the chunks in order, each loaded during the one before.
+  auto walk = [&](auto&& f) {
+    uint32_t ra[32], rb[32];
+    tmem_ld32_async(tm_s, ra);
+#pragma unroll 1
+    for (int c = 0; c < 4; c += 2) {
+      tmem_wait_ld();
+      pin32(ra);
+      tmem_ld32_async(tm_s + 32 * (c + 1), rb);
+      f(ra, c);
+      tmem_wait_ld();
+      pin32(rb);
+      if (c == 0) tmem_ld32_async(tm_s + 64, ra);
+      f(rb, c + 1);
+    }
+  };
+  if constexpr (!FIXED) {
+    // Pass 1: the row maximum (of the raw scores where the modification
+    // ascends); the reference moves before any weight.
+    float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    walk([&](uint32_t (&r)[32], int c) {
+      if (rm.biased) scores(r, c);
+      mask(r, c);
+#pragma unroll
+      for (int e = 0; e < 32; e += 2)
+        mx4[(e / 2) % 4] = fmax3(mx4[(e / 2) % 4], __uint_as_float(r[e]), __uint_as_float(r[e + 1]));
+    });
+    float m_tile = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+    if (!rm.biased && m_tile != -INFINITY)
+      m_tile = MOD == kModsCap ? capped_score(m_tile, mods) : m_tile * sl2;
+    const bool moved = m_tile > m_ref + kRescaleSlackP;
+    if (moved) {
+      alpha = fast_exp2(m_ref - m_tile);
+      l_run *= alpha;
+      m_ref = m_tile;
+    }
+    rescale = __any_sync(0xffffffffu, moved);
+  }
+  // Pass 2: the weights.
+  const float mul = MOD == kModsCap || rm.biased ? 1.f : sl2;
+  const float m = m_ref;
+  float2 sum[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+  walk([&](uint32_t (&r)[32], int c) {
+    if (MOD == kModsCap || rm.biased) scores(r, c);
+    mask(r, c);
+    uint32_t pk[16];
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+      float2 x = pair_of(r[e], r[e + 1]);
+      if constexpr (!FIXED) x = __ffma2_rn(x, make_float2(mul, mul), make_float2(-m, -m));
+      const float p0 = fast_exp2(x.x);  // 0 for the masked keys
+      const float p1 = fast_exp2(x.y);
+      pk[e / 2] = KV8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+      sum[(e / 2) % 4] = __fadd2_rn(sum[(e / 2) % 4], make_float2(p0, p1));
+    }
+    tmem_st16_async(tm_s + 16 * c, pk);
+  });
+  const float2 ps = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
+  l_run += ps.x + ps.y;  // (in the plain step's order)
 }
 
 // KV8: e4m3 K/V cache (k_scale folded into scale_log2, v_scale = o_scale):
@@ -1123,157 +1283,99 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
       }
       if (active) {
         const int limit = min(sg.ctx + sg.row0 + i_row, sg.kv_end - 1);  // last key this row sees
-        const int pos_row = sg.ctx + sg.row0 + i_row;
-        // MOD: the row's first key of its causal run, its slope (log2 units).
         PVis vis{};
-        int start = 0;
-        float slope = 0.f;
+        RowMask rm{};
         if constexpr (MOD != kNoMods) {
           vis = viss[slot];
+          rm.pos = sg.ctx + sg.row0 + i_row;
+          rm.limit = limit;
+          rm.prefix = vis.prefix;
+          rm.start = 0;
           if (a.mods.key_starts != nullptr && i_row < sg.rows)
-            start = min(max(0, __ldg(a.mods.key_starts + sg.q0 + sg.row0 + i_row)), pos_row + 1);
-          if (a.mods.slopes != nullptr) slope = -kLog2e * __ldg(a.mods.slopes + head);
+            rm.start = min(max(0, __ldg(a.mods.key_starts + sg.q0 + sg.row0 + i_row)), rm.pos + 1);
+          rm.biased = a.mods.slopes != nullptr;
+          if (rm.biased) rm.slope = kLog2e * __ldg(a.mods.slopes + head);
+          // Capped scores lie within +-cap log2(e): with bf16 weights (fp32's
+          // range) 0 will do as the reference, and no maximum is needed.
+          rm.fixed = MOD == kModsCap && !KV8 && !rm.biased && a.mods.cap_log2 <= kFixedCap;
+          if (rm.fixed) m_ref = 0.f;
         }
-        const bool biased = MOD != kNoMods && a.mods.slopes != nullptr;
         for (int k = 0; k < n && ok; ++k) {
           const int key0 = (MOD ? vis.tile(sg.j0 + k) : sg.j0 + k) * C::BN;
           if (!(ok = all_wait(B::SFULL + b, sc++ & 1, 82))) break;
           tc_fence_after();
-          const int nv = limit - key0 + 1;  // visible keys of this row in this step
-          // MOD: the row sees the step's columns [0, np) and [s0, s0 + ns).
-          const int np = vis.prefix - key0;
-          const int s0 = start - key0;
-          const unsigned ns = static_cast<unsigned>(max(0, limit + 1 - start));
-          const bool masked =
-              MOD ? !__all_sync(0xffffffffu, np >= C::BN || (nv >= C::BN && (s0 <= 0 || start <= vis.prefix)))
-                  : key0 + C::BN - 1 > sg.ctx + sg.row0 || key0 + C::BN > sg.kv_end;
-          auto visible = [&](int e) -> bool {
-            return MOD ? e < np || static_cast<unsigned>(e - s0) < ns : e < nv;
-          };
-          // S_b row, half a row (64 columns) at a time; keys past this row's
-          // limit get -inf (their weight 2^-inf = 0); only a step on the
-          // diagonal or at the end of the keys has any.
-          auto load_half = [&](int hf, uint32_t (&sr)[C::BN / 2]) {
-            tmem_ld32_async(tm_s + hf * 64, sr);
-            tmem_ld32_async(tm_s + hf * 64 + 32, sr + 32);
-            tmem_wait_ld();
-          };
-          auto mask_half = [&](int hf, uint32_t (&sr)[C::BN / 2]) {
-            if (masked) {
-#pragma unroll
-              for (int e = 0; e < C::BN / 2; ++e) sr[e] = visible(hf * 64 + e) ? sr[e] : 0xff800000u;  // -inf
-            }
-          };
-          // What pass 2 multiplies S by: MOD leaves log2 units there when the
-          // scores were biased (pass 1) or capped (pass 2).
-          const float mul = MOD == kModsCap || biased ? 1.f : sl2;
-          float2 ps4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
-                           make_float2(0.f, 0.f)};
-          uint32_t pk[C::BN / 4];
-          // Weights of one pair of columns: scale and shift (packed fp32),
-          // exponentiate, round to 16 bits for the P.V product; l sums the
-          // fp32 weights.
-          auto weights = [&](uint32_t s0, uint32_t s1, float m, int e) {
-            const float2 x = __ffma2_rn(make_float2(__uint_as_float(s0), __uint_as_float(s1)),
-                                        make_float2(mul, mul), make_float2(-m, -m));
-            const float p0 = fast_exp2(x.x);  // 0 for the masked keys
-            const float p1 = fast_exp2(x.y);
-            pk[e / 2] = KV8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
-            ps4[(e / 2) % 4] = __fadd2_rn(ps4[(e / 2) % 4], make_float2(p0, p1));
-          };
-          // Pass 1: the row maximum; the reference moves (lazily: only when
-          // the maximum exceeds it by more than 2^8) before any weight.
-          float mx8[8];
-#pragma unroll
-          for (int u = 0; u < 8; ++u) mx8[u] = -INFINITY;
-          float mn4[4] = {INFINITY, INFINITY, INFINITY, INFINITY};  // kModsCap: the row minimum
-          auto masked_high = [](uint32_t x) -> float {  // a masked score (-inf) as +inf
-            return x == 0xff800000u ? INFINITY : __uint_as_float(x);
-          };
-          // 64 scores capped, in log2 units; `far`: some may lie beyond the polynomial.
-          auto cap_half = [&](uint32_t (&sr)[C::BN / 2], bool any_far) {
-            if (any_far) {
-#pragma unroll
-              for (int e = 0; e < C::BN / 2; ++e)
-                sr[e] = __float_as_uint(capped_score(__uint_as_float(sr[e]), a.mods));
-            } else {
-#pragma unroll
-              for (int e = 0; e < C::BN / 2; e += 2) {
-                const float2 y = capped_near(make_float2(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])), a.mods);
-                sr[e] = __float_as_uint(y.x);
-                sr[e + 1] = __float_as_uint(y.y);
-              }
-            }
-          };
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            uint32_t sr[C::BN / 2];
-            load_half(hf, sr);
-            if (MOD != kNoMods && biased) {
-              // Capped, biased and masked in log2 units, back over S for pass 2.
-              if constexpr (MOD == kModsCap) cap_half(sr, true);
-              const float d0 = static_cast<float>(key0 + hf * 64 - pos_row);
-              const float s = MOD == kModsCap ? 1.f : sl2;
-#pragma unroll
-              for (int e = 0; e < C::BN / 2; ++e)
-                sr[e] = __float_as_uint(
-                    fmaf(__uint_as_float(sr[e]), s, slope * fabsf(d0 + static_cast<float>(e))));
-              mask_half(hf, sr);
-              tmem_st32_async(tm_s + hf * 64, sr);
-              tmem_st32_async(tm_s + hf * 64 + 32, sr + 32);
-            } else {
-              mask_half(hf, sr);
-              if constexpr (MOD == kModsCap) {
-#pragma unroll
-                for (int e = 0; e < C::BN / 2; e += 2)
-                  mn4[(e / 2) % 4] = fmin3(mn4[(e / 2) % 4], masked_high(sr[e]), masked_high(sr[e + 1]));
-              }
-            }
-#pragma unroll
-            for (int e = 0; e < C::BN / 2; e += 2)
-              mx8[(e / 2) % 8] = fmax3(mx8[(e / 2) % 8], __uint_as_float(sr[e]), __uint_as_float(sr[e + 1]));
-          }
-          const float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
-                                 fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
-          float m_tile = biased ? mx : mx * sl2;
-          bool far = false;  // some score lies beyond the polynomial of cap_half
-          if constexpr (MOD == kModsCap) {
-            if (biased) {
-              tmem_wait_st();
-            } else {
-              // tanh ascends: the capped maximum is the maximum's cap.
-              m_tile = mx == -INFINITY ? mx : capped_score(mx, a.mods);
-              const float mn = fminf(fminf(mn4[0], mn4[1]), fminf(mn4[2], mn4[3]));
-              far = __any_sync(0xffffffffu, fmaxf(mx, -mn) * a.mods.cap_in > kCapNear);
-            }
-          } else if (MOD != kNoMods && biased) {
-            tmem_wait_st();
-          }
-          const bool moved = m_tile > m_ref + kRescaleSlackP;
           float alpha = 1.f;
-          if (moved) {
-            alpha = fast_exp2(m_ref - m_tile);
-            l_run *= alpha;
-            m_ref = m_tile;
-          }
-          const bool rescale = __any_sync(0xffffffffu, moved);
-          // Pass 2: the weights; P_b of each half goes over S_b columns that
-          // have already been read (P_b: the first half of the S_b columns).
+          bool rescale = false;
+          if constexpr (MOD != kNoMods) {
+            if (MOD == kModsCap && !KV8 && rm.fixed)
+              masked_step<MOD, KV8, true>(tm_s, key0, rm, a.mods, sl2, m_ref, l_run, alpha, rescale);
+            else
+              masked_step<MOD, KV8, false>(tm_s, key0, rm, a.mods, sl2, m_ref, l_run, alpha, rescale);
+          } else {
+            const bool masked = key0 + C::BN - 1 > sg.ctx + sg.row0 || key0 + C::BN > sg.kv_end;
+            const int nv = limit - key0 + 1;  // visible keys of this row in this step
+            // S_b row, half a row (64 columns) at a time; keys past this row's
+            // limit get -inf (their weight 2^-inf = 0); only a step on the
+            // diagonal or at the end of the keys has any.
+            auto load_half = [&](int hf, uint32_t (&sr)[C::BN / 2]) {
+              tmem_ld32_async(tm_s + hf * 64, sr);
+              tmem_ld32_async(tm_s + hf * 64 + 32, sr + 32);
+              tmem_wait_ld();
+              if (masked) {
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            uint32_t sr[C::BN / 2];
-            load_half(hf, sr);
-            if (!biased) {
-              if constexpr (MOD == kModsCap) cap_half(sr, far);
-              mask_half(hf, sr);
+                for (int e = 0; e < C::BN / 2; ++e) sr[e] = hf * 64 + e < nv ? sr[e] : 0xff800000u;  // -inf
+              }
+            };
+            float2 ps4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                             make_float2(0.f, 0.f)};
+            uint32_t pk[C::BN / 4];
+            // Weights of one pair of columns: scale and shift (packed fp32),
+            // exponentiate, round to 16 bits for the P.V product; l sums the
+            // fp32 weights.
+            auto weights = [&](uint32_t s0, uint32_t s1, float m, int e) {
+              const float2 x = __ffma2_rn(make_float2(__uint_as_float(s0), __uint_as_float(s1)),
+                                          make_float2(sl2, sl2), make_float2(-m, -m));
+              const float p0 = fast_exp2(x.x);  // 0 for the masked keys
+              const float p1 = fast_exp2(x.y);
+              pk[e / 2] = KV8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+              ps4[(e / 2) % 4] = __fadd2_rn(ps4[(e / 2) % 4], make_float2(p0, p1));
+            };
+            // Pass 1: the row maximum; the reference moves (lazily: only when
+            // the maximum exceeds it by more than 2^8) before any weight.
+            float mx8[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) mx8[u] = -INFINITY;
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              uint32_t sr[C::BN / 2];
+              load_half(hf, sr);
+#pragma unroll
+              for (int e = 0; e < C::BN / 2; e += 2)
+                mx8[(e / 2) % 8] = fmax3(mx8[(e / 2) % 8], __uint_as_float(sr[e]), __uint_as_float(sr[e + 1]));
             }
+            const float m_tile = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
+                                       fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]))) * sl2;
+            const bool moved = m_tile > m_ref + kRescaleSlackP;
+            if (moved) {
+              alpha = fast_exp2(m_ref - m_tile);
+              l_run *= alpha;
+              m_ref = m_tile;
+            }
+            rescale = __any_sync(0xffffffffu, moved);
+            // Pass 2: the weights; P_b of each half goes over S_b columns that
+            // have already been read (P_b: the first half of the S_b columns).
 #pragma unroll
-            for (int e = 0; e < C::BN / 2; e += 2) weights(sr[e], sr[e + 1], m_ref, e);
-            tmem_st16_async(tm_s + hf * 32, pk);
-            tmem_st16_async(tm_s + hf * 32 + 16, pk + 16);
+            for (int hf = 0; hf < 2; ++hf) {
+              uint32_t sr[C::BN / 2];
+              load_half(hf, sr);
+#pragma unroll
+              for (int e = 0; e < C::BN / 2; e += 2) weights(sr[e], sr[e + 1], m_ref, e);
+              tmem_st16_async(tm_s + hf * 32, pk);
+              tmem_st16_async(tm_s + hf * 32 + 16, pk + 16);
+            }
+            const float2 ps = __fadd2_rn(__fadd2_rn(ps4[0], ps4[1]), __fadd2_rn(ps4[2], ps4[3]));
+            l_run += ps.x + ps.y;
           }
-          const float2 ps = __fadd2_rn(__fadd2_rn(ps4[0], ps4[1]), __fadd2_rn(ps4[2], ps4[3]));
-          l_run += ps.x + ps.y;
           if (rescale && k > 0) {  // (warp-uniform: the TMEM accesses are warp-wide)
             // S_b of this step completing means the P_b V before it has
             // completed too: O_b is current and may be rescaled.

@@ -15,43 +15,39 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// cap log2(e) tanh(t), t = x cap_in: the odd Taylor polynomial below
-// |t| = 0.3 (first term left out: 0.0089 t^10 relative, 6e-8), where 1 - 2 / (1 +
-// e^2t) would lose the leading digits of a small score; that quotient above
-// (2e-7 absolute, 7e-7 relative at 0.3).  The hardware's tanh
-// approximation is off by 2^-11 of the score: a capped score of 30 would
-// shift its weight by 1.5 %.
+// tanh(t) / t for |t| <= kCapNear as a polynomial in t^2, minimax in the relative
+// error (6e-7).  Up to there 1 - 2 / (1 + e^2t) would lose leading digits, and
+// two special-function operations cost more than five fused multiply-adds.
+constexpr float kCapNear = 0.75f;
+constexpr float kTanhQ0 = 0.99999946f, kTanhQ1 = -0.33328253f, kTanhQ2 = 0.13258983f,
+                kTanhQ3 = -0.050056305f, kTanhQ4 = 0.012929632f;
+
+// cap log2(e) tanh(t), t = x cap_in, for any x: the polynomial near 0, the
+// quotient beyond (2e-7 absolute).  The hardware's tanh approximation is off by
+// 2^-11 of the score: a capped score of 30 would shift its weight by 1.5 %.
 __device__ __forceinline__ float capped_score(float x, const ScoreMods& m) {
   const float t = x * m.cap_in;
   const float t2 = t * t;
-  float q = fmaf(t2, 62.f / 2835.f, -17.f / 315.f);
-  q = fmaf(t2, q, 2.f / 15.f);
-  q = fmaf(t2, q, -1.f / 3.f);
-  const float small = fmaf(t * t2, q, t);
+  float q = fmaf(t2, kTanhQ4, kTanhQ3);
+  q = fmaf(t2, q, kTanhQ2);
+  q = fmaf(t2, q, kTanhQ1);
+  q = fmaf(t2, q, kTanhQ0);
   const float e = fast_exp2(t * (2.f * kLog2e));  // 0 and infinity at the ends are fine
-  const float big = fmaf(-2.f, fast_rcp(1.f + e), 1.f);
-  return m.cap_log2 * (t2 < 0.09f ? small : big);
+  const float far = fmaf(-2.f, fast_rcp(1.f + e), 1.f);
+  return m.cap_log2 * (t2 < kCapNear * kCapNear ? t * q : far);
 }
 
-// The same for a pair of scores with |t| <= kCapNear, on the fused multiply-add
-// pipe alone: cap log2(e) t Q(t^2), Q the minimax polynomial of tanh(t) / t in
-// t^2 for |t| <= 1 (5e-8 relative, 2e-7 with fp32 evaluation).
-constexpr float kCapNear = 1.0f;
-constexpr float kTanhQ0 = 0.99999994f, kTanhQ1 = -0.3333284f, kTanhQ2 = 0.13325204f,
-                kTanhQ3 = -0.05345703f, kTanhQ4 = 0.020289982f, kTanhQ5 = -0.0062033795f,
-                kTanhQ6 = 0.0010410226f;
-
+// The same for a pair of scores with |t| <= kCapNear, by packed fused
+// multiply-adds (cap_log2 folded into the coefficients).
 __device__ __forceinline__ float2 capped_near(float2 x, const ScoreMods& m) {
   auto both = [](float c) { return make_float2(c, c); };
   const float2 t = __fmul2_rn(x, both(m.cap_in));
   const float2 t2 = __fmul2_rn(t, t);
-  float2 q = __ffma2_rn(t2, both(kTanhQ6), both(kTanhQ5));
-  q = __ffma2_rn(t2, q, both(kTanhQ4));
-  q = __ffma2_rn(t2, q, both(kTanhQ3));
-  q = __ffma2_rn(t2, q, both(kTanhQ2));
-  q = __ffma2_rn(t2, q, both(kTanhQ1));
-  q = __ffma2_rn(t2, q, both(kTanhQ0));
-  return __fmul2_rn(__fmul2_rn(t, both(m.cap_log2)), q);
+  float2 q = __ffma2_rn(t2, both(kTanhQ4 * m.cap_log2), both(kTanhQ3 * m.cap_log2));
+  q = __ffma2_rn(t2, q, both(kTanhQ2 * m.cap_log2));
+  q = __ffma2_rn(t2, q, both(kTanhQ1 * m.cap_log2));
+  q = __ffma2_rn(t2, q, both(kTanhQ0 * m.cap_log2));
+  return __fmul2_rn(t, q);
 }
 
 // The 16-token tiles of a request that hold a key its (single) row sees:
