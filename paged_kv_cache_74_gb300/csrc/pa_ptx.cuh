@@ -447,6 +447,13 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
+// max(a, b, c) in one instruction.
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // Hardware reciprocal (PTX rcp.approx, 1 ulp); 1 / infinity = 0.
 __device__ __forceinline__ float fast_rcp(float x) {
   float y;

@@ -69,13 +69,6 @@ constexpr int kSegEnd = 3;              // no more work
 // publishes its own instead of merging them.
 constexpr unsigned long long kMergeWaitNs = 20000;
 
-// max(a, b, c) in one instruction.
-__device__ __forceinline__ float fmax3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
 // Two floats rounded to bf16 (nearest even), packed low / high.
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
@@ -519,6 +512,9 @@ __device__ __noinline__ bool merge_staged(const float* __restrict__ part_ml,
 // the values.
 constexpr float kFixedCap = 80.f;
 
+// Columns of a row's scores handled at once.
+constexpr int kChunkCols = 64;
+
 // What one query row sees and how its scores are modified.
 struct RowMask {
   int pos;      // the row's position
@@ -536,116 +532,115 @@ __device__ __forceinline__ float2 pair_of(uint32_t a, uint32_t b) {
 }
 
 // Holds the registers of an asynchronous TMEM load until its wait.
-__device__ __forceinline__ void pin32(uint32_t (&r)[32]) {
+template <int N>
+__device__ __forceinline__ void pin(uint32_t (&r)[N]) {
 #pragma unroll
-  for (int e = 0; e < 32; e += 8)
+  for (int e = 0; e < N; e += 8)
     asm volatile("" : "+r"(r[e]), "+r"(r[e + 1]), "+r"(r[e + 2]), "+r"(r[e + 3]), "+r"(r[e + 4]),
                       "+r"(r[e + 5]), "+r"(r[e + 6]), "+r"(r[e + 7]));
 }
 
 // One row's 128 scores of a step, in TMEM at tm_s: m_ref and l_run follow them
 // (lazily, as in the plain step: alpha and rescale say whether O must), and
-// the weights 2^(y - m_ref) replace them, 16 bits each.  The row is walked in
-// four chunks of 32 columns, the next one's load in flight during this one's
-// arithmetic; chunk c's weights go over columns 16 c .., which have been read.
+// the weights 2^(y - m_ref) replace them, 16 bits each.  FIXED: capped scores
+// that need no maximum (kFixedCap), in one pass.  The weights of chunk c go
+// over columns W / 2 c .., which have been read.
 //
-// Bound by the instructions of the two softmax warps per scheduler: per score
-// about 3.5 issue slots of packed fp32 for the cap's polynomial and 3 for the
-// weight, its rounding and its sum; the exponential alone would need 1 of the
-// 16 special-function lanes' clocks in 16.
+// Bound by the two softmax warps of each scheduler, whose instructions issue
+// every 5 cycles or so: the loops are rolled (unrolled over the row they took
+// 330 against 255 us on four long chunks with a window, the instructions
+// coming too late; a load ahead of its chunk in a second set of registers cost
+// more than it hid), and with a cap the polynomial runs next to the
+// exponentials.
 template <int MOD, bool KV8, bool FIXED>
 __device__ __forceinline__ void masked_step(uint32_t tm_s, int key0, const RowMask& rm, const ScoreMods& mods,
                                             float sl2, float& m_ref, float& l_run, float& alpha,
                                             bool& rescale) {
-  // The row sees the step's columns [0, np) and [s0, s0 + ns).
+  constexpr int W = kChunkCols;
+  // The row sees the step's columns [0, np) and [s0, e0).
   const int np = rm.prefix - key0;
-  const int nv = rm.limit - key0 + 1;
   const int s0 = rm.start - key0;
-  const unsigned ns = static_cast<unsigned>(max(0, rm.limit + 1 - rm.start));
+  const int e0 = rm.limit + 1 - key0;
   const bool masked =
-      !__all_sync(0xffffffffu, np >= 128 || (nv >= 128 && (s0 <= 0 || rm.start <= rm.prefix)));
+      !__all_sync(0xffffffffu, np >= 128 || (e0 >= 128 && (s0 <= 0 || rm.start <= rm.prefix)));
   // Some visible key lies behind the row's position (the bias is by distance).
-  const bool behind = rm.biased && __any_sync(0xffffffffu, min(np, 128) > max(nv, 0));
-  auto mask = [&](uint32_t (&r)[32], int c) {
+  const bool behind = rm.biased && __any_sync(0xffffffffu, min(np, 128) > max(e0, 0));
+  auto mask = [&](uint32_t (&r)[W], int c) {
     if (masked) {
+      auto low = [](int n) -> uint32_t { return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u); };
 #pragma unroll
-      for (int e = 0; e < 32; ++e) {
-        const int col = 32 * c + e;
-        r[e] = col < np || static_cast<unsigned>(col - s0) < ns ? r[e] : 0xff800000u;  // -inf
+      for (int w = 0; w < W; w += 32) {
+        const int col = W * c + w;
+        const uint32_t seen = low(np - col) | (low(e0 - col) & ~low(s0 - col));
+#pragma unroll
+        for (int e = 0; e < 32; ++e) r[w + e] = seen >> e & 1u ? r[w + e] : 0xff800000u;  // -inf
       }
     }
   };
-  // The scores of chunk c in log2 units, not yet masked.
-  auto scores = [&](uint32_t (&r)[32], int c) {
-    if constexpr (MOD == kModsCap) {
-      float top = 0.f;
+  // The scores capped, in log2 units.
+  auto cap = [&](uint32_t (&r)[W]) {
+    if (any_far<W>(r, mods)) {
 #pragma unroll
-      for (int e = 0; e < 32; e += 2)
-        top = fmax3(top, fabsf(__uint_as_float(r[e])), fabsf(__uint_as_float(r[e + 1])));
-      if (__any_sync(0xffffffffu, top * mods.cap_in > kCapNear)) {
+      for (int e = 0; e < W; ++e) r[e] = __float_as_uint(capped_score(__uint_as_float(r[e]), mods));
+    } else {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(capped_score(__uint_as_float(r[e]), mods));
-      } else {
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          const float2 y = capped_near(pair_of(r[e], r[e + 1]), mods);
-          r[e] = __float_as_uint(y.x);
-          r[e + 1] = __float_as_uint(y.y);
-        }
-      }
-    }
-    if (rm.biased) {
-      const float s = MOD == kModsCap ? 1.f : sl2;
-      const float d0 = static_cast<float>(key0 + 32 * c - rm.pos);
-      if (behind) {
-#pragma unroll
-        for (int e = 0; e < 32; ++e)
-          r[e] = __float_as_uint(
-              fmaf(__uint_as_float(r[e]), s, -rm.slope * fabsf(d0 + static_cast<float>(e))));
-      } else {
-        const float b0 = rm.slope * d0;
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          const float2 bias = __ffma2_rn(make_float2(rm.slope, rm.slope),
-                                         make_float2(static_cast<float>(e), static_cast<float>(e + 1)),
-                                         make_float2(b0, b0));
-          const float2 y = __ffma2_rn(pair_of(r[e], r[e + 1]), make_float2(s, s), bias);
-          r[e] = __float_as_uint(y.x);
-          r[e + 1] = __float_as_uint(y.y);
-        }
-      }
+      for (int e = 0; e < W; e += 16) capped_near<8>(r + e, mods);
     }
   };
-  // Calls f(r, c) on the chunks in order, each loaded during the one before.
+  // Calls f(r, c) on the chunks in order.
   auto walk = [&](auto&& f) {
-    uint32_t ra[32], rb[32];
-    tmem_ld32_async(tm_s, ra);
+    uint32_t r[W];
 #pragma unroll 1
-    for (int c = 0; c < 4; c += 2) {
+    for (int c = 0; c < 128 / W; ++c) {
+#pragma unroll
+      for (int w = 0; w < W; w += 32) tmem_ld32_async(tm_s + W * c + w, r + w);
       tmem_wait_ld();
-      pin32(ra);
-      tmem_ld32_async(tm_s + 32 * (c + 1), rb);
-      f(ra, c);
-      tmem_wait_ld();
-      pin32(rb);
-      if (c == 0) tmem_ld32_async(tm_s + 64, ra);
-      f(rb, c + 1);
+      pin(r);
+      f(r, c);
     }
   };
+  // Pass 1: the row maximum; the reference moves before any weight.  Modified
+  // or masked scores go back over S, in log2 units, for pass 2 (modifying them
+  // again there is slower: 342 for 317 us on four long chunks with a window and
+  // a bias; what counts is that the loops stay small in the instruction cache).
+  const bool modified = MOD == kModsCap || rm.biased;
+  const bool back = modified || masked;
   if constexpr (!FIXED) {
-    // Pass 1: the row maximum (of the raw scores where the modification
-    // ascends); the reference moves before any weight.
     float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-    walk([&](uint32_t (&r)[32], int c) {
-      if (rm.biased) scores(r, c);
-      mask(r, c);
+    walk([&](uint32_t (&r)[W], int c) {
+      if constexpr (MOD == kModsCap) cap(r);
+      if (rm.biased) {
+        const float s = MOD == kModsCap ? 1.f : sl2;
+        const float d0 = static_cast<float>(key0 + W * c - rm.pos);
+        if (behind) {
 #pragma unroll
-      for (int e = 0; e < 32; e += 2)
+          for (int e = 0; e < W; ++e)
+            r[e] = __float_as_uint(
+                fmaf(__uint_as_float(r[e]), s, -rm.slope * fabsf(d0 + static_cast<float>(e))));
+        } else {
+          const float b0 = rm.slope * d0;
+#pragma unroll
+          for (int e = 0; e < W; e += 2) {
+            const float2 b = __ffma2_rn(make_float2(rm.slope, rm.slope),
+                                        make_float2(static_cast<float>(e), static_cast<float>(e + 1)),
+                                        make_float2(b0, b0));
+            const float2 y = __ffma2_rn(pair_of(r[e], r[e + 1]), make_float2(s, s), b);
+            r[e] = __float_as_uint(y.x);
+            r[e + 1] = __float_as_uint(y.y);
+          }
+        }
+      }
+      mask(r, c);
+      if (back) {
+#pragma unroll
+        for (int w = 0; w < W; w += 32) tmem_st32_async(tm_s + W * c + w, r + w);
+      }
+#pragma unroll
+      for (int e = 0; e < W; e += 2)
         mx4[(e / 2) % 4] = fmax3(mx4[(e / 2) % 4], __uint_as_float(r[e]), __uint_as_float(r[e + 1]));
     });
     float m_tile = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-    if (!rm.biased && m_tile != -INFINITY)
-      m_tile = MOD == kModsCap ? capped_score(m_tile, mods) : m_tile * sl2;
+    if (!modified) m_tile *= sl2;
     const bool moved = m_tile > m_ref + kRescaleSlackP;
     if (moved) {
       alpha = fast_exp2(m_ref - m_tile);
@@ -653,17 +648,14 @@ __device__ __forceinline__ void masked_step(uint32_t tm_s, int key0, const RowMa
       m_ref = m_tile;
     }
     rescale = __any_sync(0xffffffffu, moved);
+    if (back) tmem_wait_st();
   }
   // Pass 2: the weights.
-  const float mul = MOD == kModsCap || rm.biased ? 1.f : sl2;
-  const float m = m_ref;
+  const float m = m_ref, mul = modified ? 1.f : sl2;
   float2 sum[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-  walk([&](uint32_t (&r)[32], int c) {
-    if (MOD == kModsCap || rm.biased) scores(r, c);
-    mask(r, c);
-    uint32_t pk[16];
+  auto weights = [&](uint32_t* r, uint32_t* pk, int n) {
 #pragma unroll
-    for (int e = 0; e < 32; e += 2) {
+    for (int e = 0; e < n; e += 2) {
       float2 x = pair_of(r[e], r[e + 1]);
       if constexpr (!FIXED) x = __ffma2_rn(x, make_float2(mul, mul), make_float2(-m, -m));
       const float p0 = fast_exp2(x.x);  // 0 for the masked keys
@@ -671,7 +663,26 @@ __device__ __forceinline__ void masked_step(uint32_t tm_s, int key0, const RowMa
       pk[e / 2] = KV8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
       sum[(e / 2) % 4] = __fadd2_rn(sum[(e / 2) % 4], make_float2(p0, p1));
     }
-    tmem_st16_async(tm_s + 16 * c, pk);
+  };
+  walk([&](uint32_t (&r)[W], int c) {
+    uint32_t pk[W / 2];
+    if (FIXED && !masked && !any_far<W>(r, mods)) {
+      // The polynomial of one group next to the exponentials of the one before:
+      // they use different pipes (327 -> 292 us on four long chunks with a cap).
+#pragma unroll
+      for (int e = 0; e < W; e += 16) {
+        capped_near<8>(r + e, mods);
+        weights(r + e, pk + e / 2, 16);
+      }
+    } else {
+      if constexpr (FIXED) {
+        cap(r);
+        mask(r, c);
+      }
+      weights(r, pk, W);
+    }
+#pragma unroll
+    for (int w = 0; w < W / 2; w += 16) tmem_st16_async(tm_s + W / 2 * c + w, pk + w);
   });
   const float2 ps = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
   l_run += ps.x + ps.y;  // (in the plain step's order)

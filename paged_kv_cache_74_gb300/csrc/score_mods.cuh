@@ -37,17 +37,42 @@ __device__ __forceinline__ float capped_score(float x, const ScoreMods& m) {
   return m.cap_log2 * (t2 < kCapNear * kCapNear ? t * q : far);
 }
 
-// The same for a pair of scores with |t| <= kCapNear, by packed fused
-// multiply-adds (cap_log2 folded into the coefficients).
-__device__ __forceinline__ float2 capped_near(float2 x, const ScoreMods& m) {
+// The same for N pairs of scores with |t| <= kCapNear, in place, by packed fused
+// multiply-adds (cap_log2 folded into the coefficients); the pairs go through
+// the polynomial side by side, so that none waits for its own last step.
+template <int N>
+__device__ __forceinline__ void capped_near(uint32_t* r, const ScoreMods& m) {
   auto both = [](float c) { return make_float2(c, c); };
-  const float2 t = __fmul2_rn(x, both(m.cap_in));
-  const float2 t2 = __fmul2_rn(t, t);
-  float2 q = __ffma2_rn(t2, both(kTanhQ4 * m.cap_log2), both(kTanhQ3 * m.cap_log2));
-  q = __ffma2_rn(t2, q, both(kTanhQ2 * m.cap_log2));
-  q = __ffma2_rn(t2, q, both(kTanhQ1 * m.cap_log2));
-  q = __ffma2_rn(t2, q, both(kTanhQ0 * m.cap_log2));
-  return __fmul2_rn(t, q);
+  const float qs[5] = {kTanhQ0 * m.cap_log2, kTanhQ1 * m.cap_log2, kTanhQ2 * m.cap_log2,
+                       kTanhQ3 * m.cap_log2, kTanhQ4 * m.cap_log2};
+  float2 t[N], t2[N], q[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    t[i] = __fmul2_rn(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), both(m.cap_in));
+#pragma unroll
+  for (int i = 0; i < N; ++i) t2[i] = __fmul2_rn(t[i], t[i]);
+#pragma unroll
+  for (int i = 0; i < N; ++i) q[i] = __ffma2_rn(t2[i], both(qs[4]), both(qs[3]));
+#pragma unroll
+  for (int k = 2; k >= 0; --k)
+#pragma unroll
+    for (int i = 0; i < N; ++i) q[i] = __ffma2_rn(t2[i], q[i], both(qs[k]));
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    q[i] = __fmul2_rn(t[i], q[i]);
+    r[2 * i] = __float_as_uint(q[i].x);
+    r[2 * i + 1] = __float_as_uint(q[i].y);
+  }
+}
+
+// Whether some lane of the warp holds a score beyond kCapNear among its N.
+template <int N>
+__device__ __forceinline__ bool any_far(const uint32_t* r, const ScoreMods& m) {
+  float top[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int e = 0; e < N; e += 2)
+    top[(e / 2) % 4] = fmax3(top[(e / 2) % 4], fabsf(__uint_as_float(r[e])), fabsf(__uint_as_float(r[e + 1])));
+  return __any_sync(0xffffffffu, fmaxf(fmax3(top[0], top[1], top[2]), top[3]) * m.cap_in > kCapNear);
 }
 
 // The 16-token tiles of a request that hold a key its (single) row sees:
