@@ -416,9 +416,8 @@ pa_status pa_decode_fp8(void* out, const void* q, const void* key_cache, const v
  * included), and blocks (of 16 tokens, whatever block_size) without a seen key
  * are not read, nor are their block_tables entries: blocks that have left a
  * window may be reused.
- * Other arguments, workspace (pa_decode_workspace_size), sizes and errors as
- * pa_decode; always the warp-level tensor-core decode: groups of more than 4
- * q heads are cut into units of at most 4 as in pa_decode_xsplit.
+ * Other arguments, workspace (pa_decode_workspace_size), sizes, kernels and
+ * errors as pa_decode.
  */
 pa_status pa_decode_masked(void* out, const void* q, const void* key_cache, const void* value_cache,
                            const int32_t* block_tables, int32_t max_blocks_per_seq,

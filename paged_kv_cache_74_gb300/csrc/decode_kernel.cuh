@@ -572,7 +572,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
             const bool real = j < seg_n && !(MOD && span.empty);
             const int flags = (real ? 0 : kSkip) | (j >= (rows - 1) * C::NC ? kLastRow : 0);
             const int tile = MOD ? span.tile(b + j) : b + j;  // of the request's 16-token tiles
-            const int kvc = (XS || MOD) ? kvh / a.kv_div : kvh;  // kv head of the cache
+            const int kvc = XS ? kvh / a.kv_div : kvh;  // kv head of the cache
             meta[s] = make_int2(tile, flags);
             const uint32_t full = full0 + 8 * s;
             if (real) {

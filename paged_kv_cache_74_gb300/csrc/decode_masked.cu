@@ -3,10 +3,7 @@
 // instantiations of decode_kernel.cuh.
 //
 // The kernel is bound by the K/V bytes of the visible keys, as the plain
-// decode is; tiles without a visible key are not loaded.  Groups of more than 4
-// q heads are cut into units of at most 4 that each read their kv head's K/V
-// (the units of a kv head are neighbours in the tile order, so the repeated
-// reads mostly hit L2).
+// decode is; tiles without a visible key are not loaded.
 #include "decode_kernel.cuh"
 
 namespace pa {

@@ -423,9 +423,9 @@ pa_status launch_decode_rows(void* out, const void* q, const void* key_cache, co
   // The TMA views address the cache in 16-token tiles.
   const int num_tiles16 = num_blocks * (block_size / kBlockSize);
   const int group = num_heads / num_kv_heads;
-  const bool tc = !kv.xsplit && mods == nullptr && decode_uses_tc(head_dim, group);
-  // x-split and modified scores: units of up to 4 q heads (see xsplit_heads_per_unit).
-  const int unit_heads = kv.xsplit || mods != nullptr ? xsplit_heads_per_unit(group) : group;
+  const bool tc = !kv.xsplit && decode_uses_tc(head_dim, group);
+  // x-split: units of up to 4 q heads (see xsplit_heads_per_unit).
+  const int unit_heads = kv.xsplit ? xsplit_heads_per_unit(group) : group;
   const int kv_div = group / unit_heads;
   const bool pair = kv.pair && kv.e4m3 && !kv.xsplit && !tc && decode_fp8_pairs(head_dim, num_heads, num_kv_heads);
   if (kv.pair && !pair) return PA_ERR_INVALID;
@@ -483,9 +483,11 @@ pa_status launch_decode_rows(void* out, const void* q, const void* key_cache, co
   a.ctas_per_sm = tile_sms > 0 ? static_cast<int>(L.num_ctas / tile_sms) : 0;
   a.max_query_len = max_query_len;
   if (mods != nullptr) a.mods = *mods;
-  const cudaError_t err = mods != nullptr ? launch_decode_masked(a, kmap, vmap, head_dim, kv.e4m3, stream)
-                          : tc            ? launch_decode_tc(a, qmap, kmap, vmap, head_dim, kv.e4m3, stream)
-                                          : launch_decode(a, kmap, vmap, head_dim, kv.e4m3, kv.xsplit, stream);
+  const cudaError_t err =
+      tc ? (mods != nullptr ? launch_decode_tc_masked(a, qmap, kmap, vmap, head_dim, kv.e4m3, stream)
+                            : launch_decode_tc(a, qmap, kmap, vmap, head_dim, kv.e4m3, stream))
+         : (mods != nullptr ? launch_decode_masked(a, kmap, vmap, head_dim, kv.e4m3, stream)
+                            : launch_decode(a, kmap, vmap, head_dim, kv.e4m3, kv.xsplit, stream));
   return err == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
@@ -523,11 +525,8 @@ pa_status decode_masked_impl(void* out, const void* q, const void* key_cache, co
   if (partition_tokens < 0 || partition_tokens % kBlockSize != 0) return PA_ERR_INVALID;
   if (num_seqs == 0) return PA_OK;
   kv.pair = kv.e4m3 && decode_fp8_pairs(head_dim, num_heads, num_kv_heads);
-  const int group = num_heads / num_kv_heads;
-  const int units = kv.pair ? num_kv_heads / 2 : num_kv_heads * (group / xsplit_heads_per_unit(group));
-  if (units > 65535) return PA_ERR_UNSUPPORTED;
-  const DecodeLayout L =
-      decode_layout(num_seqs, num_heads, units, head_dim, max_seq_len, partition_tokens, kv.pair);
+  const DecodeLayout L = decode_layout(num_seqs, num_heads, kv.pair ? num_kv_heads / 2 : num_kv_heads,
+                                       head_dim, max_seq_len, partition_tokens, kv.pair);
   if (L.num_ctas > kMaxDecodeCtas) return PA_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < pa_decode_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim,
                                                                max_seq_len, partition_tokens))
@@ -1064,11 +1063,8 @@ pa_status prefill_varlen_impl(void* out, const void* q, const void* key_cache,
   // The decode rows' work units (masked: as in pa_decode_masked).
   const int group = num_heads / num_kv_heads;
   kv.pair = mods != nullptr && kv.e4m3 && decode_fp8_pairs(head_dim, num_heads, num_kv_heads);
-  const int units = mods == nullptr ? num_kv_heads
-                    : kv.pair       ? num_kv_heads / 2
-                                    : num_kv_heads * (group / xsplit_heads_per_unit(group));
-  if (units > 65535) return PA_ERR_UNSUPPORTED;
-  const DecodeLayout L = decode_layout(num_seqs, num_heads, units, head_dim, max_seq_len, 0, kv.pair);
+  const DecodeLayout L = decode_layout(num_seqs, num_heads, kv.pair ? num_kv_heads / 2 : num_kv_heads,
+                                       head_dim, max_seq_len, 0, kv.pair);
   if (L.num_ctas > kMaxDecodeCtas) return PA_ERR_UNSUPPORTED;
   const PrefillLayout PL =
       prefill_layout(L.total, num_seqs, total_q, num_heads, num_kv_heads, head_dim);

@@ -119,6 +119,8 @@ cudaError_t launch_decode_masked(const DecodeArgs& a, const CUtensorMap& kmap, c
 // (128-byte swizzle at head_dim 128, 64-byte at 64).
 cudaError_t launch_decode_tc(const DecodeArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
                              const CUtensorMap& vmap, int head_dim, bool kv8, cudaStream_t stream);
+cudaError_t launch_decode_tc_masked(const DecodeArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
+                                    const CUtensorMap& vmap, int head_dim, bool kv8, cudaStream_t stream);
 // Smallest group size the decode kernel is instantiated for that covers g.
 int decode_gmax(int group);
 // CTAs per SM the decode kernel for (head_dim, group) is built for.
