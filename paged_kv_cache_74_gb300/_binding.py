@@ -307,66 +307,111 @@ def append_tokens(key, value, key_cache, value_cache, block_tables, query_start_
     return slot_mapping
 
 
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, not on {device}")
+# The calls below are made for every layer of every step, often for a few
+# microseconds of GPU work: their checks go over plain tuples, tensors are
+# passed as integers, and the stream is read without building a Stream object.
+
+def _fn(name):
+    """The library's function of that name (loaded on first use)."""
+    return getattr(_lib if _lib is not None else load_library(), name)
 
 
-def _heads(name, t, T, heads, d):
-    _cuda(name, t, torch.bfloat16)
-    if tuple(t.shape) != (T, heads, d) or t.stride(2) != 1 or t.stride(1) != d:
+def _refuse(name, t, dtype, dev):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _check_all(dev, needed, optional):
+    """Every (name, tensor, dtype) a contiguous CUDA tensor of device `dev`, the
+    optional ones or None."""
+    for name, t, dtype in needed:
+        if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev or \
+                not t.is_contiguous():
+            _refuse(name, t, dtype, dev)
+    for name, t, dtype in optional:
+        if t is not None and (not isinstance(t, torch.Tensor) or t.dtype is not dtype or
+                              t.get_device() != dev or not t.is_contiguous()):
+            _refuse(name, t, dtype, dev)
+
+
+def _device_of(name, t):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.get_device()
+
+
+def _addr(t):
+    return t.data_ptr() if t is not None else 0
+
+
+def _launch(name, dev, *args):
+    """Calls the library with `dev` current, on its current stream."""
+    fn = _fn(name)
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    if torch._C._cuda_getDevice() == dev:
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, stream)
+    if status != PA_OK:
+        _check(name, status)
+
+
+def _heads(name, t, dev, T, heads, d):
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or t.get_device() != dev:
+        _refuse(name, t, torch.bfloat16, dev)
+    stride = t.stride()
+    if t.shape != (T, heads, d) or stride[2] != 1 or (stride[1] != d and heads > 1):
         raise ValueError(f"{name} must be [{T}, {heads}, {d}] with contiguous heads")
+    return stride[0]
 
 
 def _qk_norm_rope(fn, cache_dtype, scales, q, key, value, key_cache, value_cache, block_tables,
                   query_start_loc, seq_lens, cos_sin, q_weight, k_weight, eps, interleaved, positions,
                   out, slot_mapping, status):
-    _contig("key_cache", key_cache, cache_dtype)
-    _contig("value_cache", value_cache, cache_dtype)
-    _contig("block_tables", block_tables, torch.int32)
-    _contig("query_start_loc", query_start_loc, torch.int32)
-    _contig("seq_lens", seq_lens, torch.int32)
-    _contig("cos_sin", cos_sin, torch.float32)
+    dev = _device_of("q", q)
+    i32 = torch.int32
+    _check_all(dev, (("key_cache", key_cache, cache_dtype), ("value_cache", value_cache, cache_dtype),
+                     ("block_tables", block_tables, i32), ("query_start_loc", query_start_loc, i32),
+                     ("seq_lens", seq_lens, i32), ("cos_sin", cos_sin, torch.float32)),
+               (("q_weight", q_weight, torch.float32), ("k_weight", k_weight, torch.float32),
+                ("positions", positions, i32), ("out", out, torch.bfloat16),
+                ("slot_mapping", slot_mapping, torch.int64), ("status", status, i32)))
+    if key_cache.dim() != 4 or value_cache.shape != key_cache.shape:
+        raise ValueError("key_cache and value_cache must be [num_blocks, block, kv_heads, head_dim]")
     nb, bs, hkv, d = key_cache.shape
-    if value_cache.shape != key_cache.shape:
-        raise ValueError("key_cache and value_cache shapes differ")
     if q.dim() != 3:
         raise ValueError("q must be [T, heads, head_dim]")
-    T, hq = q.shape[0], q.shape[1]
-    _heads("q", q, T, hq, d)
-    _heads("key", key, T, hkv, d)
-    _heads("value", value, T, hkv, d)
+    T, hq, _ = q.shape
+    qs = _heads("q", q, dev, T, hq, d)
+    ks = _heads("key", key, dev, T, hkv, d)
+    vs = _heads("value", value, dev, T, hkv, d)
     S = seq_lens.shape[0]
     if block_tables.dim() != 2 or block_tables.shape[0] != S or query_start_loc.shape[0] != S + 1:
         raise ValueError("block_tables must be [num_seqs, max_blocks] and query_start_loc [num_seqs + 1]")
-    for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if t is not None and tuple(_contig(name, t, torch.float32).shape) != (d,):
-            raise ValueError(f"{name} must be [{d}]")
     if cos_sin.dim() != 2:
         raise ValueError("cos_sin must be [max_position, rot_dim]")
-    if positions is not None and _contig("positions", positions, torch.int32).numel() != T:
-        raise ValueError(f"positions must be [{T}]")
-    if slot_mapping is not None and _contig("slot_mapping", slot_mapping, torch.int64).numel() != T:
-        raise ValueError(f"slot_mapping must be [{T}]")
-    if status is not None and _contig("status", status, torch.int32).numel() < 4:
+    for name, t, n in (("q_weight", q_weight, d), ("k_weight", k_weight, d), ("positions", positions, T),
+                       ("slot_mapping", slot_mapping, T)):
+        if t is not None and t.numel() != n:
+            raise ValueError(f"{name} must be [{n}]")
+    if status is not None and status.numel() < 4:
         raise ValueError("status must hold 4 values")
     if out is None:
         out = torch.empty((T, hq, d), dtype=torch.bfloat16, device=q.device)
-    if tuple(_contig("out", out, torch.bfloat16).shape) != (T, hq, d):
+    elif out.shape != q.shape:
         raise ValueError(f"out must be [{T}, {hq}, {d}]")
-    _same_device(q.device, key=key, value=value, key_cache=key_cache, value_cache=value_cache,
-                 block_tables=block_tables, query_start_loc=query_start_loc, seq_lens=seq_lens,
-                 cos_sin=cos_sin, q_weight=q_weight, k_weight=k_weight, positions=positions, out=out,
-                 slot_mapping=slot_mapping, status=status)
-    with torch.cuda.device(q.device):
-        _check(fn, getattr(load_library(), fn)(
-            _ptr(out), _ptr(q), _ptr(key), _ptr(value), q.stride(0), key.stride(0), value.stride(0),
-            _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(cos_sin), cos_sin.shape[0],
-            cos_sin.shape[1], int(bool(interleaved)), _ptr(positions), _ptr(key_cache),
-            _ptr(value_cache), _ptr(block_tables), block_tables.shape[1], _ptr(query_start_loc),
-            _ptr(seq_lens), S, T, hq, hkv, d, bs, nb, *scales, _ptr(slot_mapping), _ptr(status),
-            _stream()))
+    _launch(fn, dev, out.data_ptr(), q.data_ptr(), key.data_ptr(), value.data_ptr(), qs, ks, vs,
+            _addr(q_weight), _addr(k_weight), eps, cos_sin.data_ptr(), cos_sin.shape[0],
+            cos_sin.shape[1], 1 if interleaved else 0, _addr(positions), key_cache.data_ptr(),
+            value_cache.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
+            query_start_loc.data_ptr(), seq_lens.data_ptr(), S, T, hq, hkv, d, bs, nb, *scales,
+            _addr(slot_mapping), _addr(status))
     return out
 
 
@@ -550,55 +595,54 @@ def decode_noalloc(q, key_cache, value_cache, block_tables, seq_lens, max_seq_le
     return out
 
 
-def _masks(q, rows, num_seqs, slopes, key_starts, prefix_lens):
-    if slopes is not None and _contig("slopes", slopes, torch.float32).numel() != q.shape[1]:
-        raise ValueError(f"slopes must be [{q.shape[1]}]")
-    if key_starts is not None and _contig("key_starts", key_starts, torch.int32).numel() != rows:
-        raise ValueError(f"key_starts must be [{rows}]")
-    if prefix_lens is not None and _contig("prefix_lens", prefix_lens, torch.int32).numel() != num_seqs:
-        raise ValueError(f"prefix_lens must be [{num_seqs}]")
-
-
-def _attention_args(q, key_cache, value_cache, cache_dtype, block_tables, seq_lens, out):
-    """Checks shared by the masked attention calls; returns out."""
-    _contig("q", q, torch.bfloat16)
-    _contig("key_cache", key_cache, cache_dtype)
-    _contig("value_cache", value_cache, cache_dtype)
-    _contig("block_tables", block_tables, torch.int32)
-    _contig("seq_lens", seq_lens, torch.int32)
+def _attention_args(q, key_cache, value_cache, cache_dtype, block_tables, seq_lens, out, slopes,
+                    key_starts, prefix_lens, workspace, query_start_loc):
+    """Checks shared by the masked attention calls; returns (device index, out)."""
+    dev = _device_of("q", q)
+    bf16, i32 = torch.bfloat16, torch.int32
+    _check_all(dev, (("q", q, bf16), ("key_cache", key_cache, cache_dtype),
+                     ("value_cache", value_cache, cache_dtype), ("block_tables", block_tables, i32),
+                     ("seq_lens", seq_lens, i32)),
+               (("query_start_loc", query_start_loc, i32), ("out", out, bf16),
+                ("slopes", slopes, torch.float32), ("key_starts", key_starts, i32),
+                ("prefix_lens", prefix_lens, i32), ("workspace", workspace, torch.uint8)))
     if q.dim() != 3 or key_cache.dim() != 4 or key_cache.shape[3] != q.shape[2] or \
             value_cache.shape != key_cache.shape:
         raise ValueError("cache shapes do not match q")
-    if block_tables.dim() != 2 or block_tables.shape[0] != seq_lens.shape[0]:
+    S = seq_lens.shape[0]
+    if block_tables.dim() != 2 or block_tables.shape[0] != S:
         raise ValueError("block_tables must be [num_seqs, max_blocks]")
+    rows, hq = q.shape[0], q.shape[1]
+    if slopes is not None and slopes.numel() != hq:
+        raise ValueError(f"slopes must be [{hq}]")
+    if key_starts is not None and key_starts.numel() != rows:
+        raise ValueError(f"key_starts must be [{rows}]")
+    if prefix_lens is not None and prefix_lens.numel() != S:
+        raise ValueError(f"prefix_lens must be [{S}]")
     if out is None:
         out = torch.empty_like(q)
-    if _contig("out", out, torch.bfloat16).shape != q.shape:
+    elif out.shape != q.shape:
         raise ValueError("out must have q's shape")
-    return out
+    return dev, out
 
 
 def _decode_masked(fn, cache_dtype, scales, q, key_cache, value_cache, block_tables, seq_lens,
                    max_seq_len, scale, softcap, slopes, key_starts, prefix_lens, out, workspace,
                    partition_tokens):
-    out = _attention_args(q, key_cache, value_cache, cache_dtype, block_tables, seq_lens, out)
+    dev, out = _attention_args(q, key_cache, value_cache, cache_dtype, block_tables, seq_lens, out,
+                               slopes, key_starts, prefix_lens, workspace, None)
     S, hq, d = q.shape
     nb, bs, hkv, _ = key_cache.shape
     if seq_lens.shape[0] != S:
         raise ValueError(f"seq_lens must be [{S}]")
-    _masks(q, S, S, slopes, key_starts, prefix_lens)
-    _same_device(q.device, key_cache=key_cache, value_cache=value_cache, block_tables=block_tables,
-                 seq_lens=seq_lens, slopes=slopes, key_starts=key_starts, prefix_lens=prefix_lens,
-                 out=out, workspace=workspace)
-    with torch.cuda.device(q.device):
-        if workspace is None:
+    if workspace is None:
+        with torch.cuda.device(dev):
             workspace = new_workspace(
                 decode_workspace_size(S, hq, hkv, d, max_seq_len, partition_tokens), q.device)
-        _check(fn, getattr(load_library(), fn)(
-            _ptr(out), _ptr(q), _ptr(key_cache), _ptr(value_cache), _ptr(block_tables),
-            block_tables.shape[1], _ptr(seq_lens), S, int(max_seq_len), hq, hkv, d, bs, nb,
-            float(scale), *scales, float(softcap), _ptr(slopes), _ptr(key_starts), _ptr(prefix_lens),
-            int(partition_tokens), _ptr(workspace), workspace.numel(), _stream()))
+    _launch(fn, dev, out.data_ptr(), q.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
+            block_tables.data_ptr(), block_tables.shape[1], seq_lens.data_ptr(), S, int(max_seq_len), hq,
+            hkv, d, bs, nb, scale, *scales, softcap, _addr(slopes), _addr(key_starts),
+            _addr(prefix_lens), int(partition_tokens), workspace.data_ptr(), workspace.numel())
     return out
 
 
@@ -690,26 +734,22 @@ def prefill_masked_workspace_size(num_seqs, total_q, num_heads, num_kv_heads, he
 def _prefill_masked(fn, cache_dtype, scales, q, key_cache, value_cache, query_start_loc, seq_lens,
                     block_tables, max_query_len, max_seq_len, scale, softcap, slopes, key_starts,
                     prefix_lens, out, workspace):
-    out = _attention_args(q, key_cache, value_cache, cache_dtype, block_tables, seq_lens, out)
+    dev, out = _attention_args(q, key_cache, value_cache, cache_dtype, block_tables, seq_lens, out,
+                               slopes, key_starts, prefix_lens, workspace, query_start_loc)
     tq, hq, d = q.shape
     nb, bs, hkv, _ = key_cache.shape
     S = seq_lens.shape[0]
-    if _contig("query_start_loc", query_start_loc, torch.int32).numel() != S + 1:
+    if query_start_loc is None or query_start_loc.numel() != S + 1:
         raise ValueError(f"query_start_loc must be [{S + 1}]")
-    _masks(q, tq, S, slopes, key_starts, prefix_lens)
-    _same_device(q.device, key_cache=key_cache, value_cache=value_cache, query_start_loc=query_start_loc,
-                 seq_lens=seq_lens, block_tables=block_tables, slopes=slopes, key_starts=key_starts,
-                 prefix_lens=prefix_lens, out=out, workspace=workspace)
-    with torch.cuda.device(q.device):
-        if workspace is None:
+    if workspace is None:
+        with torch.cuda.device(dev):
             workspace = new_workspace(prefill_masked_workspace_size(S, tq, hq, hkv, d, max_seq_len),
                                       q.device)
-        _check(fn, getattr(load_library(), fn)(
-            _ptr(out), _ptr(q), _ptr(key_cache), _ptr(value_cache), _ptr(query_start_loc),
-            _ptr(seq_lens), S, tq, int(max_query_len), int(max_seq_len), _ptr(block_tables),
-            block_tables.shape[1], hq, hkv, d, bs, nb, float(scale), *scales, float(softcap),
-            _ptr(slopes), _ptr(key_starts), _ptr(prefix_lens), _ptr(workspace), workspace.numel(),
-            _stream()))
+    _launch(fn, dev, out.data_ptr(), q.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
+            query_start_loc.data_ptr(), seq_lens.data_ptr(), S, tq, int(max_query_len), int(max_seq_len),
+            block_tables.data_ptr(), block_tables.shape[1], hq, hkv, d, bs, nb, scale, *scales, softcap,
+            _addr(slopes), _addr(key_starts), _addr(prefix_lens), workspace.data_ptr(),
+            workspace.numel())
     return out
 
 
