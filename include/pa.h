@@ -618,7 +618,7 @@ size_t pa_prefill_masked_workspace_size(int32_t num_seqs, int32_t total_q, int32
  * infinity in the tile's product).  Rows that see no key give zeros.
  * When max_query_len > 1 a first kernel plans the query tiles (which keys each
  * needs), then the tile kernel and the decode kernel follow as in
- * pa_prefill_varlen, without the split of the SMs between them.  Other
+ * pa_prefill_varlen.  Other
  * arguments, sizes and errors as pa_prefill_varlen; rows with q_len == 1 run as
  * in pa_decode_masked.
  */

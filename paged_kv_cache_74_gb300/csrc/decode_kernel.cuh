@@ -350,24 +350,24 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
     long long nb_sum = 0;
     for (int r = lane; r < a.num_seqs; r += 32) {
       int len, row;
-      int n = request_blocks(a, r, &len, &row);
       if constexpr (MOD)
-        if (n > 0) n = tile_span(a.mods, r, row, len).nb;
-      nb_sum += n;
+        nb_sum += tiles_from(a, r, row_info(a, r));
+      else
+        nb_sum += request_blocks(a, r, &len, &row);
     }
     const long long W = warp_sum_ll(nb_sum) * a.num_kv_heads;
     long long lo, hi;
     if constexpr (MIX) {
       // The tile kernel's cost (the call's prefill rows) sets how many CTAs
-      // take the decode rows.
+      // take the decode rows (MOD: the plan says, which is complete).
       long long tc_sum = 0;
-      for (int r = lane; r < a.num_seqs; r += 32) {
+      for (int r = lane; !MOD && r < a.num_seqs; r += 32) {
         const TileReq p = tile_req(a.query_start_loc[r], a.query_start_loc[r + 1], a.seq_lens[r], row_limits(a));
         tc_sum += kCostStep * tile_req_steps(p) + kCostUnit * p.ntq;
       }
       const long long Ct = warp_sum_ll(tc_sum) * a.num_kv_heads * ((a.group + 1) / 2);
-      const int nct =
-          decode_split_ctas(tile_kernel_sms(Ct, W, a.tile_sms, KV8), a.tile_sms, a.num_ctas, a.ctas_per_sm);
+      const int tile_ctas = MOD ? __ldcg(&a.plan->tile_ctas) : tile_kernel_sms(Ct, W, a.tile_sms, KV8);
+      const int nct = decode_split_ctas(tile_ctas, a.tile_sms, a.num_ctas, a.ctas_per_sm);
       lo = W > 0 && cta < nct ? range_lo(W, nct, cta) : 0;
       hi = W > 0 && cta < nct ? range_lo(W, nct, cta + 1) : 0;
       if (lane == 0) *split_ctas = nct;
@@ -390,12 +390,18 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
       // Request holding tile `lo`: scan the per-request tile counts 32 at a time.
       long long base = 0;  // tiles before request r0
       int r0 = -1;
+      RowInfo first_info{};  // MOD: of r0
       for (int rc = 0; rc < a.num_seqs && r0 < 0; rc += 32) {
         const int r = rc + lane;
         int len, row;
-        int nr = r < a.num_seqs ? request_blocks(a, r, &len, &row) : 0;
-        if constexpr (MOD)
-          if (nr > 0) nr = tile_span(a.mods, r, row, len).nb;
+        RowInfo info{};
+        int nr = 0;
+        if constexpr (MOD) {
+          info = row_info(a, r);
+          if (r < a.num_seqs) nr = tiles_from(a, r, info);
+        } else if (r < a.num_seqs) {
+          nr = request_blocks(a, r, &len, &row);
+        }
         const long long nt = static_cast<long long>(nr) * a.num_kv_heads;
         const long long chunk = warp_sum_ll(nt);
         if (base + chunk <= lo) {  // tile `lo` lies past these 32 requests
@@ -414,6 +420,13 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
           const long long excl = __shfl_sync(0xffffffffu, incl - nt, first);
           r0 = rc + first;
           base += excl;
+          if constexpr (MOD) {
+            first_info.len = __shfl_sync(0xffffffffu, info.len, first);
+            first_info.q0 = __shfl_sync(0xffffffffu, info.q0, first);
+            first_info.q1 = __shfl_sync(0xffffffffu, info.q1, first);
+            first_info.prefix = __shfl_sync(0xffffffffu, info.prefix, first);
+            first_info.start = __shfl_sync(0xffffffffu, info.start, first);
+          }
         } else {
           base += __shfl_sync(0xffffffffu, incl, 31);
         }
@@ -442,33 +455,20 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
       // lengths and masks are read one request further ahead than the ids.
       TileSpan nxt_span{};
       int nxt_nb = 0, nxt_row = 0;
-      int fut_r = -1, fut_len = 0, fut_q0 = 0, fut_q1 = 0, fut_prefix = 0, fut_start = 0;
-      auto load_future = [&](int rr) {
-        fut_r = rr;
-        fut_prefix = 0;
-        fut_start = 0;
-        if (rr >= a.num_seqs) return;
-        fut_len = __ldg(a.seq_lens + rr);
-        int at = rr;
-        if (a.query_start_loc != nullptr) {
-          fut_q0 = __ldg(a.query_start_loc + rr);
-          fut_q1 = __ldg(a.query_start_loc + rr + 1);
-          at = fut_q0 >= 0 && fut_q0 < a.total_q ? fut_q0 : 0;
-        }
-        if (a.mods.prefix_lens != nullptr) fut_prefix = __ldg(a.mods.prefix_lens + rr);
-        if (a.mods.key_starts != nullptr) fut_start = __ldg(a.mods.key_starts + at);
-      };
+      int fut_r = -1;
+      RowInfo fut{};
       auto prefetch_next = [&](int rr) {
         if constexpr (MOD) {
-          if (fut_r != rr + 1) load_future(rr + 1);
+          if (fut_r != rr + 1) fut = row_info(a, rr + 1);
           nxt_r = rr + 1;
-          nxt_nb = nxt_r < a.num_seqs ? blocks_from(a, nxt_r, fut_len, fut_q0, fut_q1, &nxt_len, &nxt_row) : 0;
+          nxt_nb = nxt_r < a.num_seqs ? blocks_from(a, nxt_r, fut.len, fut.q0, fut.q1, &nxt_len, &nxt_row) : 0;
           if (nxt_nb > 0) {
-            nxt_span = make_span(nxt_len, fut_prefix, fut_start);
+            nxt_span = make_span(nxt_len, fut.prefix, fut.start);
             nxt_nb = nxt_span.nb;
             load_row(nxt_r, nxt_ids, nxt_span);
           }
-          load_future(rr + 2);
+          fut_r = rr + 2;
+          fut = row_info(a, fut_r);
         } else {
           nxt_r = rr + 1;
           if (nxt_r < a.num_seqs) {
@@ -483,11 +483,11 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
       };
       // Length, q row and tile count of request rr, and its block ids.
       int r = r0, len = 0, row = 0;
-      auto take_request = [&](int rr) -> int {
+      auto take_request = [&](int rr, const RowInfo& info) -> int {
         if constexpr (MOD) {
-          int n = request_blocks(a, rr, &len, &row);
+          int n = blocks_from(a, rr, info.len, info.q0, info.q1, &len, &row);
           if (n > 0) {
-            span = tile_span(a.mods, rr, row, len);
+            span = make_span(len, info.prefix, info.start);
             n = span.nb;
             load_row(rr, cur_ids, span);
           }
@@ -497,7 +497,11 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
           return request_blocks(a, rr, &len, &row);
         }
       };
-      int nb = take_request(r);
+      if constexpr (MOD) {
+        fut_r = r + 1;
+        fut = row_info(a, fut_r);
+      }
+      int nb = take_request(r, first_info);
       prefetch_next(r);
       long long off = lo - base;
       int kvh = static_cast<int>(off / nb);
@@ -631,7 +635,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
 #pragma unroll
                 for (int m = 0; m < kRowCache; ++m) cur_ids[m] = nxt_ids[m];
               } else {
-                nb = take_request(r);
+                nb = take_request(r, MOD ? row_info(a, r) : first_info);
               }
             }
             if (nb == 0) ok = false;  // cannot happen while t < hi

@@ -10,14 +10,18 @@ namespace pa {
 
 cudaError_t launch_decode_masked(const DecodeArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
                                  int head_dim, bool kv8, cudaStream_t stream) {
+  const bool mix = a.tile_sms > 0;  // built for head_dim 128 (the host splits the SMs only there)
   // e4m3 units of two kv heads (8 q heads, head_dim 128).
   if (kv8 && a.group == 8 && head_dim == 128)
-    return launch_decode_impl<128, 8, true, false, false, true>(a, kmap, vmap, stream);
+    return mix ? launch_decode_impl<128, 8, true, false, true, true>(a, kmap, vmap, stream)
+               : launch_decode_impl<128, 8, true, false, false, true>(a, kmap, vmap, stream);
   const int gmax = decode_gmax(a.group);
-#define PA_DECODE_CASE(DD, GG)                                                            \
-  if (head_dim == DD && gmax == GG)                                                       \
-    return kv8 ? launch_decode_impl<DD, GG, true, false, false, true>(a, kmap, vmap, stream) \
-               : launch_decode_impl<DD, GG, false, false, false, true>(a, kmap, vmap, stream);
+#define PA_DECODE_CASE(DD, GG)                                                                     \
+  if (head_dim == DD && gmax == GG)                                                                \
+    return kv8 ? (mix ? launch_decode_impl<DD, GG, true, false, DD == 128, true>(a, kmap, vmap, stream)  \
+                      : launch_decode_impl<DD, GG, true, false, false, true>(a, kmap, vmap, stream))     \
+               : (mix ? launch_decode_impl<DD, GG, false, false, DD == 128, true>(a, kmap, vmap, stream) \
+                      : launch_decode_impl<DD, GG, false, false, false, true>(a, kmap, vmap, stream));
   PA_DECODE_CASE(128, 1) PA_DECODE_CASE(128, 2) PA_DECODE_CASE(128, 4)
   PA_DECODE_CASE(64, 1) PA_DECODE_CASE(64, 2) PA_DECODE_CASE(64, 4)
 #undef PA_DECODE_CASE

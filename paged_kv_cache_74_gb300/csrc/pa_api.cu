@@ -419,7 +419,7 @@ pa_status launch_decode_rows(void* out, const void* q, const void* key_cache, co
                              const DecodeLayout& L, void* workspace, cudaStream_t stream,
                              const KvFormat& kv = KvFormat(), bool after_prefill = false,
                              int tile_sms = 0, int max_query_len = 0,
-                             const ScoreMods* mods = nullptr) {
+                             const ScoreMods* mods = nullptr, const PlanHead* plan = nullptr) {
   // The TMA views address the cache in 16-token tiles.
   const int num_tiles16 = num_blocks * (block_size / kBlockSize);
   const int group = num_heads / num_kv_heads;
@@ -483,6 +483,7 @@ pa_status launch_decode_rows(void* out, const void* q, const void* key_cache, co
   a.ctas_per_sm = tile_sms > 0 ? static_cast<int>(L.num_ctas / tile_sms) : 0;
   a.max_query_len = max_query_len;
   if (mods != nullptr) a.mods = *mods;
+  a.plan = plan;
   const cudaError_t err =
       tc ? (mods != nullptr ? launch_decode_tc_masked(a, qmap, kmap, vmap, head_dim, kv.e4m3, stream)
                             : launch_decode_tc(a, qmap, kmap, vmap, head_dim, kv.e4m3, stream))
@@ -1120,9 +1121,9 @@ pa_status prefill_varlen_impl(void* out, const void* q, const void* key_cache,
     // them (tile_kernel_sms()), so that the decode rows start at once on the
     // SMs the tiles leave instead of after the tile CTAs.
     const bool split_sms =
-        mods == nullptr && head_dim == 128 && !decode_uses_tc(head_dim, group) &&
+        head_dim == 128 && !decode_uses_tc(head_dim, group) &&
         L.num_ctas == static_cast<int64_t>(PL.num_ctas) * decode_ctas_per_sm(head_dim, group);
-    p.partition = split_sms ? 1 : 0;
+    p.partition = split_sms ? (mods != nullptr && kv.e4m3 ? 2 : 1) : 0;
     // Both kernels go on the caller's stream.  The tile kernel lets the
     // decode launch start once the kernels before this call are complete;
     // the decode CTAs then take the SMs the tiles leave free, and the decode
@@ -1142,7 +1143,8 @@ pa_status prefill_varlen_impl(void* out, const void* q, const void* key_cache,
     return launch_decode_rows(out, q, key_cache, value_cache, block_tables, max_blocks_per_seq,
                               seq_lens, query_start_loc, num_seqs, total_q, max_seq_len,
                               num_heads, num_kv_heads, head_dim, num_blocks, block_size, scale, L,
-                              workspace, cs, kv, true, split_sms ? PL.num_ctas : 0, max_query_len, mods);
+                              workspace, cs, kv, true, split_sms ? PL.num_ctas : 0, max_query_len, mods,
+                              p.plan.head);
   }
   // Only decode rows: the decode kernel.
   return launch_decode_rows(out, q, key_cache, value_cache, block_tables, max_blocks_per_seq,

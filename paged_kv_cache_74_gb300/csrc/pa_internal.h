@@ -29,6 +29,8 @@ struct ScoreMods {
   float cap_log2 = 0.f;                  // cap * log2(e); 0: no cap
 };
 
+struct PlanHead;
+
 // Decode work.  The tiles (request, kv head, block) of all decode rows are
 // numbered request-major, then kv head, then block; the W tiles are split
 // into num_ctas contiguous, equal ranges, one per CTA of a persistent grid.
@@ -75,6 +77,7 @@ struct DecodeArgs {
   int ctas_per_sm;
   int max_query_len;                // of the call (the tile kernel's row checks)
   ScoreMods mods;                   // masked calls only
+  const PlanHead* plan;             // masked calls with tile_sms > 0
 };
 
 // Launch `kernel` on `stream` with programmatic stream serialization: the
@@ -135,7 +138,8 @@ struct PlanTile {
 };
 static_assert(sizeof(PlanTile) == 48, "read as three 16-byte words");
 struct PlanHead {
-  int tiles, pad;
+  int tiles;
+  int tile_ctas;                    // CTAs (one per SM) the tile kernel works on
   long long steps;                  // 128-key steps of all tiles (one head pair)
 };
 struct PrefillPlan {
@@ -184,7 +188,8 @@ struct PrefillArgs {
   PrefillPlan plan;
   // 1: the decode rows of the same call follow in the streaming decode
   // kernel, which takes the SMs this grid leaves (tile_kernel_sms()); only
-  // that many CTAs work.  0: every CTA works.
+  // that many CTAs work.  0: every CTA works.  (Masked calls: 2 over e4m3
+  // caches, and the plan holds the number.)
   int partition;
 };
 // Bytes of the prefill partial records (part_ml and part_o) for num_ctas CTAs.

@@ -835,7 +835,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
     const long long Cw = (kCostStep * n_steps + kCostUnit * static_cast<long long>(MOD ? n_tiles : usum)) * NP;
     // The CTAs that work: all, or (mixed batch) the share of the SMs the
     // decode rows leave; the others exit at once.
-    const int nct = a.partition
+    const int nct = MOD ? __ldcg(&a.plan.head->tile_ctas)
+                    : a.partition
                         ? tile_kernel_sms(Cw, static_cast<long long>(__reduce_add_sync(0xffffffffu, dsum)) *
                                                   a.num_kv_heads,
                                           a.num_ctas, KV8)

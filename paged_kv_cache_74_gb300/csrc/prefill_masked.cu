@@ -47,10 +47,20 @@ __device__ __forceinline__ long long block_scan(long long v, long long* sums, lo
 
 __global__ void __launch_bounds__(kPlanThreads) plan_prefill_kernel(const PrefillArgs a) {
   __shared__ long long sums[33];
+  __shared__ unsigned long long decode_tiles;  // 16-token tiles of the decode rows (per kv head)
   griddep_launch_dependents();
   griddep_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const PrefillPlan& pl = a.plan;
+  if (tid == 0) decode_tiles = 0;
+  if (a.partition) {
+    __syncthreads();
+    for (int r = tid; r < a.num_seqs; r += kPlanThreads) {
+      const int q0 = __ldg(a.query_start_loc + r), len = __ldg(a.seq_lens + r);
+      if (decode_row_tiles(q0, __ldg(a.query_start_loc + r + 1), len, row_limits(a)) > 0)
+        atomicAdd(&decode_tiles, static_cast<unsigned long long>(tile_span(a.mods, r, q0, len).nb));
+    }
+  }
   // First tile of each request.
   long long tiles = 0;
   for (int base = 0; base < a.num_seqs; base += kPlanThreads) {
@@ -117,6 +127,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_prefill_kernel(const Prefil
   if (tid == 0) {
     pl.head->tiles = n;
     pl.head->steps = steps;
+    // The split of the SMs with the decode rows.
+    const long long pairs = static_cast<long long>(a.num_kv_heads) * ((a.group + 1) / 2);
+    pl.head->tile_ctas =
+        a.partition ? masked_tile_sms((kCostStep * steps + kCostUnit * n) * pairs,
+                                      static_cast<long long>(decode_tiles) * a.num_kv_heads, a.num_ctas,
+                                      a.partition == 2)
+                    : a.num_ctas;
   }
 }
 

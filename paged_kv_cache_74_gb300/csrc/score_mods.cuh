@@ -7,6 +7,7 @@
 //   j < prefix  or  start <= j <= p.
 #pragma once
 
+#include "decode_common.cuh"
 #include "pa_internal.h"
 #include "pa_ptx.cuh"
 
@@ -105,6 +106,32 @@ __device__ __forceinline__ TileSpan make_span(int len, int prefix, int start) {
 __device__ __forceinline__ TileSpan tile_span(const ScoreMods& m, int r, int row, int len) {
   return make_span(len, m.prefix_lens != nullptr ? __ldg(m.prefix_lens + r) : 0,
                    m.key_starts != nullptr ? __ldg(m.key_starts + row) : 0);
+}
+
+// What a decode row's tiles follow from, read in one round of loads (two where
+// the row comes from query_start_loc).
+struct RowInfo {
+  int len, q0, q1, prefix, start;
+};
+__device__ __forceinline__ RowInfo row_info(const DecodeArgs& a, int r) {
+  RowInfo i{0, 0, 0, 0, 0};
+  if (r >= a.num_seqs) return i;
+  i.len = __ldg(a.seq_lens + r);
+  int row = r;
+  if (a.query_start_loc != nullptr) {
+    i.q0 = __ldg(a.query_start_loc + r);
+    i.q1 = __ldg(a.query_start_loc + r + 1);
+    row = i.q0 >= 0 && i.q0 < a.total_q ? i.q0 : 0;
+  }
+  if (a.mods.prefix_lens != nullptr) i.prefix = __ldg(a.mods.prefix_lens + r);
+  if (a.mods.key_starts != nullptr) i.start = __ldg(a.mods.key_starts + row);
+  return i;
+}
+
+// Its tiles (0: not a decode row, or lengths out of range).
+__device__ __forceinline__ int tiles_from(const DecodeArgs& a, int r, const RowInfo& i) {
+  int len = 0, row = 0;
+  return blocks_from(a, r, i.len, i.q0, i.q1, &len, &row) > 0 ? make_span(len, i.prefix, i.start).nb : 0;
 }
 
 // Whether the row at the last position sees key t; vis = {prefix, start}.

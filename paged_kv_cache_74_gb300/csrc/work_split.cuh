@@ -116,6 +116,30 @@ __host__ __device__ __forceinline__ int tile_kernel_sms(long long tile_cost, lon
   return static_cast<int>(n < 1 ? 1 : (n > num_sms ? num_sms : n));
 }
 
+// The same for a masked call, whose steps the plan has counted: of the two
+// whole numbers next to the proportional share the one whose slower side ends
+// first (a few short decode rows want two SMs rather than one; 126 against 87 us
+// of tiles when they were left with one).  Tile weights measured on a 512-token
+// chunk before 63 decode rows, with and without a cap (500, 600, 690, 850 ns
+// bf16: 275, 233, 237, 244 us capped; e4m3 1275, 1434, 1590 ns: 184, 174, 182 us).
+constexpr long long kMaskedTileNsPerCost = 650;
+constexpr long long kMaskedTileNsPerCost8 = 1434;
+
+__host__ __device__ __forceinline__ int masked_tile_sms(long long tile_cost, long long decode_tiles, int num_sms,
+                                               bool e4m3) {
+  if (tile_cost <= 0) return 0;
+  const long long t = tile_cost * (e4m3 ? kMaskedTileNsPerCost8 : kMaskedTileNsPerCost);
+  const long long d = decode_tiles * (e4m3 ? kDecodeNsPerTile8 : kDecodeNsPerTile);
+  if (decode_tiles <= 0 || num_sms < 2 || t > kSplitMaxTileNsPerSm * num_sms) return num_sms;
+  const long long share = static_cast<long long>(num_sms) * t / (t + d);
+  const int lo = static_cast<int>(share < 1 ? 1 : (share > num_sms - 1 ? num_sms - 1 : share));
+  auto end = [&](int n) -> long long {
+    const long long a = t / n, b = d / (num_sms - n);
+    return a > b ? a : b;
+  };
+  return lo + 1 >= num_sms || end(lo) <= end(lo + 1) ? lo : lo + 1;
+}
+
 // CTAs of a decode grid of num_ctas (ctas_per_sm on each of num_sms SMs)
 // that take the decode rows when the tile kernel keeps tile_sms SMs.
 __host__ __device__ __forceinline__ int decode_split_ctas(int tile_sms, int num_sms, int num_ctas, int ctas_per_sm) {
