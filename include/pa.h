@@ -218,7 +218,8 @@ pa_status pa_append_tokens(const void* key, const void* value, int64_t key_strid
  * position lies outside the table is skipped altogether (slot -1,
  * PA_DEV_BAD_POSITION).  Rows behind query_start_loc[num_seqs] are left as
  * they are in q_out and slot_mapping.  num_seqs == 0 or total_tokens == 0 is
- * a no-op.  A head with a NaN or an infinity norms to NaN.
+ * a no-op.  A head with a NaN or an infinity norms to NaN; the squares of a
+ * normed head must sum to a finite float (values below 1e18).
  */
 pa_status pa_qk_norm_rope_append(void* q_out, const void* q, const void* key, const void* value,
                                  int64_t q_stride, int64_t key_stride, int64_t value_stride,
@@ -615,7 +616,11 @@ size_t pa_prefill_masked_workspace_size(int32_t num_seqs, int32_t total_q, int32
  * Keys that no row of a request's 128-row query tile sees may hold anything,
  * and 16-token blocks without a seen key are not read; V of a key that some
  * row of the tile sees must be finite (a weight of 0 does not cancel an
- * infinity in the tile's product).  Rows that see no key give zeros.
+ * infinity in the tile's product).  Rows that see no key give zeros.  Over
+ * bf16 caches with a softcap up to 50 the softmax needs no running maximum
+ * and uses none: values of magnitude 2^-45 to 2^45 then keep their precision
+ * whatever the scores (smaller ones lose theirs only in rows whose scores all
+ * lie near -softcap).
  * When max_query_len > 1 a first kernel plans the query tiles (which keys each
  * needs), then the tile kernel and the decode kernel follow as in
  * pa_prefill_varlen.  Other

@@ -407,7 +407,7 @@ def _qk_norm_rope(fn, cache_dtype, scales, q, key, value, key_cache, value_cache
     elif out.shape != q.shape:
         raise ValueError(f"out must be [{T}, {hq}, {d}]")
     _launch(fn, dev, out.data_ptr(), q.data_ptr(), key.data_ptr(), value.data_ptr(), qs, ks, vs,
-            _addr(q_weight), _addr(k_weight), eps, cos_sin.data_ptr(), cos_sin.shape[0],
+            _addr(q_weight), _addr(k_weight), float(eps), cos_sin.data_ptr(), cos_sin.shape[0],
             cos_sin.shape[1], 1 if interleaved else 0, _addr(positions), key_cache.data_ptr(),
             value_cache.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
             query_start_loc.data_ptr(), seq_lens.data_ptr(), S, T, hq, hkv, d, bs, nb, *scales,
@@ -641,7 +641,7 @@ def _decode_masked(fn, cache_dtype, scales, q, key_cache, value_cache, block_tab
                 decode_workspace_size(S, hq, hkv, d, max_seq_len, partition_tokens), q.device)
     _launch(fn, dev, out.data_ptr(), q.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
             block_tables.data_ptr(), block_tables.shape[1], seq_lens.data_ptr(), S, int(max_seq_len), hq,
-            hkv, d, bs, nb, scale, *scales, softcap, _addr(slopes), _addr(key_starts),
+            hkv, d, bs, nb, float(scale), *scales, float(softcap), _addr(slopes), _addr(key_starts),
             _addr(prefix_lens), int(partition_tokens), workspace.data_ptr(), workspace.numel())
     return out
 
@@ -747,8 +747,8 @@ def _prefill_masked(fn, cache_dtype, scales, q, key_cache, value_cache, query_st
                                       q.device)
     _launch(fn, dev, out.data_ptr(), q.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
             query_start_loc.data_ptr(), seq_lens.data_ptr(), S, tq, int(max_query_len), int(max_seq_len),
-            block_tables.data_ptr(), block_tables.shape[1], hq, hkv, d, bs, nb, scale, *scales, softcap,
-            _addr(slopes), _addr(key_starts), _addr(prefix_lens), workspace.data_ptr(),
+            block_tables.data_ptr(), block_tables.shape[1], hq, hkv, d, bs, nb, float(scale), *scales,
+            float(softcap), _addr(slopes), _addr(key_starts), _addr(prefix_lens), workspace.data_ptr(),
             workspace.numel())
     return out
 

@@ -507,10 +507,12 @@ __device__ __noinline__ bool merge_staged(const float* __restrict__ part_ml,
 
 // ---- the softmax of a step with modified scores
 //
-// Largest cap (log2 units) for which the weights 2^y, |y| <= cap, need no
-// running maximum: sums over 2^31 keys stay below 2^111, and O keeps 2^16 for
-// the values.
-constexpr float kFixedCap = 80.f;
+// Largest cap (log2 units, a cap of 50.6) for which the weights need no running
+// maximum, and their reference.  The weights then lie between 2^-81 and 2^65,
+// bf16 and fp32 numbers both; values of 2^-45 to 2^45 stay normal in O even in a
+// row whose scores all sit at -cap, and finite in one over 2^17 keys at +cap.
+constexpr float kFixedCap = 73.f;
+constexpr float kFixedRef = 8.f;
 
 // Columns of a row's scores handled at once.
 constexpr int kChunkCols = 64;
@@ -523,7 +525,7 @@ struct RowMask {
   int prefix;
   float slope;  // distance slope * log2(e)
   bool biased;
-  bool fixed;   // weights 2^y without a reference
+  bool fixed;   // the reference stays (kFixedCap)
 };
 
 // A pair of values in registers.
@@ -584,7 +586,7 @@ __device__ __forceinline__ void masked_step(uint32_t tm_s, int key0, const RowMa
       for (int e = 0; e < W; ++e) r[e] = __float_as_uint(capped_score(__uint_as_float(r[e]), mods));
     } else {
 #pragma unroll
-      for (int e = 0; e < W; e += 16) capped_near<8>(r + e, mods);
+      for (int e = 0; e < W; e += 16) capped_near<8>(r + e, mods, 0.f);
     }
   };
   // Calls f(r, c) on the chunks in order.
@@ -653,11 +655,11 @@ __device__ __forceinline__ void masked_step(uint32_t tm_s, int key0, const RowMa
   // Pass 2: the weights.
   const float m = m_ref, mul = modified ? 1.f : sl2;
   float2 sum[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-  auto weights = [&](uint32_t* r, uint32_t* pk, int n) {
+  auto weights = [&](uint32_t* r, uint32_t* pk, int n, bool relative) {  // relative: to m already
 #pragma unroll
     for (int e = 0; e < n; e += 2) {
       float2 x = pair_of(r[e], r[e + 1]);
-      if constexpr (!FIXED) x = __ffma2_rn(x, make_float2(mul, mul), make_float2(-m, -m));
+      if (!relative) x = __ffma2_rn(x, make_float2(mul, mul), make_float2(-m, -m));
       const float p0 = fast_exp2(x.x);  // 0 for the masked keys
       const float p1 = fast_exp2(x.y);
       pk[e / 2] = KV8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
@@ -671,15 +673,15 @@ __device__ __forceinline__ void masked_step(uint32_t tm_s, int key0, const RowMa
       // they use different pipes (327 -> 292 us on four long chunks with a cap).
 #pragma unroll
       for (int e = 0; e < W; e += 16) {
-        capped_near<8>(r + e, mods);
-        weights(r + e, pk + e / 2, 16);
+        capped_near<8>(r + e, mods, m);
+        weights(r + e, pk + e / 2, 16, true);
       }
     } else {
       if constexpr (FIXED) {
         cap(r);
         mask(r, c);
       }
-      weights(r, pk, W);
+      weights(r, pk, W, false);
     }
 #pragma unroll
     for (int w = 0; w < W / 2; w += 16) tmem_st16_async(tm_s + W / 2 * c + w, pk + w);
@@ -1307,10 +1309,10 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
             rm.start = min(max(0, __ldg(a.mods.key_starts + sg.q0 + sg.row0 + i_row)), rm.pos + 1);
           rm.biased = a.mods.slopes != nullptr;
           if (rm.biased) rm.slope = kLog2e * __ldg(a.mods.slopes + head);
-          // Capped scores lie within +-cap log2(e): with bf16 weights (fp32's
-          // range) 0 will do as the reference, and no maximum is needed.
+          // Capped scores lie within +-cap log2(e): bf16 weights (fp32's range)
+          // need no maximum.
           rm.fixed = MOD == kModsCap && !KV8 && !rm.biased && a.mods.cap_log2 <= kFixedCap;
-          if (rm.fixed) m_ref = 0.f;
+          if (rm.fixed) m_ref = kFixedRef;
         }
         for (int k = 0; k < n && ok; ++k) {
           const int key0 = (MOD ? vis.tile(sg.j0 + k) : sg.j0 + k) * C::BN;

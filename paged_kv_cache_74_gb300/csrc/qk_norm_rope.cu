@@ -163,7 +163,7 @@ qk_norm_rope_append_kernel(const NormRopeArgs a) {
         cp_async_16(smem_u32(&mine[k][1][lane]), src + c1, 16);
       }
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
+    cp_async_commit();
   };
 #pragma unroll
   for (int k = 0; k < kRopeDepth - 1; ++k) fetch(part + k * a.warps_per_token, k);  // not tied to the request
@@ -172,7 +172,10 @@ qk_norm_rope_append_kernel(const NormRopeArgs a) {
     record_error(a.status, PA_DEV_BAD_QUERY_LEN, a.num_seqs - 1, a.query_start_loc[a.num_seqs]);
   const TokenRequest req = request_of_token(a.query_start_loc, a.seq_lens, a.num_seqs, token, lane);
   const int r = req.r, seq_len = req.seq_len;
-  if (r < 0) return;  // a row behind the last request: left as it is
+  if (r < 0) {  // a row behind the last request: left as it is
+    cp_async_wait_all();
+    return;
+  }
   const int64_t pos = static_cast<int64_t>(seq_len) - req.q1 + token;
   const int64_t rpos = a.positions != nullptr ? a.positions[token] : pos;
   int64_t slot = -1;
@@ -195,7 +198,10 @@ qk_norm_rope_append_kernel(const NormRopeArgs a) {
     slot = -1;
   }
   if (a.slot_mapping != nullptr && lane == 0 && part == 0) a.slot_mapping[token] = slot;
-  if (!in_table) return;
+  if (!in_table) {
+    cp_async_wait_all();  // no copy outlives the CTA
+    return;
+  }
 
   // cos and sin of this lane's pairs: pair e of the half-split form is
   // (chunk 0 value e, chunk 1 value e); interleaved, pairs 0-3 are in chunk 0
@@ -217,7 +223,7 @@ qk_norm_rope_append_kernel(const NormRopeArgs a) {
 
   int slot_k = 0;
   for (int p = part; p < passes; p += a.warps_per_token) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kRopeDepth - 2) : "memory");
+    cp_async_wait<kRopeDepth - 2>();
     const uint4 x0 = mine[slot_k][0][lane], x1 = mine[slot_k][1][lane];
     fetch(p + (kRopeDepth - 1) * a.warps_per_token, (slot_k + kRopeDepth - 1) % kRopeDepth);
     slot_k = (slot_k + 1) % kRopeDepth;

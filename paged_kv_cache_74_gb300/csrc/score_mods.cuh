@@ -38,11 +38,12 @@ __device__ __forceinline__ float capped_score(float x, const ScoreMods& m) {
   return m.cap_log2 * (t2 < kCapNear * kCapNear ? t * q : far);
 }
 
-// The same for N pairs of scores with |t| <= kCapNear, in place, by packed fused
-// multiply-adds (cap_log2 folded into the coefficients); the pairs go through
-// the polynomial side by side, so that none waits for its own last step.
+// The same for N pairs of scores with |t| <= kCapNear, in place and less `ref`, by
+// packed fused multiply-adds (cap_log2 folded into the coefficients); the pairs
+// go through the polynomial side by side, so that none waits for its own last
+// step.
 template <int N>
-__device__ __forceinline__ void capped_near(uint32_t* r, const ScoreMods& m) {
+__device__ __forceinline__ void capped_near(uint32_t* r, const ScoreMods& m, float ref) {
   auto both = [](float c) { return make_float2(c, c); };
   const float qs[5] = {kTanhQ0 * m.cap_log2, kTanhQ1 * m.cap_log2, kTanhQ2 * m.cap_log2,
                        kTanhQ3 * m.cap_log2, kTanhQ4 * m.cap_log2};
@@ -60,7 +61,7 @@ __device__ __forceinline__ void capped_near(uint32_t* r, const ScoreMods& m) {
     for (int i = 0; i < N; ++i) q[i] = __ffma2_rn(t2[i], q[i], both(qs[k]));
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    q[i] = __fmul2_rn(t[i], q[i]);
+    q[i] = __ffma2_rn(t[i], q[i], both(-ref));
     r[2 * i] = __float_as_uint(q[i].x);
     r[2 * i + 1] = __float_as_uint(q[i].y);
   }

@@ -160,6 +160,17 @@ def test_steep_and_negative_slopes(cuda_lib):
     assert_within(b.run(cuda_lib, **m), *b.ref(**m))
 
 
+@pytest.mark.parametrize("hq", [4, 16])
+@pytest.mark.parametrize("cap", [0.0, 30.0, 300.0])
+@pytest.mark.parametrize("power", [60, -60])
+def test_range_of_the_values(cuda_lib, hq, cap, power):
+    """V times a power of two gives the output times it, bit for bit."""
+    b = Batch([200, 31, 1000], hq, 2, 128, qmul=40.0)
+    want = b.run(cuda_lib, softcap=cap)
+    b.vc *= 2.0 ** power
+    assert torch.equal(b.run(cuda_lib, softcap=cap), want * 2.0 ** power)
+
+
 def test_long_context_window(cuda_lib):
     b = Batch([32768, 30001, 5], 8, 2, 128)
     starts = torch.tensor([32768 - 4096, 29999, 0], dtype=torch.int32, device="cuda")

@@ -219,6 +219,21 @@ def test_steep_and_negative_slopes(cuda_lib):
     b.check(cuda_lib, slopes=torch.tensor([50.0, 1.0, 0.0, 1e-3, -1e-2, 0.3, -0.5, 7.0], device="cuda"))
 
 
+@pytest.mark.parametrize("cap,power", [(cap, power) for cap in (0.0, 5.0, 30.0, 55.0, 56.0) for power in (60, -60)] +
+                         [(50.0, 45), (50.0, -45)])
+def test_range_of_the_values(cuda_lib, cap, power):
+    """V times a power of two gives the output times it, bit for bit: no weight
+    or sum leaves the range on the way (rows whose scores all sit at -cap too)."""
+    b = Batch([(200, 31), (130, 500)], 4, 2, 128, qmul=40.0)
+    b.q[5] = 100.0
+    b.kc[b.t.block_tables[0].long()] = b.kc[b.t.block_tables[0].long()].abs()
+    b.q[6] = -100.0
+    want = b.run(cuda_lib, softcap=cap)
+    assert_within(want, *b.ref(softcap=cap))
+    b.vc *= 2.0 ** power
+    assert torch.equal(b.run(cuda_lib, softcap=cap), want * 2.0 ** power)
+
+
 def test_many_requests(cuda_lib):
     """More requests than the plan's threads, most of them chunks."""
     rng = np.random.default_rng(3)
