@@ -68,9 +68,14 @@ constexpr float kSlackTc = 8.0f;  // log2 units
 constexpr int kEndSeg = 7;        // segment record kind: no more work
 
 // MOD: modified scores (ScoreMods, TileSpan).  The chunks hold the request's
-// tiles with a visible key, 8 by 8 in order; the chunk records also say which
-// token each MMA row is and whether the request's row sees it.
-template <int D, int GM, bool KV8 = false, bool MOD = false>
+// tiles with a visible key, 8 by 8 in order; the softmax and converter threads
+// work out from the segment's TcVis which token their MMA row is and whether the
+// request's row sees it.  Over e4m3 caches the kernel is bound by the arrival of
+// its roles' instructions (2.4 of 13 stall cycles per issue): the converter's
+// loops are rolled over 64 values of head_dim at a time, which took 200 requests
+// with 8 q heads per kv head from 382 to 348 us with a cap, from 346 to 313
+// without, and the plain form from 271 to 268.
+template <int D, int GM, bool KV8 = false, int MOD = kNoMods>
 struct TcCfg {
   static constexpr int HALVES = D / 64;             // 128-byte column chunks of head_dim
   static constexpr int CB = 8;                      // blocks per chunk
@@ -101,13 +106,12 @@ struct TcCfg {
   static constexpr int OFF_RED = OFF_SEG + SLOTS * SEG_BYTES;  // [2][4][GM] max keys
   static constexpr int OFF_ML = OFF_RED + 2 * 4 * GM * 4;       // [SLOTS][5][GM]: m, 4 partial l
   static constexpr int NREC = 2 * NST;              // chunk records (K producer -> V producer)
-  static constexpr int OFF_REC = OFF_ML + SLOTS * 5 * GM * 4;  // [NREC][RECI] ints
-  // 12 ints; MOD: also 4 words of visible tokens and the 8 tiles' numbers.
-  static constexpr int RECI = MOD ? 24 : 12;
-  static constexpr int OFF_BAR = OFF_REC + NREC * RECI * 4;
+  static constexpr int OFF_REC = OFF_ML + SLOTS * 5 * GM * 4;  // [NREC][12] ints
+  static constexpr int OFF_BAR = OFF_REC + NREC * 48;
   static constexpr int NBAR = 4 * NST + 3 * SLOTS + 2 * 6 + 2 + NREC + 2 * NCK + 2 * NCV + SLOTS;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
-  static constexpr int SMEM = OFF_MISC + 64 + 1024;  // + 1024-byte alignment slack
+  static constexpr int OFF_VIS = OFF_MISC + 64;      // MOD: [SLOTS] TcVis
+  static constexpr int SMEM = OFF_VIS + (MOD ? SLOTS * 32 : 0) + 1024;  // + 1024-byte alignment slack
   static constexpr int THREADS = (KV8 ? 15 : 11) * 32;  // + 4 converter warps for e4m3
   // TMEM: S0 0, S1 16, O0 32, O1 48; e4m3: converted K chunks from KCOL.
   static constexpr uint32_t KCOL = 64;
@@ -165,6 +169,22 @@ struct TcSeg {
 };
 static_assert(sizeof(TcSeg) <= 48, "segment record");
 
+// MOD: what the segment's row sees, and which tiles its chunks hold.
+struct TcVis {
+  int len, prefix, start, n1;
+  int gap, b0, pad[2];
+  // The token of MMA row tl of the segment's chunk c, and whether the row sees
+  // it (`blocks`: of the chunk; the empty segment has prefix 0 and start len).
+  __device__ __forceinline__ int token(int c, int tl) const {
+    const int t = b0 + 8 * c + (tl >> 4);
+    return (t < n1 ? t : t + gap) * kBlockSize + (tl & 15);
+  }
+  __device__ __forceinline__ bool sees(int c, int tl, int blocks) const {
+    return (tl >> 4) < blocks && sees_key(token(c, tl), len, make_int2(prefix, start));
+  }
+};
+static_assert(sizeof(TcVis) == 32, "two 16-byte words");
+
 // The batch's chunks are split over the CTAs by cost, not by count: every
 // chunk costs kCostChunk and every (request, kv head) segment another
 // kCostSeg.  A segment start (q load, first S before any softmax, partial
@@ -195,7 +215,7 @@ __device__ __forceinline__ uint32_t e8_chunk(int t, int c) {
   return static_cast<uint32_t>(t * D + ((c ^ sw) * 16));
 }
 
-template <int D, int GM, bool KV8, bool MOD = false>
+template <int D, int GM, bool KV8, int MOD = kNoMods>
 __global__ void __launch_bounds__(TcCfg<D, GM, KV8, MOD>::THREADS, 1)
 paged_decode_tc_kernel(const __grid_constant__ CUtensorMap qmap,
                        const __grid_constant__ CUtensorMap kmap,
@@ -231,10 +251,10 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap qmap,
   volatile int* n_v_issued = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 36);
   volatile long long* total_cost = reinterpret_cast<volatile long long*>(smem + C::OFF_MISC + 40);
   volatile int* cost_chunk = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 48);
-  // [NREC][RECI]: V rows of 8 blocks, kv head, blocks, valid tokens (MOD: blocks
-  // to load), first chunk of segment slot + 1; MOD: 12 .. 15 visible tokens (a bit
-  // each), 16 .. 23 the tiles
+  // [NREC][12]: V rows of 8 blocks, kv head, blocks, valid tokens (MOD: blocks to
+  // load), first chunk of segment slot + 1
   int* recs = reinterpret_cast<int*>(smem + C::OFF_REC);
+  TcVis* segvis = reinterpret_cast<TcVis*>(smem + C::OFF_VIS);
 
   if (tid == 0) {
     for (int k = 0; k < B::COUNT; ++k) {
@@ -525,6 +545,16 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap qmap,
           si.c0 = cbase + static_cast<long long>(kvh) * (static_cast<long long>(cu_chunk) * nc + cu_seg) +
                   cu_seg;
           segs[slot] = si;
+          if constexpr (MOD) {
+            TcVis v;
+            v.len = len;
+            v.prefix = span.prefix;
+            v.start = span.start;
+            v.n1 = span.n1;
+            v.gap = span.gap;
+            v.b0 = b;
+            segvis[slot] = v;
+          }
           mbar_arrive_expect_tx(bar(B::QFULL + slot), a.group * D * 2);
 #pragma unroll
           for (int h = 0; h < C::HALVES; ++h)
@@ -572,19 +602,8 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap qmap,
             ok = false;
             break;
           }
-          int* rec = recs + (chunk % C::NREC) * C::RECI;
+          int* rec = recs + (chunk % C::NREC) * 12;
           if (lane < C::CB) rec[lane] = vrow;
-          if constexpr (MOD) {
-            // The 16 tokens of this lane's tile that the row sees.
-            auto low = [](int n) -> uint32_t { return n <= 0 ? 0u : (n >= 16 ? 0xffffu : (1u << n) - 1u); };
-            const int t0 = tile * kBlockSize;
-            const uint32_t seen =
-                lane < nld ? low(len - t0) & (low(span.prefix - t0) | ~low(span.start - t0)) : 0u;
-            const uint32_t s_lo = __shfl_sync(0xffffffffu, seen, (2 * lane) & 31);
-            const uint32_t s_hi = __shfl_sync(0xffffffffu, seen, (2 * lane + 1) & 31);
-            if (lane < 4) rec[12 + lane] = static_cast<int>(s_lo | (s_hi << 16));
-            if (lane < C::CB) rec[16 + lane] = tile;
-          }
           if (lane == 0) {
             rec[8] = kvh;
             rec[9] = nbc;
@@ -655,7 +674,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap qmap,
         !lane0_wait(bar(B::KFREE + chunk % C::NST), ((chunk / C::NST) - 1) & 1, 25))
       ok = false;
     if (ok && lane == 0) {
-      recs[(chunk % C::NREC) * C::RECI + 9] = 0;
+      recs[(chunk % C::NREC) * 12 + 9] = 0;
       mbar_arrive(bar(B::CREC + chunk % C::NREC));
     }
     // End record (no q load: a plain arrive completes the phase).
@@ -684,7 +703,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap qmap,
     for (int i = 0; ok; ++i) {
       const int rs = i % C::NREC;
       if (!(ok = warp_wait(bar(B::CREC + rs), (i / C::NREC) & 1, 24))) break;
-      const int* rec = recs + rs * C::RECI;
+      const int* rec = recs + rs * 12;
       const int nbc = rec[9];
       if (nbc == 0) break;
       const int kvh = rec[8];
@@ -840,14 +859,13 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap qmap,
       if (si.kind == kEndSeg) break;
       const int nch = (si.nseg + C::CB - 1) / C::CB;
       const int ob = seg & 1;
+      TcVis vis{};
+      if constexpr (MOD) vis = segvis[slot];
       float m_ref[GM], l_run[GM];
-      float slope[MOD ? GM : 1];  // distance slopes of the segment's heads (log2 units)
 #pragma unroll
       for (int h = 0; h < GM; ++h) {
         m_ref[h] = kNegBigTc;
         l_run[h] = 0.f;
-        if constexpr (MOD)
-          slope[h] = a.mods.slopes != nullptr && h < G ? __ldg(a.mods.slopes + si.kvh * G + h) * kLog2e : 0.f;
       }
       for (int c = 0; c < nch; ++c, ++j) {
         const int sb = j & 1;
@@ -864,18 +882,25 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap qmap,
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(B::SFREE + sb));
         if constexpr (MOD) {
-          // This row's token, whether it is seen, its scores in log2 units.  (The
-          // record of chunk j is written again for chunk j + 2 NST, once the S
-          // MMA of chunk j + NST is done, or over e4m3 caches its conversion, which
-          // follows that of V of chunk j + NST - 2 and so P.V(j + NST - 4): both
-          // come after every softmax warp has read this one.)
-          const volatile int* rec = recs + (j % C::NREC) * C::RECI;
-          valid = static_cast<uint32_t>(rec[12 + q4]) >> lane & 1u;
-          const float d = static_cast<float>(rec[16 + (tl >> 4)] * kBlockSize + (tl & 15) - (si.seq_len - 1));
-          const bool capped = a.mods.cap_log2 > 0.f;
+          // Whether this row's token is seen, its scores in log2 units.
+          valid = vis.sees(c, tl, nbc);
+          if constexpr (MOD == kModsCap) {
+            if (any_far<GM>(s, a.mods)) {
 #pragma unroll
-          for (int h = 0; h < GM; ++h)
-            s[h] = fmaf(slope[h], d, capped ? capped_score(s[h], a.mods) : s[h] * sl2);
+              for (int h = 0; h < GM; ++h) s[h] = capped_score(s[h], a.mods);
+            } else {
+              capped_near<GM / 2>(s, a.mods, 0.f);
+            }
+          } else {
+#pragma unroll
+            for (int h = 0; h < GM; ++h) s[h] *= sl2;
+          }
+          if (a.mods.slopes != nullptr) {
+            const float d = static_cast<float>(vis.token(c, tl) - (si.seq_len - 1));
+#pragma unroll
+            for (int h = 0; h < GM; ++h)
+              if (h < G) s[h] = fmaf(__ldg(a.mods.slopes + si.kvh * G + h) * kLog2e, d, s[h]);
+          }
         }
         // Chunk maximum of every head: one redux per warp, then across warps.
         int* rk = red_key + (j & 1) * 4 * GM;
@@ -1097,6 +1122,8 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap qmap,
     };
     bool ok = true;
     int seg = 0;
+    TcVis vis{};    // MOD: of the chunk's segment, and the chunk's number in it
+    int chunk = 0;
     int prev_ntok = 0;  // valid tokens of chunk i - 1 (its V is converted after K of chunk i)
                         // (MOD: not zero if this thread's token is seen)
     // Chunk i's K is converted before chunk i - 1's V, so that an S MMA never
@@ -1104,10 +1131,14 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap qmap,
     for (int i = 0; ok; ++i) {
       const int rs = i % C::NREC;
       if (!(ok = all_wait(B::CREC + rs, (i / C::NREC) & 1, 90))) break;
-      const int* rec = recs + rs * C::RECI;
+      const int* rec = recs + rs * 12;
       const int nbc = rec[9];
-      const int ntok = MOD ? rec[12 + q4] >> lane & 1 : rec[10];
       const int first = rec[11];
+      if constexpr (MOD) {
+        if (nbc > 0 && first) vis = segvis[first - 1];
+        chunk = first ? 0 : chunk + 1;
+      }
+      const int ntok = MOD ? (vis.sees(chunk, tl, nbc) ? 1 : 0) : rec[10];
       if (nbc > 0) {
         const int st = i % C::NST, ck = i % C::NCK;
         if (first) {
@@ -1127,7 +1158,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap qmap,
         if (!(ok = all_wait(B::KFULL + st, (i / C::NST) & 1, 92))) break;
         if (i >= C::NCK && !(ok = all_wait(B::KCFREE + ck, ((i / C::NCK) - 1) & 1, 93))) break;
         const uint32_t krow = k_s + st * C::RSTAGE + (tl >> 4) * C::BLK8;
-#pragma unroll
+#pragma unroll 1
         for (int h = 0; h < C::HALVES; ++h) {
           uint32_t kw[32];  // head_dim 64 h .. 64 h + 63 as 32 f16 pairs
 #pragma unroll
@@ -1161,18 +1192,24 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap qmap,
         const uint32_t vdst = vc_s + cv * C::STAGE + (tl >> 4) * C::BLK + ((tl >> 3) & 1) * C::GSTRIDE +
                               (tl & 7) * 128;
         const bool valid = MOD ? prev_ntok != 0 : tl < prev_ntok;
+#pragma unroll 1
+        for (int g = 0; g < D / 64; ++g) {
+          uint4 w[4];
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-          uint4 w = make_uint4(0u, 0u, 0u, 0u);
-          if (valid) w = ld_shared_v4(vrow + e8_chunk<D>(tl & 15, c));
-          // dims 16 c .. 16 c + 15: 16-byte units 2 (c % 4) and + 1 of head_dim half c / 4
-          const uint4 lo = make_uint4(e4m3x2_to_f16x2(w.x), e4m3x2_to_f16x2(w.x >> 16),
-                                      e4m3x2_to_f16x2(w.y), e4m3x2_to_f16x2(w.y >> 16));
-          const uint4 hi = make_uint4(e4m3x2_to_f16x2(w.z), e4m3x2_to_f16x2(w.z >> 16),
-                                      e4m3x2_to_f16x2(w.w), e4m3x2_to_f16x2(w.w >> 16));
-          const int u = 2 * (c & 3);
-          st_shared_v4(vdst + (c >> 2) * 1024 + ((u ^ (tl & 7)) * 16), lo);
-          st_shared_v4(vdst + (c >> 2) * 1024 + (((u + 1) ^ (tl & 7)) * 16), hi);
+          for (int k = 0; k < 4; ++k) {
+            w[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (valid) w[k] = ld_shared_v4(vrow + e8_chunk<D>(tl & 15, 4 * g + k));
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            // dims 64 g + 16 k .. + 15: 16-byte units 2 k and + 1 of head_dim half g
+            const uint4 lo = make_uint4(e4m3x2_to_f16x2(w[k].x), e4m3x2_to_f16x2(w[k].x >> 16),
+                                        e4m3x2_to_f16x2(w[k].y), e4m3x2_to_f16x2(w[k].y >> 16));
+            const uint4 hi = make_uint4(e4m3x2_to_f16x2(w[k].z), e4m3x2_to_f16x2(w[k].z >> 16),
+                                        e4m3x2_to_f16x2(w[k].w), e4m3x2_to_f16x2(w[k].w >> 16));
+            st_shared_v4(vdst + g * 1024 + (((2 * k) ^ (tl & 7)) * 16), lo);
+            st_shared_v4(vdst + g * 1024 + (((2 * k + 1) ^ (tl & 7)) * 16), hi);
+          }
         }
         fence_proxy_async_smem();  // read by the tensor core
         __syncwarp();
@@ -1213,7 +1250,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap qmap,
   if (a.defer_griddep && tid == 0) griddep_wait();
 }
 
-template <int D, int GM, bool KV8, bool MOD = false>
+template <int D, int GM, bool KV8, int MOD = kNoMods>
 cudaError_t launch_decode_tc_impl(const DecodeArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
                                   const CUtensorMap& vmap, cudaStream_t stream) {
   using C = TcCfg<D, GM, KV8, MOD>;

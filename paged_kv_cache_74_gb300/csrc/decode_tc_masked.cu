@@ -8,8 +8,13 @@ namespace {
 template <int D, bool KV8>
 cudaError_t launch_group(const DecodeArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
                          const CUtensorMap& vmap, cudaStream_t stream) {
-  if (a.group <= 8) return launch_decode_tc_impl<D, 8, KV8, true>(a, qmap, kmap, vmap, stream);
-  if (a.group <= 16) return launch_decode_tc_impl<D, 16, KV8, true>(a, qmap, kmap, vmap, stream);
+  const bool cap = a.mods.cap_log2 > 0.f;
+  if (a.group <= 8)
+    return cap ? launch_decode_tc_impl<D, 8, KV8, kModsCap>(a, qmap, kmap, vmap, stream)
+               : launch_decode_tc_impl<D, 8, KV8, kMods>(a, qmap, kmap, vmap, stream);
+  if (a.group <= 16)
+    return cap ? launch_decode_tc_impl<D, 16, KV8, kModsCap>(a, qmap, kmap, vmap, stream)
+               : launch_decode_tc_impl<D, 16, KV8, kMods>(a, qmap, kmap, vmap, stream);
   return cudaErrorInvalidValue;
 }
 

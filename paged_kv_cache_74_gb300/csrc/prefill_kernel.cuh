@@ -75,13 +75,8 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&b);
 }
 
-// Modified scores (ScoreMods; kNoMods: plain causal attention).  The units come
-// from a plan (plan_prefill_kernel): which keys some row of a query tile sees
-// cannot be summed in closed form.  kCap: with a tanh cap.
-constexpr int kNoMods = 0;
-constexpr int kMods = 1;
-constexpr int kModsCap = 2;
-
+// Modified scores: the units come from a plan (plan_prefill_kernel), for which
+// keys some row of a query tile sees cannot be summed in closed form.
 template <int D>
 struct PrefillCfg {
   static constexpr int BM = 128;                    // query rows per unit

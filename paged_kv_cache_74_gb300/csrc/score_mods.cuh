@@ -14,6 +14,11 @@
 namespace pa {
 namespace {
 
+// Which scores an instantiation computes: plain ones, modified, or also capped.
+constexpr int kNoMods = 0;
+constexpr int kMods = 1;
+constexpr int kModsCap = 2;
+
 constexpr float kLog2e = 1.4426950408889634f;
 
 // tanh(t) / t for |t| <= kCapNear as a polynomial in t^2, minimax in the relative
@@ -38,19 +43,25 @@ __device__ __forceinline__ float capped_score(float x, const ScoreMods& m) {
   return m.cap_log2 * (t2 < kCapNear * kCapNear ? t * q : far);
 }
 
+// Scores as floats or as their bits (as TMEM loads leave them).
+__device__ __forceinline__ float as_float(uint32_t x) { return __uint_as_float(x); }
+__device__ __forceinline__ float as_float(float x) { return x; }
+__device__ __forceinline__ void put_float(uint32_t& x, float v) { x = __float_as_uint(v); }
+__device__ __forceinline__ void put_float(float& x, float v) { x = v; }
+
 // The same for N pairs of scores with |t| <= kCapNear, in place and less `ref`, by
 // packed fused multiply-adds (cap_log2 folded into the coefficients); the pairs
 // go through the polynomial side by side, so that none waits for its own last
 // step.
-template <int N>
-__device__ __forceinline__ void capped_near(uint32_t* r, const ScoreMods& m, float ref) {
+template <int N, typename T>
+__device__ __forceinline__ void capped_near(T* r, const ScoreMods& m, float ref) {
   auto both = [](float c) { return make_float2(c, c); };
   const float qs[5] = {kTanhQ0 * m.cap_log2, kTanhQ1 * m.cap_log2, kTanhQ2 * m.cap_log2,
                        kTanhQ3 * m.cap_log2, kTanhQ4 * m.cap_log2};
   float2 t[N], t2[N], q[N];
 #pragma unroll
   for (int i = 0; i < N; ++i)
-    t[i] = __fmul2_rn(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), both(m.cap_in));
+    t[i] = __fmul2_rn(make_float2(as_float(r[2 * i]), as_float(r[2 * i + 1])), both(m.cap_in));
 #pragma unroll
   for (int i = 0; i < N; ++i) t2[i] = __fmul2_rn(t[i], t[i]);
 #pragma unroll
@@ -62,18 +73,18 @@ __device__ __forceinline__ void capped_near(uint32_t* r, const ScoreMods& m, flo
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     q[i] = __ffma2_rn(t[i], q[i], both(-ref));
-    r[2 * i] = __float_as_uint(q[i].x);
-    r[2 * i + 1] = __float_as_uint(q[i].y);
+    put_float(r[2 * i], q[i].x);
+    put_float(r[2 * i + 1], q[i].y);
   }
 }
 
 // Whether some lane of the warp holds a score beyond kCapNear among its N.
-template <int N>
-__device__ __forceinline__ bool any_far(const uint32_t* r, const ScoreMods& m) {
+template <int N, typename T>
+__device__ __forceinline__ bool any_far(const T* r, const ScoreMods& m) {
   float top[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int e = 0; e < N; e += 2)
-    top[(e / 2) % 4] = fmax3(top[(e / 2) % 4], fabsf(__uint_as_float(r[e])), fabsf(__uint_as_float(r[e + 1])));
+    top[(e / 2) % 4] = fmax3(top[(e / 2) % 4], fabsf(as_float(r[e])), fabsf(as_float(r[e + 1])));
   return __any_sync(0xffffffffu, fmaxf(fmax3(top[0], top[1], top[2]), top[3]) * m.cap_in > kCapNear);
 }
 
