@@ -574,14 +574,14 @@ __device__ __forceinline__ void masked_step(uint32_t tm_s, int key0, const RowMa
       }
     }
   };
-  // The scores capped, in log2 units.
-  auto cap = [&](uint32_t (&r)[W]) {
+  // The scores capped, in log2 units and less ref.
+  auto cap = [&](uint32_t (&r)[W], float ref) {
     if (any_far<W>(r, mods)) {
 #pragma unroll
-      for (int e = 0; e < W; ++e) r[e] = __float_as_uint(capped_score(__uint_as_float(r[e]), mods));
+      for (int e = 0; e < W; ++e) r[e] = __float_as_uint(capped_score(__uint_as_float(r[e]), mods, ref));
     } else {
 #pragma unroll
-      for (int e = 0; e < W; e += 16) capped_near<8>(r + e, mods, 0.f);
+      for (int e = 0; e < W; e += 16) capped_near<8>(r + e, mods, ref);
     }
   };
   // Calls f(r, c) on the chunks in order.
@@ -605,7 +605,7 @@ __device__ __forceinline__ void masked_step(uint32_t tm_s, int key0, const RowMa
   if constexpr (!FIXED) {
     float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
     walk([&](uint32_t (&r)[W], int c) {
-      if constexpr (MOD == kModsCap) cap(r);
+      if constexpr (MOD == kModsCap) cap(r, 0.f);
       if (rm.biased) {
         const float s = MOD == kModsCap ? 1.f : sl2;
         const float d0 = static_cast<float>(key0 + W * c - rm.pos);
@@ -673,10 +673,10 @@ __device__ __forceinline__ void masked_step(uint32_t tm_s, int key0, const RowMa
       }
     } else {
       if constexpr (FIXED) {
-        cap(r);
+        cap(r, m);
         mask(r, c);
       }
-      weights(r, pk, W, false);
+      weights(r, pk, W, FIXED);
     }
 #pragma unroll
     for (int w = 0; w < W / 2; w += 16) tmem_st16_async(tm_s + W / 2 * c + w, pk + w);

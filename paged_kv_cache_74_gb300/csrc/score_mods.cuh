@@ -28,19 +28,20 @@ constexpr float kCapNear = 0.75f;
 constexpr float kTanhQ0 = 0.99999946f, kTanhQ1 = -0.33328253f, kTanhQ2 = 0.13258983f,
                 kTanhQ3 = -0.050056305f, kTanhQ4 = 0.012929632f;
 
-// cap log2(e) tanh(t), t = x cap_in, for any x: the polynomial near 0, the
-// quotient beyond (2e-7 absolute).  The hardware's tanh approximation is off by
-// 2^-11 of the score: a capped score of 30 would shift its weight by 1.5 %.
-__device__ __forceinline__ float capped_score(float x, const ScoreMods& m) {
+// cap log2(e) tanh(t) - ref, t = x cap_in, for any x: the polynomial near 0 (its
+// coefficients times cap_log2), the quotient beyond (2e-7 absolute).  The
+// hardware's tanh approximation is off by 2^-11 of the score: a capped score of
+// 30 would shift its weight by 1.5 %.
+__device__ __forceinline__ float capped_score(float x, const ScoreMods& m, float ref = 0.f) {
   const float t = x * m.cap_in;
   const float t2 = t * t;
-  float q = fmaf(t2, kTanhQ4, kTanhQ3);
-  q = fmaf(t2, q, kTanhQ2);
-  q = fmaf(t2, q, kTanhQ1);
-  q = fmaf(t2, q, kTanhQ0);
+  float q = fmaf(t2, kTanhQ4 * m.cap_log2, kTanhQ3 * m.cap_log2);
+  q = fmaf(t2, q, kTanhQ2 * m.cap_log2);
+  q = fmaf(t2, q, kTanhQ1 * m.cap_log2);
+  q = fmaf(t2, q, kTanhQ0 * m.cap_log2);
   const float e = fast_exp2(t * (2.f * kLog2e));  // 0 and infinity at the ends are fine
   const float far = fmaf(-2.f, fast_rcp(1.f + e), 1.f);
-  return m.cap_log2 * (t2 < kCapNear * kCapNear ? t * q : far);
+  return t2 <= kCapNear * kCapNear ? fmaf(t, q, -ref) : fmaf(m.cap_log2, far, -ref);
 }
 
 // Scores as floats or as their bits (as TMEM loads leave them).
@@ -50,9 +51,10 @@ __device__ __forceinline__ void put_float(uint32_t& x, float v) { x = __float_as
 __device__ __forceinline__ void put_float(float& x, float v) { x = v; }
 
 // The same for N pairs of scores with |t| <= kCapNear, in place and less `ref`, by
-// packed fused multiply-adds (cap_log2 folded into the coefficients); the pairs
-// go through the polynomial side by side, so that none waits for its own last
-// step.
+// packed fused multiply-adds, bit for bit what capped_score gives (so that it
+// does not matter to a score which of the two its neighbours call for); the
+// pairs go through the polynomial side by side, so that none waits for its own
+// last step.
 template <int N, typename T>
 __device__ __forceinline__ void capped_near(T* r, const ScoreMods& m, float ref) {
   auto both = [](float c) { return make_float2(c, c); };
@@ -78,14 +80,16 @@ __device__ __forceinline__ void capped_near(T* r, const ScoreMods& m, float ref)
   }
 }
 
-// Whether some lane of the warp holds a score beyond kCapNear among its N.
+// Whether some lane of the warp holds a score beyond kCapNear among its N (squared
+// as capped_score squares it).
 template <int N, typename T>
 __device__ __forceinline__ bool any_far(const T* r, const ScoreMods& m) {
   float top[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int e = 0; e < N; e += 2)
     top[(e / 2) % 4] = fmax3(top[(e / 2) % 4], fabsf(as_float(r[e])), fabsf(as_float(r[e + 1])));
-  return __any_sync(0xffffffffu, fmaxf(fmax3(top[0], top[1], top[2]), top[3]) * m.cap_in > kCapNear);
+  const float t = fmaxf(fmax3(top[0], top[1], top[2]), top[3]) * m.cap_in;
+  return __any_sync(0xffffffffu, t * t > kCapNear * kCapNear);
 }
 
 // The 16-token tiles of a request that hold a key its (single) row sees:

@@ -10,7 +10,12 @@ A score error delta moves the weights by factors within e^(+-2 delta), the
 output by 2.1 delta (sum w |v| + |O|) while delta < 0.02:
   delta = 2^-17 scale max_j |q| . |k_j|     (128 fp32 additions of the products)
         + 2^-19 max |s|                      (scale, cap and bias in fp32: a few roundings; tanh 7e-7)
-        + 2^-22                              (the exponential's own error)."""
+        + 2^-22                              (the exponential's own error).
+f16 numbers below 2^-14 are multiples of 2^-24: over e4m3 caches a small weight is
+off by up to 2^-25 instead, relative to a sum of weights that is at least 1 (the
+reference is the maximum of some earlier tile, which weighs 1 there), so the
+output by 2^-25 sum |v| over the seen keys; a small q by 2^-25, the score by
+2^-25 scale sum_i |k_ij|."""
 import math
 
 import numpy as np
@@ -55,9 +60,13 @@ def attend(q, k, v, pos, scale, softcap=0.0, slopes=None, starts=None, prefix=0,
         size = w @ vh.abs() + o.abs()
         top = s.amax(1, keepdim=True).abs().masked_fill(none, 0.0)
         delta = 2.0 ** -17 * mag + 2.0 ** -19 * top + 2.0 ** -22
+        small = 0.0
+        if u == 2.0 ** -11:
+            delta = delta + 2.0 ** -25 * scale * kh.abs().sum(1)[None, :].masked_fill(~seen, 0).amax(1, keepdim=True)
+            small = 2.0 ** -25 * (seen.double() @ vh.abs())
         assert float(delta.max()) < 0.02
         out[:, h] = o
-        tol[:, h] = 2.0 ** -8 * o.abs() + (1.01 * u + 2.1 * delta) * size
+        tol[:, h] = 2.0 ** -8 * o.abs() + (1.01 * u + 2.1 * delta) * size + small
     return out, tol
 
 

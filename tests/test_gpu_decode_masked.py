@@ -279,3 +279,18 @@ def test_refusals(cuda_lib):
             b.run(pa, **bad)
     with pytest.raises(ValueError):
         pa.decode_masked_fp8(b.q, b.kc, b.vc, b.t.block_tables, b.t.seq_lens, 333, b.scale, 1.0, 1.0)
+
+
+@pytest.mark.parametrize("hq,fp8", [(16, False), (16, True), (8, True), (10, False)])
+def test_result_does_not_depend_on_what_ran_before(cuda_lib, hq, fp8):
+    """Bit for bit the same after calls that leave other keys in shared memory,
+    with scores within and beyond the cap's polynomial."""
+    pa = cuda_lib
+    b = Batch([100, 70, 233, 1, 17], hq, 2, 128, fp8=fp8, qmul=20.0)
+    m = b.mods("docs prefix")
+    m["softcap"] = 30.0
+    first = b.run(pa, **m)
+    other = Batch([900, 1200], hq, 2, 128, fp8=fp8, qmul=90.0)
+    for _ in range(6):
+        other.run(pa, softcap=0.5)
+        assert torch.equal(b.run(pa, **m), first)

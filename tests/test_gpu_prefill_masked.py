@@ -353,3 +353,21 @@ def test_refusals(cuda_lib):
                 dict(out=torch.empty_like(b.q[:1])), dict(tables=b.t.block_tables[:1])):
         with pytest.raises(ValueError):
             b.run(pa, **bad)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("cap", [30.0, 80.0])
+def test_result_does_not_depend_on_what_is_not_seen(cuda_lib, fp8, cap):
+    """Bit for bit the same, with scores within and beyond the cap's polynomial,
+    whatever stands in hidden keys, in the cache blocks that earlier calls read
+    and in the query rows behind the batch."""
+    pa = cuda_lib
+    b = Batch([(100, 30), (70, 0), (33, 200)], 8, 2, 128, fp8=fp8, qmul=20.0, num_blocks=200, pad_rows=50)
+    m = b.mods("docs")
+    m["softcap"] = cap
+    first = b.run(pa, **m)
+    other = Batch([(300, 900)], 8, 2, 128, fp8=fp8, qmul=90.0)
+    for k in range(6):
+        other.run(pa, softcap=0.5)  # leaves other keys in shared memory
+        b.q[b.rows:] = (0.0, 1e30, float("inf"), float("nan"), -1e4, 3.0)[k]
+        assert torch.equal(b.run(pa, **m)[:b.rows], first[:b.rows])
