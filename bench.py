@@ -42,24 +42,24 @@ FALLBACK_BF16_TFLOPS = 1900.0
 
 # dram__bytes_read.sum + dram__bytes_write.sum of one launch of the named
 # workload's dominant kernel, from an ncu capture of the full workload; valid
-# only while that kernel's source is unchanged (sha256 prefix of its .cu file
-# when the counters were taken), else reported as null.
+# only while that kernel's source is unchanged (sha256 prefix of its file when
+# the counters were taken), else reported as null.
 PROFILED_TRAFFIC: dict = {
-    # 636.340736 MB read + 3.247616 MB written
-    "llama8b_decode_b64": {"bytes": 639588352, "src": "decode.cu",
-                           "src_sha": "28bbfc5e29ee225b"},
-    # 940.190720 MB read + 5.581824 MB written
-    "prefix_shared_decode_b256": {"bytes": 945772544, "src": "decode_tc.cu",
-                                  "src_sha": "77528aa33e5a5c65"},
-    # prefill rows of the four-chunk batch: 877.759744 MB read + 14.742016 MB written
-    "multi_chunk_prefill": {"bytes": 892501760, "src": "prefill.cu",
-                            "src_sha": "02e57917f8ebd2f1"},
+    # 636.355840 MB read + 3.224832 MB written
+    "llama8b_decode_b64": {"bytes": 639580672, "src": "decode_kernel.cuh",
+                           "src_sha": "984a1ff3459743cf"},
+    # 940.555520 MB read + 5.621248 MB written
+    "prefix_shared_decode_b256": {"bytes": 946176768, "src": "decode_tc_kernel.cuh",
+                                  "src_sha": "44dd168286968ac1"},
+    # prefill rows of the four-chunk batch: 894.937600 MB read + 15.723264 MB written
+    "multi_chunk_prefill": {"bytes": 910660864, "src": "prefill_kernel.cuh",
+                            "src_sha": "4cd172af577355f6"},
 }
 
 
 # ----------------------------------------------------------------- helpers
 
-def decode_src_sha(src: str = "decode.cu") -> str:
+def decode_src_sha(src: str = "decode_kernel.cuh") -> str:
     p = os.path.join(ROOT, "paged_kv_cache_74_gb300", "csrc", src)
     return hashlib.sha256(open(p, "rb").read()).hexdigest()[:16]
 
