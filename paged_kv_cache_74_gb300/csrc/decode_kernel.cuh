@@ -976,7 +976,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
         const int stok = (KV8 && XS) ? xs8_token(srow) : srow;
         if constexpr (MOD) {
           const int tok = tok0 + stok;
-          const float y = a.mods.cap_log2 > 0.f ? capped_score(sacc[i], a.mods) : sacc[i] * a.scale_log2;
+          const float y = a.mods.cap_log2 > 0.f ? capped_alone(sacc[i], a.mods) : sacc[i] * a.scale_log2;
           const bool ok = sees_key(tok, seq_len, vis) && 2 * ft + (i & 1) < a.group;
           p[i] = ok ? fmaf(slope[i & 1], static_cast<float>(tok - (seq_len - 1)), y) : -INFINITY;
         } else {

@@ -44,6 +44,21 @@ __device__ __forceinline__ float capped_score(float x, const ScoreMods& m, float
   return t2 <= kCapNear * kCapNear ? fmaf(t, q, -ref) : fmaf(m.cap_log2, far, -ref);
 }
 
+// The same where a lane's scores stand alone, without ref: the coefficients as
+// immediates (115 -> 113 us for the 8B-shaped decode batch; from the launch's
+// parameters they took 123).
+__device__ __forceinline__ float capped_alone(float x, const ScoreMods& m) {
+  const float t = x * m.cap_in;
+  const float t2 = t * t;
+  float q = fmaf(t2, kTanhQ4, kTanhQ3);
+  q = fmaf(t2, q, kTanhQ2);
+  q = fmaf(t2, q, kTanhQ1);
+  q = fmaf(t2, q, kTanhQ0);
+  const float e = fast_exp2(t * (2.f * kLog2e));
+  const float far = fmaf(-2.f, fast_rcp(1.f + e), 1.f);
+  return m.cap_log2 * (t2 <= kCapNear * kCapNear ? t * q : far);
+}
+
 // Scores as floats or as their bits (as TMEM loads leave them).
 __device__ __forceinline__ float as_float(uint32_t x) { return __uint_as_float(x); }
 __device__ __forceinline__ float as_float(float x) { return x; }
