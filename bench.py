@@ -45,14 +45,14 @@ FALLBACK_BF16_TFLOPS = 1900.0
 # only while that kernel's source is unchanged (sha256 prefix of its file when
 # the counters were taken), else reported as null.
 PROFILED_TRAFFIC: dict = {
-    # 636.355840 MB read + 3.224832 MB written
-    "llama8b_decode_b64": {"bytes": 639580672, "src": "decode_kernel.cuh",
-                           "src_sha": "984a1ff3459743cf"},
-    # 940.555520 MB read + 5.621248 MB written
-    "prefix_shared_decode_b256": {"bytes": 946176768, "src": "decode_tc_kernel.cuh",
+    # 636.414208 MB read + 3.333888 MB written
+    "llama8b_decode_b64": {"bytes": 639748096, "src": "decode_kernel.cuh",
+                           "src_sha": "4a0b7de88cfc2080"},
+    # 940.237312 MB read + 6.021120 MB written
+    "prefix_shared_decode_b256": {"bytes": 946258432, "src": "decode_tc_kernel.cuh",
                                   "src_sha": "44dd168286968ac1"},
-    # prefill rows of the four-chunk batch: 894.937600 MB read + 15.723264 MB written
-    "multi_chunk_prefill": {"bytes": 910660864, "src": "prefill_kernel.cuh",
+    # prefill rows of the four-chunk batch: 868.027136 MB read + 15.460864 MB written
+    "multi_chunk_prefill": {"bytes": 883488000, "src": "prefill_kernel.cuh",
                             "src_sha": "4cd172af577355f6"},
 }
 

@@ -120,8 +120,8 @@ __host__ __device__ __forceinline__ int tile_kernel_sms(long long tile_cost, lon
 // whole numbers next to the proportional share the one whose slower side ends
 // first (a few short decode rows want two SMs rather than one; 126 against 87 us
 // of tiles when they were left with one).  Tile weights measured on a 512-token
-// chunk before 63 decode rows, with and without a cap (500, 600, 690, 850 ns
-// bf16: 275, 233, 237, 244 us capped; e4m3 1275, 1434, 1590 ns: 184, 174, 182 us).
+// chunk with a cap before 63 decode rows (531, 637, 744, 850 ns bf16: 275, 233,
+// 241, 244 us; e4m3 1275, 1434, 1594 ns: 184, 176, 182 us).
 constexpr long long kMaskedTileNsPerCost = 650;
 constexpr long long kMaskedTileNsPerCost8 = 1434;
 
