@@ -45,12 +45,12 @@ FALLBACK_BF16_TFLOPS = 1900.0
 # only while that kernel's source is unchanged (sha256 prefix of its file when
 # the counters were taken), else reported as null.
 PROFILED_TRAFFIC: dict = {
-    # 636.414208 MB read + 3.333888 MB written
-    "llama8b_decode_b64": {"bytes": 639748096, "src": "decode_kernel.cuh",
-                           "src_sha": "4a0b7de88cfc2080"},
-    # 940.237312 MB read + 6.021120 MB written
-    "prefix_shared_decode_b256": {"bytes": 946258432, "src": "decode_tc_kernel.cuh",
-                                  "src_sha": "44dd168286968ac1"},
+    # 636.342528 MB read + 3.276288 MB written
+    "llama8b_decode_b64": {"bytes": 639618816, "src": "decode_kernel.cuh",
+                           "src_sha": "adf64e76ff2e8a58"},
+    # 940.193280 MB read + 5.579008 MB written
+    "prefix_shared_decode_b256": {"bytes": 945772288, "src": "decode_tc_kernel.cuh",
+                                  "src_sha": "85fb83992cd38f9d"},
     # prefill rows of the four-chunk batch: 868.027136 MB read + 15.460864 MB written
     "multi_chunk_prefill": {"bytes": 883488000, "src": "prefill_kernel.cuh",
                             "src_sha": "4cd172af577355f6"},
