@@ -134,9 +134,11 @@ int decode_ctas_per_sm(int head_dim, int group);
 struct PlanTile {
   int r, q0, row0, rows;
   int ctx, kv_end, steps, prefix;   // prefix clipped to the request's keys
-  int lo, hi, n1, gap;              // [lo, hi): the union of the rows' causal runs
+  int lo, hi, gap;                  // [lo, hi): from the first to the last key of the rows' causal runs
+  uint32_t blocks;                  // with unseen keys among them (PVis); all ones: none
+  uint32_t seen[4];
 };
-static_assert(sizeof(PlanTile) == 48, "read as three 16-byte words");
+static_assert(sizeof(PlanTile) == 64, "read as four 16-byte words");
 struct PlanHead {
   int tiles;
   int tile_ctas;                    // CTAs (one per SM) the tile kernel works on

@@ -53,6 +53,7 @@
 #include "pa_internal.h"
 #include "pa_ptx.cuh"
 #include "score_mods.cuh"
+#include "visible_keys.cuh"
 #include "warp_search.cuh"
 #include "work_split.cuh"
 
@@ -115,7 +116,7 @@ struct PrefillCfg {
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int OFF_VIS = OFF_MISC + 64;      // [SEGS] PVis (modified scores only)
   static constexpr int SMEM = OFF_MISC + 64 + 1024;  // + 1024-byte alignment slack
-  static constexpr int SMEM_MOD = SMEM + SEGS * 32;
+  static constexpr int SMEM_MOD = SMEM + SEGS * sizeof(PVis);
   static constexpr int THREADS = 11 * 32;
   static constexpr uint32_t TMEM_COLS = 512;         // S0 0, S1 128, O0 256, O1 256 + D
   static constexpr uint32_t IDESC_S = idesc_bf16_f32(BM, BN, 0);
@@ -159,24 +160,6 @@ struct PSeg {
   int kind, unit, c0, c1;
 };
 static_assert(sizeof(PSeg) == 64, "segment record");
-
-// The keys that some row of a unit with modified scores sees, [0, prefix)
-// and [lo, hi), and the map from its steps to 128-key tiles.
-struct PVis {
-  int prefix, lo, hi, n1;
-  int gap, pad[3];
-  __device__ __forceinline__ int tile(int j) const { return j < n1 ? j : j + gap; }
-  __device__ __forceinline__ bool key(int t) const { return t < prefix || (t >= lo && t < hi); }
-  // A 16-token block with such a key, from its first key.
-  __device__ __forceinline__ bool block(int t) const {
-    return t < prefix || (t + kBlockSize > lo && t < hi);
-  }
-  // Whether all keys t .. t + n - 1 are such keys.
-  __device__ __forceinline__ bool all(int t, int n) const {
-    return t + n <= prefix || (t + n <= hi && (t >= lo || prefix >= lo));
-  }
-};
-static_assert(sizeof(PVis) == 32, "visible keys");
 
 using PReq = TileReq;
 
@@ -760,10 +743,11 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
   };
   // Cache row of 16-token tile t8 + lane (lane < 8) of request r in the
   // grouped TMA view; an id outside the pool is reported (if `report`) and
-  // read as wholly out of bounds (TMA fills zeros).
+  // read as wholly out of bounds (TMA fills zeros).  MOD: -1 for a block without a
+  // key that the unit's rows see.
   auto tile_rows = [&](int r, int t8, int nblk, bool report, const PVis& vis) -> int {
     const int t16 = t8 + lane;
-    if (lane >= 8 || (MOD ? !vis.block(t16 * kBlockSize) : t16 >= nblk)) return 0;
+    if (lane >= 8 || (MOD ? !vis.block(t16 * kBlockSize) : t16 >= nblk)) return MOD ? -1 : 0;
     const int id = __ldg(a.block_tables + static_cast<size_t>(r) * a.max_blocks_per_seq + (t16 >> a.tile_shift));
     if (static_cast<unsigned>(id) >= static_cast<unsigned>(a.num_blocks)) {
       if (report) record_error(a.status, PA_DEV_BAD_BLOCK_ID, r, id);
@@ -872,7 +856,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
       // MOD: the plan's tile T becomes the current one.
       auto take_tile = [&]() {
         const int4* rec = reinterpret_cast<const int4*>(a.plan.tiles + T);
-        const int4 w0 = __ldcg(rec), w1 = __ldcg(rec + 1), w2 = __ldcg(rec + 2);
+        const int4 w0 = __ldcg(rec), w1 = __ldcg(rec + 1), w2 = __ldcg(rec + 2), w3 = __ldcg(rec + 3);
         r = w0.x;
         p.q0 = w0.y;
         row0 = w0.z;
@@ -883,8 +867,14 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         vis.prefix = w1.w;
         vis.lo = w2.x;
         vis.hi = w2.y;
-        vis.n1 = w2.z;
-        vis.gap = w2.w;
+        vis.n1 = (vis.prefix + 127) / 128;
+        vis.gap = w2.z;
+        vis.blocks = static_cast<uint32_t>(w2.w);
+        vis.own = w2.w == -1 ? kNoHoles : p.ctx + row0;
+        vis.seen[0] = static_cast<uint32_t>(w3.x);
+        vis.seen[1] = static_cast<uint32_t>(w3.y);
+        vis.seen[2] = static_cast<uint32_t>(w3.z);
+        vis.seen[3] = static_cast<uint32_t>(w3.w);
         ub = static_cast<long long>(T) * NP;
       };
       if constexpr (MOD != kNoMods) {
@@ -1012,11 +1002,10 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         // K of every step: lane L < 8 copies block L of the step.
         const int nblk = (kv_end + kBlockSize - 1) / kBlockSize;
         // Step jj: its first 16-token block, whether this lane copies a block
-        // of it, how many blocks arrive, and up to which block they reach.
+        // of it (to cache row `row`), and how many blocks arrive.
         auto first_block = [&](int jj) -> int { return (MOD ? vis.tile(jj) : jj) * 8; };
-        auto copies = [&](int jj) -> bool {
-          return MOD ? lane < 8 && vis.block((first_block(jj) + lane) * kBlockSize)
-                     : lane < min(8, nblk - jj * 8);
+        auto copies = [&](int jj, int row) -> bool {
+          return MOD ? row >= 0 : lane < min(8, nblk - jj * 8);
         };
         auto arriving = [&](int jj, bool mine) -> int {
           return MOD ? __popc(__ballot_sync(0xffffffffu, mine)) : min(8, nblk - jj * 8);
@@ -1028,7 +1017,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
           auto issue_raw = [&](int jj, int gg, int row) -> bool {
             const int st = gg % C::NST;
             if (gg >= C::NST && !lane0_wait(bar(B::KFREE + st), ((gg / C::NST) - 1) & 1, 62)) return false;
-            const bool mine = copies(jj);
+            const bool mine = copies(jj, row);
             const int nb = arriving(jj, mine);
             if (lane == 0) mbar_arrive_expect_tx(bar(B::KRAW + st), nb * C::RAW_BLOCK);
             __syncwarp();
@@ -1056,7 +1045,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
           for (int jj = j0; jj < j1 && ok; ++jj) {
             const int st = g % C::NST;
             if (g >= C::NST && !(ok = lane0_wait(bar(B::KFREE + st), ((g / C::NST) - 1) & 1, 62))) break;
-            const bool mine = copies(jj);
+            const bool mine = copies(jj, rowc);
             const int nb = arriving(jj, mine);
             if (lane == 0) mbar_arrive_expect_tx(bar(B::KFULL + st), nb * C::BLOCK_BYTES);
             __syncwarp();
@@ -1100,9 +1089,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
       PVis vis{};
       if constexpr (MOD != kNoMods) vis = viss[slot];
       auto first_block = [&](int jj) -> int { return (MOD ? vis.tile(jj) : jj) * 8; };
-      auto copies = [&](int jj) -> bool {
-        return MOD ? lane < 8 && vis.block((first_block(jj) + lane) * kBlockSize)
-                   : lane < min(8, nblk - jj * 8);
+      auto copies = [&](int jj, int row) -> bool {
+        return MOD ? row >= 0 : lane < min(8, nblk - jj * 8);
       };
       auto arriving = [&](int jj, bool mine) -> int {
         return MOD ? __popc(__ballot_sync(0xffffffffu, mine)) : min(8, nblk - jj * 8);
@@ -1114,7 +1102,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
           const int st = gg % C::NST;
           const int rowc = tile_rows(sg.r, first_block(jj), nblk, false, vis);
           if (gg >= C::NST && !warp_wait(bar(B::VFREE + st), ((gg / C::NST) - 1) & 1, 64)) return false;
-          const bool mine = copies(jj);
+          const bool mine = copies(jj, rowc);
           const int nb = arriving(jj, mine);
           if (lane == 0) mbar_arrive_expect_tx(bar(B::VRAW + st), nb * C::RAW_BLOCK);
           __syncwarp();
@@ -1140,7 +1128,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
           const int st = g % C::NST;
           const int rowc = tile_rows(sg.r, first_block(jj), nblk, false, vis);
           if (g >= C::NST && !(ok = warp_wait(bar(B::VFREE + st), ((g / C::NST) - 1) & 1, 64))) break;
-          const bool mine = copies(jj);
+          const bool mine = copies(jj, rowc);
           const int nb = arriving(jj, mine);
           if (lane == 0) mbar_arrive_expect_tx(bar(B::VFULL + st), nb * C::BLOCK_BYTES);
           __syncwarp();
@@ -1292,10 +1280,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
       }
       if (active) {
         const int limit = min(sg.ctx + sg.row0 + i_row, sg.kv_end - 1);  // last key this row sees
-        PVis vis{};
+        const PVisBrief vis(MOD != kNoMods ? viss[slot] : PVis{});
         RowMask rm{};
         if constexpr (MOD != kNoMods) {
-          vis = viss[slot];
           rm.pos = sg.ctx + sg.row0 + i_row;
           rm.limit = limit;
           rm.prefix = vis.prefix;
@@ -1406,7 +1393,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
               const int st = (g + k) % C::NST;
               if (!(ok = all_wait(B::VFULL + st, ((g + k) / C::NST) & 1, 83))) break;
               const int row = tid - 64;
-              if (!vis.key(key0 + row)) {
+              if (!viss[slot].key(key0 + row)) {
 #pragma unroll
                 for (int c = 0; c < C::HALVES * 8; ++c)
                   st_shared_v4(v_s + st * C::TBYTES + (row >> 4) * C::BLOCK_BYTES + ((row >> 3) & 1) * C::GSTRIDE +

@@ -4,8 +4,9 @@
 //
 // A query tile (128 rows of a request) reads the 128-key steps that hold a key
 // some of its rows sees: those of [0, prefix) and of [lo, hi), where lo is the
-// least first key of its rows and hi its last position + 1.  lo comes from
-// the rows' key_starts, so the tiles' steps have no closed form: one CTA
+// least first key of its rows that see one and hi the last such row's position
+// + 1; of these steps the 16-token blocks with such a key (visible_keys.cuh).  All
+// of it comes from the rows' key_starts and has no closed form: one CTA
 // computes them, a warp per tile, and scans them, and the tile kernel finds
 // its range of steps in the scan.  The tile kernel's CTAs start meanwhile and
 // wait for it.  (8 to 10 us alone from cold caches; with the requests and scans
@@ -52,7 +53,7 @@ __device__ __forceinline__ long long block_scan(long long v, long long* sums, lo
   return before;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) plan_prefill_kernel(const PrefillArgs a) {
+__global__ void __launch_bounds__(kPlanThreads, 1) plan_prefill_kernel(const PrefillArgs a) {
   __shared__ long long sums[33];
   __shared__ unsigned long long decode_tiles;  // 16-token tiles of the decode rows (per kv head)
   griddep_launch_dependents();
@@ -90,16 +91,54 @@ __global__ void __launch_bounds__(kPlanThreads) plan_prefill_kernel(const Prefil
     const PReq p = prefill_req(a, r);
     const int row0 = max(0, p.ntq - 1 - (t - pl.first[r])) * 128;
     const int rows = min(128, p.q_len - row0);
-    int lo = 0x7fffffff;
-    for (int i = lane; i < rows; i += 32) {
-      const int start = a.mods.key_starts != nullptr ? max(0, __ldg(a.mods.key_starts + p.q0 + row0 + i)) : 0;
-      if (start <= p.ctx + row0 + i) lo = min(lo, start);
+    // Row i = 32 w + lane: its first key, if it sees one of its run.
+    const int own = p.ctx + row0;  // position of the tile's first row
+    int start[4], lo = 0x7fffffff, last = -1;
+    bool all_see = true;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const int i = 32 * w + lane;
+      start[w] = 0x7fffffff;
+      if (i < rows)
+        start[w] = a.mods.key_starts != nullptr ? max(0, __ldg(a.mods.key_starts + p.q0 + row0 + i)) : 0;
+    }
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const int i = 32 * w + lane;
+      if (start[w] > own + i) start[w] = 0x7fffffff;
+      lo = min(lo, start[w]);
+      const uint32_t see = __ballot_sync(0xffffffffu, start[w] != 0x7fffffff);
+      if (see != 0) last = 32 * w + 31 - __clz(see);
+      all_see &= see == __ballot_sync(0xffffffffu, i < rows);
     }
     lo = __reduce_min_sync(0xffffffffu, lo);
+    // Which of the keys own .. own + 127 some row sees (key own + k: a row i >= k
+    // that starts at or before it); all of them up to the last row that sees
+    // one, unless a row sees nothing.
+    uint32_t seen[4] = {0, 0, 0, 0}, blocks = 0xffffffffu;
+    if (!all_see && last >= 0) {
+      int least = 0x7fffffff;  // first key of the rows behind word w
+      bool holes = false;
+#pragma unroll
+      for (int w = 3; w >= 0; --w) {
+        int m = start[w];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int next = __shfl_down_sync(0xffffffffu, m, o);
+          if (lane + o < 32) m = min(m, next);
+        }
+        m = min(m, least);
+        least = __shfl_sync(0xffffffffu, m, 0);
+        const int k = 32 * w + lane;
+        seen[w] = __ballot_sync(0xffffffffu, m <= own + k);
+        holes |= __any_sync(0xffffffffu, k <= last && m > own + k) != 0;
+      }
+      if (holes) blocks = __ballot_sync(0xffffffffu, lane < 9 && own_block_seen(seen, own, lo, lane));
+    }
     if (lane != 0) continue;
     const int prefix =
         a.mods.prefix_lens != nullptr ? min(max(__ldg(a.mods.prefix_lens + r), 0), p.seq_len) : 0;
-    const int hi = lo != 0x7fffffff ? p.ctx + row0 + rows : 0;
+    const int hi = last >= 0 ? own + last + 1 : 0;
     PlanTile w;
     w.r = r;
     w.q0 = p.q0;
@@ -112,10 +151,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_prefill_kernel(const Prefil
     w.hi = hi;
     // Steps [0, n1) hold the prefix; those of the run that are not among them
     // follow after a gap.
-    w.n1 = (prefix + 127) / 128;
-    const int second = hi > 0 ? max(w.n1, lo / 128) : w.n1;
-    w.gap = second - w.n1;
-    w.steps = w.n1 + max(0, (hi + 127) / 128 - second);
+    const int n1 = (prefix + 127) / 128;
+    const int second = hi > 0 ? max(n1, lo / 128) : n1;
+    w.gap = second - n1;
+    w.blocks = blocks;
+    for (int u = 0; u < 4; ++u) w.seen[u] = seen[u];
+    w.steps = n1 + max(0, (hi + 127) / 128 - second);
     if (w.steps == 0) {  // no row sees a key: one step without data writes the zeros
       w.steps = 1;
       w.gap = 0;
