@@ -363,12 +363,14 @@ def _launch(name, dev, *args):
 
 
 def _heads(name, t, dev, T, heads, d):
+    """The token stride of t [T, heads, d].  One token has none of its own (torch
+    leaves that stride arbitrary): a row's size then."""
     if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or t.get_device() != dev:
         _refuse(name, t, torch.bfloat16, dev)
     stride = t.stride()
     if t.shape != (T, heads, d) or stride[2] != 1 or (stride[1] != d and heads > 1):
         raise ValueError(f"{name} must be [{T}, {heads}, {d}] with contiguous heads")
-    return stride[0]
+    return stride[0] if T != 1 else heads * d
 
 
 def _qk_norm_rope(fn, cache_dtype, scales, q, key, value, key_cache, value_cache, block_tables,
