@@ -22,9 +22,9 @@ int decode_ctas_per_sm(int head_dim, int group) {
 
 cudaError_t launch_decode(const DecodeArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
                           int head_dim, bool kv8, bool xsplit, cudaStream_t stream) {
-  // e4m3 units of two kv heads (8 q heads, head_dim 128): one instantiation.
+  // e4m3 units of two kv heads (8 q heads, head_dim 128).
   if (kv8 && !xsplit && a.group == 8 && head_dim == 128 && a.tile_sms == 0)
-    return launch_decode_impl<128, 8, true, false>(a, kmap, vmap, stream);
+    return launch_decode_pair<false, false>(a, kmap, vmap, stream);
   const int gmax = decode_gmax(a.group);
   const bool mix = a.tile_sms > 0;  // built for head_dim 128 (the host splits the SMs only there)
 #define PA_DECODE_CASE(DD, GG)                                                      \

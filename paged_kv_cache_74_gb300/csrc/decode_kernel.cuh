@@ -168,18 +168,29 @@ __device__ __forceinline__ float inverse_sum(float l, float num) {
 // computed at once, lane i those of contributor base + i, from a running maximum
 // over the lanes; the O loads of kAtOnce contributors are issued together, one
 // memory round trip for all.  `mine`: the contributor whose record is still in
-// shared memory at hr (-1: none).  One request of 32768 tokens: 77 us, with the
-// epilogue's loop alone 99; e4m3, 30000 tokens: 152 and 208.  Out of line: inline
-// the 8B-shaped batch, whose pairs have two or three pieces, took 117.5 us, not
-// 112.8.
+// shared memory at hr (-1: none).  One request of 32768 tokens: 80 us, with the
+// epilogue's loop alone 99.  Out of line: inline the 8B-shaped batch, whose pairs
+// have two or three pieces, took 117.5 us, not 112.8.
+//
+// What a kernel calls takes part of its registers.  At head_dim 128 with units of
+// two kv heads (GMAX 8) this function beside the epilogue's loop costs the kernel
+// spills: 8B-shaped batch 76.4 us, 200 short requests 43.7 us, against 72.3 and
+// 39.6 without the call; a merge small enough not to spill still 3 % on both.
+// So those kernels are built twice: with the loop alone, and with this merge
+// alone for calls whose grid has more than kFewPieces CTAs per pair (one request
+// of 32768 tokens: 147 us against 205; 4 of 8000: 59 against 75; 16 of 512 to 4096:
+// 45 against 50).
 constexpr int kFewPieces = 4;
+constexpr int kMergeByPieces = 0;  // by the pair's pieces
+constexpr int kMergeFew = 1;       // the epilogue's loop for any number of them
+constexpr int kMergeMany = 2;      // merge_many for any number of them
 template <int D, int GMAX, bool MOD>
 __device__ __noinline__ void merge_many(const float* hr, const float* __restrict__ part_ml,
                                         const float* __restrict__ part_o, int c0, int n, int mine, int group,
                                         float v_scale, int lane, __nv_bfloat16* __restrict__ out) {
   constexpr int kPer = D / 64;  // head_dim pairs per lane and head
-  constexpr int kHeads = GMAX < 2 ? 1 : 2;
-  constexpr int kAtOnce = 16 / kPer;
+  constexpr int kHeads = GMAX < 2 ? 1 : (GMAX == 8 ? 4 : 2);
+  constexpr int kAtOnce = GMAX == 8 ? 4 : 8;
 #pragma unroll 1
   for (int h0 = 0; h0 < group; h0 += kHeads) {
     float M[kHeads], L[kHeads], o[kHeads][kPer][2];
@@ -403,7 +414,9 @@ __device__ __forceinline__ uint32_t e8_row_offset(int r, int c) {
 // MIX: the decode rows of a pa_prefill_varlen call that may split the SMs
 // with its tile kernel (DecodeArgs::tile_sms); a separate instantiation, so
 // that the plain decode's start-up stays as short as it is.
-template <int D, int GMAX, bool KV8, bool XS, bool MIX, bool MOD = false>
+//
+// MERGE: how a pair's partials are merged (merge_many).
+template <int D, int GMAX, bool KV8, bool XS, bool MIX, bool MOD, int MERGE>
 __global__ void __launch_bounds__(DecodeCfg<D, GMAX, KV8, XS, MOD>::THREADS,
                                   DecodeCfg<D, GMAX, KV8, XS, MOD>::MINB)
 paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
@@ -841,11 +854,11 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
         if (last) {
           __syncwarp();  // lane 0 saw the other contributors' counts
           __threadfence();
-          if (c1 - c0 >= kFewPieces) {
+          if (MERGE == kMergeMany || (MERGE == kMergeByPieces && c1 - c0 >= kFewPieces)) {
             merge_many<D, GMAX, MOD>(hr, a.part_ml, a.part_o, c0, c1 - c0 + 1, last == 2 ? cta - c0 : -1, a.group,
                                      a.v_scale, lane,
                                      a.out + (static_cast<size_t>(e.row) * a.num_heads + head0) * D);
-          } else {
+          } else if constexpr (MERGE != kMergeMany) {
             // Lane L merges head_dim pairs L, L + 32, ... of every head.  The
             // loads of one contributor are independent of each other, so each
             // contributor costs one memory round trip.
@@ -1342,11 +1355,11 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
   }
 }
 
-template <int D, int GMAX, bool KV8, bool XS, bool MIX = false, bool MOD = false>
+template <int D, int GMAX, bool KV8, bool XS, bool MIX = false, bool MOD = false, int MERGE = kMergeByPieces>
 cudaError_t launch_decode_impl(const DecodeArgs& a, const CUtensorMap& kmap,
                                const CUtensorMap& vmap, cudaStream_t stream) {
   using C = DecodeCfg<D, GMAX, KV8, XS, MOD>;
-  auto* kernel = paged_decode_kernel<D, GMAX, KV8, XS, MIX, MOD>;
+  auto* kernel = paged_decode_kernel<D, GMAX, KV8, XS, MIX, MOD, MERGE>;
   static bool attr_set[64] = {false};  // per device: set once
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
@@ -1361,6 +1374,15 @@ cudaError_t launch_decode_impl(const DecodeArgs& a, const CUtensorMap& kmap,
   }
   return launch_overlapped(kernel, dim3(a.num_ctas), dim3(C::THREADS), C::SMEM, stream, kmap,
                            vmap, a);
+}
+
+// The e4m3 units of two kv heads (8 q heads, head_dim 128).
+template <bool MIX, bool MOD>
+cudaError_t launch_decode_pair(const DecodeArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                               cudaStream_t stream) {
+  const bool many = a.num_ctas > static_cast<int64_t>(kFewPieces) * a.num_seqs * a.num_kv_heads;
+  return many ? launch_decode_impl<128, 8, true, false, MIX, MOD, kMergeMany>(a, kmap, vmap, stream)
+              : launch_decode_impl<128, 8, true, false, MIX, MOD, kMergeFew>(a, kmap, vmap, stream);
 }
 
 }  // namespace

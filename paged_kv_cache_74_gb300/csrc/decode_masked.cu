@@ -17,8 +17,8 @@ cudaError_t launch_decode_masked(const DecodeArgs& a, const CUtensorMap& kmap, c
   const bool mix = a.tile_sms > 0;  // built for head_dim 128 (the host splits the SMs only there)
   // e4m3 units of two kv heads (8 q heads, head_dim 128).
   if (kv8 && a.group == 8 && head_dim == 128)
-    return mix ? launch_decode_impl<128, 8, true, false, true, true>(a, kmap, vmap, stream)
-               : launch_decode_impl<128, 8, true, false, false, true>(a, kmap, vmap, stream);
+    return mix ? launch_decode_pair<true, true>(a, kmap, vmap, stream)
+               : launch_decode_pair<false, true>(a, kmap, vmap, stream);
   const int gmax = decode_gmax(a.group);
 #define PA_DECODE_CASE(DD, GG)                                                                     \
   if (head_dim == DD && gmax == GG)                                                                \
