@@ -91,49 +91,55 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_prefill_kernel(const Pre
     const PReq p = prefill_req(a, r);
     const int row0 = max(0, p.ntq - 1 - (t - pl.first[r])) * 128;
     const int rows = min(128, p.q_len - row0);
-    // Row i = 32 w + lane: its first key, if it sees one of its run.
     const int own = p.ctx + row0;  // position of the tile's first row
-    int start[4], lo = 0x7fffffff, last = -1;
-    bool all_see = true;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const int i = 32 * w + lane;
-      start[w] = 0x7fffffff;
-      if (i < rows)
-        start[w] = a.mods.key_starts != nullptr ? max(0, __ldg(a.mods.key_starts + p.q0 + row0 + i)) : 0;
-    }
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const int i = 32 * w + lane;
-      if (start[w] > own + i) start[w] = 0x7fffffff;
-      lo = min(lo, start[w]);
-      const uint32_t see = __ballot_sync(0xffffffffu, start[w] != 0x7fffffff);
-      if (see != 0) last = 32 * w + 31 - __clz(see);
-      all_see &= see == __ballot_sync(0xffffffffu, i < rows);
-    }
-    lo = __reduce_min_sync(0xffffffffu, lo);
-    // Which of the keys own .. own + 127 some row sees (key own + k: a row i >= k
-    // that starts at or before it); all of them up to the last row that sees
-    // one, unless a row sees nothing.
+    int lo = 0, last = rows - 1;   // the least first key, and the last row that sees one of its run
     uint32_t seen[4] = {0, 0, 0, 0}, blocks = 0xffffffffu;
-    if (!all_see && last >= 0) {
-      int least = 0x7fffffff;  // first key of the rows behind word w
-      bool holes = false;
+    if (a.mods.key_starts != nullptr) {
+      // Row 32 w + lane: its first key, if it sees one of its run.
+      int start[4];
+      uint32_t see[4];
 #pragma unroll
-      for (int w = 3; w >= 0; --w) {
-        int m = start[w];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int next = __shfl_down_sync(0xffffffffu, m, o);
-          if (lane + o < 32) m = min(m, next);
-        }
-        m = min(m, least);
-        least = __shfl_sync(0xffffffffu, m, 0);
-        const int k = 32 * w + lane;
-        seen[w] = __ballot_sync(0xffffffffu, m <= own + k);
-        holes |= __any_sync(0xffffffffu, k <= last && m > own + k) != 0;
+      for (int w = 0; w < 4; ++w) {
+        const int i = 32 * w + lane;
+        start[w] = i < rows ? max(0, __ldg(a.mods.key_starts + p.q0 + row0 + i)) : 0x7fffffff;
       }
-      if (holes) blocks = __ballot_sync(0xffffffffu, lane < 9 && own_block_seen(seen, own, lo, lane));
+      lo = 0x7fffffff;
+      last = -1;
+      int seeing = 0;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        if (start[w] > own + 32 * w + lane) start[w] = 0x7fffffff;
+        lo = min(lo, start[w]);
+        see[w] = __ballot_sync(0xffffffffu, start[w] != 0x7fffffff);
+        if (see[w] != 0) last = 32 * w + 31 - __clz(see[w]);
+        seeing += __popc(see[w]);
+      }
+      lo = __reduce_min_sync(0xffffffffu, lo);
+      if (seeing <= last) {
+        // Some row before the last one sees nothing.  Key own + k is seen by a row
+        // i >= k that starts at or before it.
+        int least = 0x7fffffff;  // first key of the rows behind word w
+        bool holes = false;
+#pragma unroll 1
+        for (int w = 3; w >= 0; --w) {
+          int m = w == 0 ? start[0] : w == 1 ? start[1] : w == 2 ? start[2] : start[3];
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int next = __shfl_down_sync(0xffffffffu, m, o);
+            if (lane + o < 32) m = min(m, next);
+          }
+          m = min(m, least);
+          least = __shfl_sync(0xffffffffu, m, 0);
+          const int k = 32 * w + lane;
+          const uint32_t word = __ballot_sync(0xffffffffu, m <= own + k);
+          if (w == 0) seen[0] = word;
+          if (w == 1) seen[1] = word;
+          if (w == 2) seen[2] = word;
+          if (w == 3) seen[3] = word;
+          holes |= __any_sync(0xffffffffu, k <= last && m > own + k) != 0;
+        }
+        if (holes) blocks = __ballot_sync(0xffffffffu, lane < 9 && own_block_seen(seen, own, lo, lane));
+      }
     }
     if (lane != 0) continue;
     const int prefix =
