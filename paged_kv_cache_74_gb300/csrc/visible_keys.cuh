@@ -27,10 +27,12 @@ constexpr int kNoHoles = 0x7fffffff;
 // some row sees (bit k of seen: key own + k; keys of [lo, own) are all seen).
 PA_HD bool own_block_seen(const uint32_t (&seen)[4], int own, int lo, int b) {
   const int s = 16 * b - (own & 15);  // the block holds bits s .. s + 15
-  if (s < 0 && lo < own) return true;
-  for (int k = s < 0 ? 0 : s; k < s + 16 && k < 128; ++k)
-    if (seen[k >> 5] >> (k & 31) & 1u) return true;
-  return false;
+  if (s < 0) return lo < own || (seen[0] & ((1u << (s + 16)) - 1u)) != 0;
+  // (selects rather than indexed loads: `seen` stays in registers)
+  const int w = s >> 5;
+  const uint32_t low = w == 0 ? seen[0] : w == 1 ? seen[1] : w == 2 ? seen[2] : w == 3 ? seen[3] : 0u;
+  const uint32_t high = w == 0 ? seen[1] : w == 1 ? seen[2] : w == 2 ? seen[3] : 0u;
+  return ((static_cast<uint64_t>(high) << 32 | low) >> (s & 31) & 0xffffu) != 0;
 }
 
 // The keys that some row of a unit with modified scores sees, and the map from
