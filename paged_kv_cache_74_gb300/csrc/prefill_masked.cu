@@ -9,14 +9,17 @@
 // of it comes from the rows' key_starts and has no closed form: one CTA
 // computes them, a warp per tile, and scans them, and the tile kernel finds
 // its range of steps in the scan.  The tile kernel's CTAs start meanwhile and
-// wait for it.  (8 to 10 us alone from cold caches; with the requests and scans
-// held in shared memory it was no faster: its time is the arrival of its
-// instructions and three dependent loads.)
+// wait for it.  (8 to 10 us alone from cold caches, 12 where rows see nothing and
+// the unseen keys are worked out; with the requests and scans held in shared
+// memory it was no faster: its time is the arrival of its instructions and three
+// dependent loads.)
 //
-// Measured, one GB300: four long chunks with a 4096-key window (32 q, 8 kv heads
-// of 128, bf16) 255 us, with a cap of 30 292 us (249 GFLOP on visible pairs: 0.52
-// and 0.45 of the bf16 peak); a 512-token chunk with a cap before 63 decode rows
-// 232 us (1.1 GB of K/V, 0.70 of the copy peak).
+// Measured, one GB300, call after call (L2 flushed before each call: 11 us more):
+// four long chunks with a 4096-key window (32 q, 8 kv heads of 128, bf16) 246 us,
+// with a cap of 30 289 us, with slopes 307 us, capped over e4m3 417 us (249 GFLOP
+// on visible pairs: 0.54, 0.46, 0.43 and 0.32 of the bf16 peak); a 512-token chunk
+// with a cap before 63 decode rows 234 us (1.1 GB of K/V, 0.69 of the copy peak),
+// over e4m3 170 us (0.48).
 #include "prefill_kernel.cuh"
 
 namespace pa {
@@ -115,9 +118,20 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_prefill_kernel(const Pre
         seeing += __popc(see[w]);
       }
       lo = __reduce_min_sync(0xffffffffu, lo);
+      bool gap = false;  // some key before that of row `last` is seen neither by its own nor by the next row
       if (seeing <= last) {
-        // Some row before the last one sees nothing.  Key own + k is seen by a row
-        // i >= k that starts at or before it.
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const int behind = w < 3 ? __shfl_sync(0xffffffffu, start[w + 1 < 4 ? w + 1 : 3], 0) : 0x7fffffff;
+          int next = __shfl_down_sync(0xffffffffu, start[w], 1);
+          if (lane == 31) next = behind;
+          const int k = 32 * w + lane;
+          gap |= k < last && start[w] == 0x7fffffff && next > own + k;
+        }
+        gap = __any_sync(0xffffffffu, gap) != 0;
+      }
+      if (gap) {
+        // Key own + k is seen by a row i >= k that starts at or before it.
         int least = 0x7fffffff;  // first key of the rows behind word w
         bool holes = false;
 #pragma unroll 1
