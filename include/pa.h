@@ -219,7 +219,8 @@ pa_status pa_append_tokens(const void* key, const void* value, int64_t key_strid
  * PA_DEV_BAD_POSITION).  Rows behind query_start_loc[num_seqs] are left as
  * they are in q_out and slot_mapping.  num_seqs == 0 or total_tokens == 0 is
  * a no-op.  A head with a NaN or an infinity norms to NaN; the squares of a
- * normed head must sum to a finite float (values below 1e18).
+ * normed head must sum to a finite float (values below 1e18), and with eps 0 to a
+ * normal one (some value above 1e-18; an all-zero head then gives NaN).
  */
 pa_status pa_qk_norm_rope_append(void* q_out, const void* q, const void* key, const void* value,
                                  int64_t q_stride, int64_t key_stride, int64_t value_stride,
@@ -613,14 +614,18 @@ size_t pa_prefill_masked_workspace_size(int32_t num_seqs, int32_t total_q, int32
  * a prefix is seen by all rows of its request, those before its end included
  * (its keys must be in the cache: prefix_lens is clipped to seq_lens), and the
  * distance bias of a key behind the row is by |p - j| as well.
- * Keys that no row of a request's 128-row query tile sees may hold anything,
- * and 16-token blocks without a seen key are not read; V of a key that some
+ * Keys that no row of a request's 128-row query tile (rows 128 t .. 128 t + 127
+ * of the request) sees may hold anything, and 16-token blocks without a key that a
+ * row of the tile sees are not read for it, nor are their block_tables entries,
+ * wherever rows that see nothing leave such keys; V of a key that some
  * row of the tile sees must be finite (a weight of 0 does not cancel an
  * infinity in the tile's product).  Rows that see no key give zeros.  Over
- * bf16 caches with a softcap up to 50 the softmax needs no running maximum
- * and uses none: values of magnitude 2^-45 to 2^45 then keep their precision
- * whatever the scores (smaller ones lose theirs only in rows whose scores all
- * lie near -softcap).
+ * bf16 caches with a softcap up to 50 and without slopes the softmax needs no
+ * running maximum and uses none: values of magnitude 2^-45 to 2^45 then keep their
+ * precision whatever the scores (smaller ones lose theirs only in rows whose
+ * scores all lie near -softcap; larger ones may overflow), and a row's heaviest
+ * weight is rounded to bf16 like the others (relative error of the output 0.0023
+ * where a running maximum gives 0.0016 to 0.0022).
  * When max_query_len > 1 a first kernel plans the query tiles (which keys each
  * needs), then the tile kernel and the decode kernel follow as in
  * pa_prefill_varlen.  Other

@@ -71,10 +71,10 @@ constexpr int kEndSeg = 7;        // segment record kind: no more work
 // tiles with a visible key, 8 by 8 in order; the softmax and converter threads
 // work out from the segment's TcVis which token their MMA row is and whether the
 // request's row sees it.  Over e4m3 caches the kernel is bound by the arrival of
-// its roles' instructions (2.4 of 13 stall cycles per issue): the converter's
-// loops are rolled over 64 values of head_dim at a time, which took 200 requests
-// with 8 q heads per kv head from 382 to 348 us with a cap, from 346 to 313
-// without, and the plain form from 271 to 268.
+// its roles' instructions (1.2 stall cycles per issue wait for them): the converter's
+// loops are rolled over 64 values of head_dim at a time.  200 requests with 8 q
+// heads per kv head, call after call, rolled and unrolled: with a cap 317 and 365
+// us, without 285 and 328, the plain form 253 and 273.
 template <int D, int GM, bool KV8 = false, int MOD = kNoMods>
 struct TcCfg {
   static constexpr int HALVES = D / 64;             // 128-byte column chunks of head_dim

@@ -1,8 +1,9 @@
 // decode_tc_masked.cu -- the tensor-core paged decode with modified scores: launchers
 // of the MOD instantiations of decode_tc_kernel.cuh (5 to 16 q heads per kv head).
 // Measured on 200 requests of 16 to 4099 keys, 64 q and 8 kv heads of 128, with a
-// cap: bf16 281 us, 6.2 TB/s of visible K/V, 0.92 of the copy peak; e4m3 348 us, 2.5
-// TB/s (the conversion and the softmax of a chunk set its rate, not the bytes).
+// cap, call after call: bf16 274 us, 6.4 TB/s of visible K/V, 0.94 of the copy
+// peak (L2 flushed before each call 312); e4m3 318 us, 2.8 TB/s (the conversion and
+// the softmax of a chunk set its rate, not the bytes), without a cap 285.
 #include "decode_tc_kernel.cuh"
 
 namespace pa {

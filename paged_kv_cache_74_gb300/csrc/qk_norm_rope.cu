@@ -22,11 +22,14 @@
 // lanes fill with asynchronous copies, three passes ahead, without holding
 // registers for what is in flight.
 //
-// Measured on 24065 prompt tokens (32 q and 8 kv heads of 128, bf16): 105 us, 5.7
-// TB/s, 0.84 of the copy peak; with one pass ahead in registers 136 us; ring
-// slots 3, 6, 8: 109, 107, 115 us; 64 registers (four CTAs per SM): 126 us.
-// Few tokens: the time is the chain launch, query_start_loc and seq_lens, block
-// id and cos / sin, write: one token 7-9 us, 575 tokens 13 us.
+// Measured on 24065 prompt tokens (32 q and 8 kv heads of 128, bf16): 99 us call
+// after call, 6.0 TB/s, 0.89 of the copy peak; with L2 flushed before each call 105
+// us, 0.84, and there with one pass ahead in registers 136 us, ring slots 3, 6, 8:
+// 109, 107, 115 us, 64 registers (four CTAs per SM): 126 us.  Over e4m3 caches 101 us
+// call after call (80 by the bytes); 16 q heads and 1 kv head 54 (33), 32 and 2 over
+// e4m3 83 (64): there the padded k and v passes and the division per stored value
+// show.  Few tokens: the time is the chain launch, query_start_loc and
+// seq_lens, block id and cos / sin, write: one token 9 us, 575 tokens 13 us.
 #include <algorithm>
 
 #include "pa_internal.h"

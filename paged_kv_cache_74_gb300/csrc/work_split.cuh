@@ -120,8 +120,13 @@ __host__ __device__ __forceinline__ int tile_kernel_sms(long long tile_cost, lon
 // whole numbers next to the proportional share the one whose slower side ends
 // first (a few short decode rows want two SMs rather than one; 126 against 87 us
 // of tiles when they were left with one).  Tile weights measured on a 512-token
-// chunk with a cap before 63 decode rows (531, 637, 744, 850 ns bf16: 275, 233,
-// 241, 244 us; e4m3 1275, 1434, 1594 ns: 184, 176, 182 us).
+// chunk before 63 decode rows, L2 flushed before each call.  bf16, weights 531, 600,
+// 650, 700, 800, 1000: with a cap 267, 252, 242, 244, 248, 257 us, with a window 128,
+// 123, 121, 123, 124, 131, with slopes 286, 268, 256, 243, 232, 241.  e4m3, weights
+// 1100, 1275, 1434, 1594, 1900: with a cap 203, 182, 179, 184, 194, with slopes
+// 191, 174, 170, 176, 184, without either 176, 163, 167, 171, 179.  One weight serves
+// all three softmaxes: the capped one's, which is the best or close to it but for
+// bf16 slopes (two passes, a store between them: 10 % from their own best).
 constexpr long long kMaskedTileNsPerCost = 650;
 constexpr long long kMaskedTileNsPerCost8 = 1434;
 
