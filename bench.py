@@ -45,15 +45,15 @@ FALLBACK_BF16_TFLOPS = 1900.0
 # only while that kernel's source is unchanged (sha256 prefix of its file when
 # the counters were taken), else reported as null.
 PROFILED_TRAFFIC: dict = {
-    # 636.342528 MB read + 3.276288 MB written
-    "llama8b_decode_b64": {"bytes": 639618816, "src": "decode_kernel.cuh",
-                           "src_sha": "adf64e76ff2e8a58"},
-    # 940.193280 MB read + 5.579008 MB written
-    "prefix_shared_decode_b256": {"bytes": 945772288, "src": "decode_tc_kernel.cuh",
-                                  "src_sha": "85fb83992cd38f9d"},
-    # prefill rows of the four-chunk batch: 868.027136 MB read + 15.460864 MB written
-    "multi_chunk_prefill": {"bytes": 883488000, "src": "prefill_kernel.cuh",
-                            "src_sha": "4cd172af577355f6"},
+    # 636.349440 MB read + 2.962432 MB written
+    "llama8b_decode_b64": {"bytes": 639311872, "src": "decode_kernel.cuh",
+                           "src_sha": "a44159fa5cf4bb3a"},
+    # 940.015104 MB read + 4.698624 MB written
+    "prefix_shared_decode_b256": {"bytes": 944713728, "src": "decode_tc_kernel.cuh",
+                                  "src_sha": "99d5cfbf2f36441d"},
+    # prefill rows of the four-chunk batch: 839.478272 MB read + 15.163136 MB written
+    "multi_chunk_prefill": {"bytes": 854641408, "src": "prefill_kernel.cuh",
+                            "src_sha": "312a4e4dbe93e7a6"},
 }
 
 

@@ -493,9 +493,10 @@ __device__ __noinline__ bool merge_staged(const float* __restrict__ part_ml,
 // What it costs in precision: the key that last set a running maximum weighs 2^0,
 // which bf16 holds exactly, and in most rows no key weighs more; with a fixed
 // reference the heaviest weight is rounded like any other, and l, which sums the
-// weights before they are rounded, does not cancel that.  Relative error of the output against 64 bits (norms) and time, L2
-// flushed, on four long chunks with a window and a cap of 30, and on a 512-token
-// chunk with a cap of 50 before 63 decode rows:
+// weights before they are rounded, does not cancel that.  Relative error of the
+// output against 64 bits (norms) and time, L2 flushed, on four long chunks with a
+// window and a cap of 30, and on a 512-token chunk with a cap of 50 before 63
+// decode rows:
 //   fixed reference (as built)                   0.0023  365 us   0.0023  243 us
 //   fixed, l the sum of the rounded weights      0.0020  389 us   0.0020  252 us
 //   running maximum (two passes)                 0.0022  443 us   0.0022  302 us
