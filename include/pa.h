@@ -80,7 +80,11 @@ typedef enum pa_device_error {
     PA_DEV_BAD_SEQ_LEN = 3,     /* seq_len < 1, > max_seq_len or > max_blocks_per_seq * block_size */
     PA_DEV_BAD_QUERY_LEN = 4,   /* q_len > seq_len, > max_query_len, or rows beyond total_q */
     PA_DEV_WAIT_TIMEOUT = 5,    /* a pipeline wait gave up (internal error); the CTA stopped */
-    PA_DEV_BAD_POSITION = 6     /* rotation position outside the cos / sin table (token skipped) */
+    PA_DEV_BAD_POSITION = 6,    /* rotation position outside the cos / sin table (token skipped) */
+    PA_DEV_OUT_OF_BLOCKS = 7,   /* more blocks asked for than are free, or given back than there is room for */
+    PA_DEV_BAD_PARENT = 8,      /* a tree row's parent outside [-1, its own index) (taken as a root) */
+    PA_DEV_BAD_HELD = 9,        /* held blocks < 0 or > max_blocks_per_seq (request skipped) */
+    PA_DEV_BAD_PATH = 10        /* accepted rows not ascending, or not rows of the request (request skipped) */
 } pa_device_error;
 
 /* Human-readable name of a pa_status value (static string, never NULL). */
@@ -657,6 +661,104 @@ pa_status pa_prefill_varlen_masked_fp8(void* out, const void* q, const void* key
                                        float k_scale, float v_scale, float softcap, const float* slopes,
                                        const int32_t* key_starts, const int32_t* prefix_lens,
                                        void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * pa_plan_step -- the bookkeeping of a step built on the device from the
+ * requests' lengths: cache blocks for the new tokens, the block tables, the row
+ * offsets, lengths, slots and positions that the append and attention calls
+ * take, and the masks of drafted token trees.  ("vLLM 深度解析（二）", section
+ * 3.1, and "vllm 深度解析：一切从 PagedAttention 谈起" build block tables and
+ * slot mappings on the host each step; here they need no round trip, so that a
+ * captured step can plan itself.)
+ *
+ *   block_tables   [num_seqs, max_blocks_per_seq] int32, in and out: new blocks are
+ *                  entered behind each request's held ones
+ *   held_blocks    [num_seqs] int32, in and out: valid entries of each row
+ *   context_lens   [num_seqs] int32 tokens already in the cache
+ *   query_lens     [num_seqs] int32 new tokens of this step (0 allowed)
+ *   free_blocks    [capacity] int32, the first *free_count of them free block ids
+ *   free_count     one int32, in and out
+ *   query_start_loc [num_seqs + 1], seq_lens [num_seqs] int32 (written)
+ *   slot_mapping   [max_tokens] int64, positions [max_tokens] int32 (written)
+ *   parents        optional [max_tokens] int32, packed like the rows: the row of
+ *                  the same request that a row follows in its tree, -1 for one that
+ *                  follows the context; a parent comes before its children
+ *                  (NULL: each row follows the one before)
+ *   tree_masks     optional [max_tokens, mask_words] 64-bit words (written): bit k of
+ *                  a row: it sees row k of its request, that is itself and its
+ *                  ancestors.  mask_words 1 to 4; query_lens up to 64 * mask_words
+ * Request r, with c = context_lens[r] and n = query_lens[r], gets
+ * max(0, ceil((c + n) / block_size) - held_blocks[r]) blocks.  The new blocks of the
+ * step, in order of request and position, come off the end of the list: the i-th
+ * is free_blocks[*free_count - 1 - i].  seq_lens[r] = c + n; row i of the request
+ * goes to the slot of position c + i, and positions (rotation positions: what
+ * pa_qk_norm_rope_append takes as `positions`) holds c + i, or with parents
+ * c + the row's depth.  Rows behind the last request's get slot -1 (which the cache
+ * writes skip), position 0 and an empty mask.
+ * Refused on the device, with a record in *device_status: a request with a length
+ * or held count out of range (seq_lens 0, its slots -1, no blocks); the whole
+ * batch, when its rows exceed max_tokens (PA_DEV_BAD_QUERY_LEN, request index
+ * num_seqs) or its blocks *free_count (PA_DEV_OUT_OF_BLOCKS): every seq_lens 0,
+ * every slot -1, tables, held_blocks and the list as they were.  Attention calls
+ * then skip the rows (q_len > seq_len).
+ * num_seqs up to 65535 and max_tokens >= 0; num_seqs == 0 still fills the rows.
+ * No output may overlap an input or another output (PA_ERR_INVALID).
+ */
+pa_status pa_plan_step(int32_t* block_tables, int32_t max_blocks_per_seq, int32_t* held_blocks,
+                       const int32_t* context_lens, const int32_t* query_lens, int32_t num_seqs,
+                       const int32_t* free_blocks, int32_t capacity, int32_t* free_count,
+                       int32_t block_size, int32_t num_blocks, int32_t* query_start_loc,
+                       int32_t* seq_lens, int64_t* slot_mapping, int32_t* positions,
+                       int32_t max_tokens, const int32_t* parents, void* tree_masks,
+                       int32_t mask_words, int32_t* device_status, void* stream);
+
+/*
+ * pa_release_blocks -- blocks given back: those of each request behind the first
+ * ceil(keep_lens[r] / block_size) (0: all of them) go back to the list of
+ * pa_plan_step, and held_blocks becomes what is left.  A request that holds no more
+ * than that is left alone.  With F blocks given back in all, in order of request and
+ * position, the j-th goes to free_blocks[*free_count + F - 1 - j]: giving back
+ * exactly what a plan took leaves the list as it was before the plan.  The
+ * tables' entries stay as they are.  A block in the tables of several requests is
+ * given back by each of them: requests that share blocks keep them out of this call.
+ * A request with keep_lens < 0 or a held count out of range is skipped; when the
+ * list has no room for F more nothing is done (PA_DEV_OUT_OF_BLOCKS); a block id out
+ * of range is recorded and kept as it is.  keep_lens overlaps no other array
+ * (PA_ERR_INVALID).
+ */
+pa_status pa_release_blocks(const int32_t* block_tables, int32_t max_blocks_per_seq,
+                            int32_t* held_blocks, const int32_t* keep_lens, int32_t num_seqs,
+                            int32_t* free_blocks, int32_t capacity, int32_t* free_count,
+                            int32_t block_size, int32_t num_blocks, int32_t* device_status,
+                            void* stream);
+
+/*
+ * pa_commit_tokens -- K and V of the accepted rows of a drafted tree moved to the
+ * slots behind the context, in the caches of num_layers layers.  (The pages
+ * verify no drafts and have no counterpart of this call.)
+ *
+ *   key_cache, value_cache  [num_layers, num_blocks, block_size, num_kv_heads,
+ *                  head_dim] of element_bytes each: 2 (bf16) or 1 (e4m3); moved bit for bit
+ *   context_lens, query_lens  [num_seqs] int32, as given to pa_plan_step
+ *   accepted       [num_seqs, max_accepted] int32: rows of the request, ascending
+ *                  (a path from a root down a tree whose parents come first is)
+ *   accept_lens    [num_seqs] int32: how many of them, 0 .. max_accepted
+ *   new_lens       optional [num_seqs] int32 (written): context_lens + accept_lens;
+ *                  may not overlap an input (PA_ERR_INVALID)
+ * The row at position context_lens[r] + i becomes the one at context_lens[r] +
+ * accepted[r][i].  Requests whose path, lengths or block ids are out of range
+ * are recorded and skipped (new_lens = context_lens).  num_kv_heads * head_dim *
+ * element_bytes a multiple of 16, any positive block_size; num_seqs == 0 or
+ * num_layers == 0 is a no-op.  Requests that move into a shared block race.
+ */
+pa_status pa_commit_tokens(void* key_cache, void* value_cache, int32_t num_layers,
+                           const int32_t* block_tables, int32_t max_blocks_per_seq,
+                           const int32_t* context_lens, const int32_t* query_lens,
+                           const int32_t* accepted, int32_t max_accepted,
+                           const int32_t* accept_lens, int32_t* new_lens, int32_t num_seqs,
+                           int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                           int32_t num_blocks, int32_t element_bytes, int32_t* device_status,
+                           void* stream);
 
 #ifdef __cplusplus
 }

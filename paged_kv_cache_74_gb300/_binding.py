@@ -21,7 +21,8 @@ _lib = None
 
 PA_OK, PA_ERR_INVALID, PA_ERR_UNSUPPORTED, PA_ERR_WORKSPACE, PA_ERR_CUDA = range(5)
 DEVICE_ERRORS = {0: "ok", 1: "bad slot", 2: "bad block id", 3: "bad seq_len",
-                 4: "bad query length", 5: "wait timeout", 6: "bad rotation position"}
+                 4: "bad query length", 5: "wait timeout", 6: "bad rotation position",
+                 7: "out of blocks", 8: "bad tree parent", 9: "bad held block count", 10: "bad accepted path"}
 ABI_SYMBOLS = ("pa_status_string", "pa_abi_version", "pa_reshape_and_cache",
                "pa_compute_slot_mapping", "pa_decode_workspace_size", "pa_decode",
                "pa_prefill_workspace_size", "pa_prefill_varlen", "pa_decode_noalloc",
@@ -30,7 +31,7 @@ ABI_SYMBOLS = ("pa_status_string", "pa_abi_version", "pa_reshape_and_cache",
                "pa_reshape_and_cache_xsplit_fp8", "pa_decode_xsplit_fp8", "pa_prefill_varlen_fp8",
                "pa_qk_norm_rope_append", "pa_qk_norm_rope_append_fp8", "pa_decode_masked",
                "pa_decode_masked_fp8", "pa_prefill_masked_workspace_size", "pa_prefill_varlen_masked",
-               "pa_prefill_varlen_masked_fp8")
+               "pa_prefill_varlen_masked_fp8", "pa_plan_step", "pa_release_blocks", "pa_commit_tokens")
 
 
 class PAError(RuntimeError):
@@ -112,6 +113,13 @@ def _declare(lib):
     lib.pa_prefill_varlen_masked.argtypes = pre + [_f32, _vp, _vp, _vp, _vp, _sz, _vp]
     lib.pa_prefill_varlen_masked_fp8.restype = ctypes.c_int
     lib.pa_prefill_varlen_masked_fp8.argtypes = pre + [_f32, _f32, _f32, _vp, _vp, _vp, _vp, _sz, _vp]
+    lib.pa_plan_step.restype = ctypes.c_int
+    lib.pa_plan_step.argtypes = [_vp, _i32, _vp, _vp, _vp, _i32, _vp, _i32, _vp, _i32, _i32, _vp, _vp, _vp, _vp,
+                                 _i32, _vp, _vp, _i32, _vp, _vp]
+    lib.pa_release_blocks.restype = ctypes.c_int
+    lib.pa_release_blocks.argtypes = [_vp, _i32, _vp, _vp, _i32, _vp, _i32, _vp, _i32, _i32, _vp, _vp]
+    lib.pa_commit_tokens.restype = ctypes.c_int
+    lib.pa_commit_tokens.argtypes = [_vp, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _i32, _vp, _vp] + [_i32] * 6 + [_vp, _vp]
     return lib
 
 
@@ -774,6 +782,111 @@ def prefill_varlen_masked_fp8(q, key_cache, value_cache, query_start_loc, seq_le
                            key_cache, value_cache, query_start_loc, seq_lens, block_tables,
                            max_query_len, max_seq_len, scale, softcap, slopes, key_starts, prefix_lens,
                            out, workspace)
+
+
+def _lens(S, *named):
+    for name, t in named:
+        if t.numel() != S:
+            raise ValueError(f"{name} must be [{S}]")
+
+
+def _status4(status):
+    if status is not None and status.numel() < 4:
+        raise ValueError("status must hold 4 values")
+
+
+def plan_step(block_tables, held_blocks, context_lens, query_lens, free_blocks, free_count, block_size,
+              num_blocks, query_start_loc, seq_lens, slot_mapping, positions, parents=None, tree_masks=None,
+              status=None):
+    """The step's bookkeeping on the device, from the requests' lengths (int32 [S]):
+    new blocks off the end of free_blocks [capacity] (free_count [1] of them valid)
+    into block_tables [S, max_blocks] behind held_blocks [S]; query_start_loc
+    [S + 1], seq_lens [S], slot_mapping (int64) and positions (int32) [max_tokens];
+    with tree_masks (int64 [max_tokens, words] or [max_tokens]) the ancestors' bits of
+    each row, from parents [max_tokens] (-1: follows the context; None: a chain).
+    Returns (query_start_loc, seq_lens, slot_mapping, positions, tree_masks)."""
+    dev = _device_of("block_tables", block_tables)
+    i32, i64 = torch.int32, torch.int64
+    _check_all(dev, (("block_tables", block_tables, i32), ("held_blocks", held_blocks, i32),
+                     ("context_lens", context_lens, i32), ("query_lens", query_lens, i32),
+                     ("free_blocks", free_blocks, i32), ("free_count", free_count, i32),
+                     ("query_start_loc", query_start_loc, i32), ("seq_lens", seq_lens, i32),
+                     ("slot_mapping", slot_mapping, i64), ("positions", positions, i32)),
+               (("parents", parents, i32), ("tree_masks", tree_masks, i64), ("status", status, i32)))
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be [num_seqs, max_blocks]")
+    S, T = block_tables.shape[0], slot_mapping.numel()
+    _lens(S, ("held_blocks", held_blocks), ("context_lens", context_lens), ("query_lens", query_lens),
+          ("seq_lens", seq_lens))
+    _lens(T, ("positions", positions))
+    if query_start_loc.numel() != S + 1 or free_count.numel() != 1:
+        raise ValueError(f"query_start_loc must be [{S + 1}] and free_count [1]")
+    if parents is not None and parents.numel() != T:
+        raise ValueError(f"parents must be [{T}]")
+    words = 0
+    if tree_masks is not None:
+        words = tree_masks.shape[1] if tree_masks.dim() == 2 else 1
+        if tree_masks.dim() not in (1, 2) or tree_masks.shape[0] != T:
+            raise ValueError(f"tree_masks must be [{T}, words]")
+    _status4(status)
+    _launch("pa_plan_step", dev, block_tables.data_ptr(), block_tables.shape[1], held_blocks.data_ptr(),
+            context_lens.data_ptr(), query_lens.data_ptr(), S, free_blocks.data_ptr(), free_blocks.numel(),
+            free_count.data_ptr(), int(block_size), int(num_blocks), query_start_loc.data_ptr(),
+            seq_lens.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(), T, _addr(parents),
+            _addr(tree_masks), words, _addr(status))
+    return query_start_loc, seq_lens, slot_mapping, positions, tree_masks
+
+
+def release_blocks(block_tables, held_blocks, keep_lens, free_blocks, free_count, block_size, num_blocks,
+                   status=None):
+    """Gives the blocks of each request behind its first keep_lens [S] tokens (0: all)
+    back to the list of plan_step; held_blocks becomes what is left."""
+    dev = _device_of("block_tables", block_tables)
+    i32 = torch.int32
+    _check_all(dev, (("block_tables", block_tables, i32), ("held_blocks", held_blocks, i32),
+                     ("keep_lens", keep_lens, i32), ("free_blocks", free_blocks, i32),
+                     ("free_count", free_count, i32)), (("status", status, i32),))
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be [num_seqs, max_blocks]")
+    S = block_tables.shape[0]
+    _lens(S, ("held_blocks", held_blocks), ("keep_lens", keep_lens))
+    _lens(1, ("free_count", free_count))
+    _status4(status)
+    _launch("pa_release_blocks", dev, block_tables.data_ptr(), block_tables.shape[1], held_blocks.data_ptr(),
+            keep_lens.data_ptr(), S, free_blocks.data_ptr(), free_blocks.numel(), free_count.data_ptr(),
+            int(block_size), int(num_blocks), _addr(status))
+
+
+def commit_tokens(key_cache, value_cache, block_tables, context_lens, query_lens, accepted, accept_lens,
+                  new_lens=None, status=None):
+    """Moves K and V of the accepted rows (accepted int32 [S, max_accepted], ascending,
+    the first accept_lens [S] of them) to the slots behind context_lens [S], in caches
+    [num_blocks, block, kv_heads, head_dim] or [layers, num_blocks, ..] (bf16 or
+    uint8).  Returns new_lens [S] = context_lens + accept_lens."""
+    dev = _device_of("key_cache", key_cache)
+    i32 = torch.int32
+    dtype = torch.uint8 if key_cache.dtype is torch.uint8 else torch.bfloat16
+    _check_all(dev, (("key_cache", key_cache, dtype), ("value_cache", value_cache, dtype),
+                     ("block_tables", block_tables, i32), ("context_lens", context_lens, i32),
+                     ("query_lens", query_lens, i32), ("accepted", accepted, i32),
+                     ("accept_lens", accept_lens, i32)), (("new_lens", new_lens, i32), ("status", status, i32)))
+    if key_cache.dim() not in (4, 5) or value_cache.shape != key_cache.shape:
+        raise ValueError("key_cache and value_cache must be [(layers,) num_blocks, block, kv_heads, head_dim]")
+    layers = key_cache.shape[0] if key_cache.dim() == 5 else 1
+    nb, bs, hkv, d = key_cache.shape[-4:]
+    if block_tables.dim() != 2 or accepted.dim() != 2 or accepted.shape[0] != block_tables.shape[0]:
+        raise ValueError("block_tables must be [num_seqs, max_blocks] and accepted [num_seqs, max_accepted]")
+    S = block_tables.shape[0]
+    _lens(S, ("context_lens", context_lens), ("query_lens", query_lens), ("accept_lens", accept_lens))
+    if new_lens is None:
+        new_lens = torch.empty_like(context_lens)
+    _lens(S, ("new_lens", new_lens))
+    _status4(status)
+    _launch("pa_commit_tokens", dev, key_cache.data_ptr(), value_cache.data_ptr(), layers, block_tables.data_ptr(),
+            block_tables.shape[1], context_lens.data_ptr(), query_lens.data_ptr(), accepted.data_ptr(),
+            accepted.shape[1], accept_lens.data_ptr(), new_lens.data_ptr(), S, hkv, d, bs, nb,
+            key_cache.element_size(), _addr(status))
+    return new_lens
 
 
 def device_status(workspace_or_status):

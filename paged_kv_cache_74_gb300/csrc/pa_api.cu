@@ -617,6 +617,23 @@ NormRopeArgs norm_rope_args(void* q_out, const void* q, const void* key, const v
   return a;
 }
 
+// Whether any of the written ranges shares bytes with another range.
+struct Range {
+  const void* base;
+  size_t bytes;
+  bool written;
+};
+template <size_t N>
+bool ranges_clash(const Range (&r)[N]) {
+  for (size_t i = 0; i < N; ++i)
+    for (size_t j = i + 1; j < N; ++j) {
+      if (!r[i].base || !r[j].base || (!r[i].written && !r[j].written)) continue;
+      const uintptr_t a = reinterpret_cast<uintptr_t>(r[i].base), b = reinterpret_cast<uintptr_t>(r[j].base);
+      if (a < b + r[j].bytes && b < a + r[i].bytes) return true;
+    }
+  return false;
+}
+
 }  // namespace
 }  // namespace pa
 
@@ -1234,5 +1251,156 @@ pa_status pa_prefill_varlen_fp8(void* out, const void* q, const void* key_cache,
                              workspace, workspace_bytes, stream, kv);
 }
 
+pa_status pa_plan_step(int32_t* block_tables, int32_t max_blocks_per_seq, int32_t* held_blocks,
+                       const int32_t* context_lens, const int32_t* query_lens, int32_t num_seqs,
+                       const int32_t* free_blocks, int32_t capacity, int32_t* free_count,
+                       int32_t block_size, int32_t num_blocks, int32_t* query_start_loc,
+                       int32_t* seq_lens, int64_t* slot_mapping, int32_t* positions,
+                       int32_t max_tokens, const int32_t* parents, void* tree_masks,
+                       int32_t mask_words, int32_t* device_status, void* stream) {
+  if (num_seqs < 0 || max_blocks_per_seq < 1 || capacity < 1 || block_size < 1 || num_blocks < 1 || max_tokens < 0)
+    return PA_ERR_INVALID;
+  if (tree_masks ? mask_words < 1 : mask_words != 0) return PA_ERR_INVALID;
+  if (num_seqs > 65535 || mask_words > kMaxMaskWords) return PA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(max_blocks_per_seq) * block_size > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
+  if (!free_blocks || !free_count || !query_start_loc) return PA_ERR_INVALID;
+  if (num_seqs > 0 && (!block_tables || !held_blocks || !context_lens || !query_lens || !seq_lens))
+    return PA_ERR_INVALID;
+  if (max_tokens > 0 && (!slot_mapping || !positions)) return PA_ERR_INVALID;
+  const void* words[] = {block_tables, held_blocks, context_lens, query_lens, free_blocks, free_count,
+                         query_start_loc, seq_lens, positions, parents, device_status};
+  for (const void* p : words)
+    if (!aligned(p, 4)) return PA_ERR_INVALID;
+  if (!aligned(slot_mapping, 8) || !aligned(tree_masks, 8)) return PA_ERR_INVALID;
+  const size_t s = static_cast<size_t>(num_seqs), t = static_cast<size_t>(max_tokens);
+  const Range ranges[] = {{block_tables, s * max_blocks_per_seq * 4, true},
+                          {held_blocks, s * 4, true},
+                          {context_lens, s * 4, false},
+                          {query_lens, s * 4, false},
+                          {free_blocks, static_cast<size_t>(capacity) * 4, false},
+                          {free_count, 4, true},
+                          {query_start_loc, (s + 1) * 4, true},
+                          {seq_lens, s * 4, true},
+                          {slot_mapping, t * 8, true},
+                          {positions, t * 4, true},
+                          {parents, t * 4, false},
+                          {tree_masks, t * mask_words * 8, true},
+                          {device_status, 16, true}};
+  if (ranges_clash(ranges)) return PA_ERR_INVALID;
+  PlanStepArgs a;
+  a.block_tables = block_tables;
+  a.held_blocks = held_blocks;
+  a.context_lens = context_lens;
+  a.query_lens = query_lens;
+  a.free_blocks = free_blocks;
+  a.free_count = free_count;
+  a.query_start_loc = query_start_loc;
+  a.seq_lens = seq_lens;
+  a.slot_mapping = slot_mapping;
+  a.positions = positions;
+  a.parents = parents;
+  a.tree_masks = static_cast<unsigned long long*>(tree_masks);
+  a.status = device_status;
+  a.words = mask_words;
+  a.capacity = capacity;
+  a.num_seqs = num_seqs;
+  a.max_tokens = max_tokens;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.block_size = block_size;
+  a.num_blocks = num_blocks;
+  return launch_plan_step(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+pa_status pa_release_blocks(const int32_t* block_tables, int32_t max_blocks_per_seq,
+                            int32_t* held_blocks, const int32_t* keep_lens, int32_t num_seqs,
+                            int32_t* free_blocks, int32_t capacity, int32_t* free_count,
+                            int32_t block_size, int32_t num_blocks, int32_t* device_status,
+                            void* stream) {
+  if (num_seqs < 0 || max_blocks_per_seq < 1 || capacity < 1 || block_size < 1 || num_blocks < 1)
+    return PA_ERR_INVALID;
+  if (num_seqs > 65535) return PA_ERR_UNSUPPORTED;
+  if (num_seqs == 0) return PA_OK;
+  if (!block_tables || !held_blocks || !keep_lens || !free_blocks || !free_count) return PA_ERR_INVALID;
+  const void* words[] = {block_tables, held_blocks, keep_lens, free_blocks, free_count, device_status};
+  for (const void* p : words)
+    if (!aligned(p, 4)) return PA_ERR_INVALID;
+  const size_t s = static_cast<size_t>(num_seqs);
+  const Range ranges[] = {{block_tables, s * max_blocks_per_seq * 4, false},
+                          {held_blocks, s * 4, true},
+                          {keep_lens, s * 4, false},
+                          {free_blocks, static_cast<size_t>(capacity) * 4, true},
+                          {free_count, 4, true},
+                          {device_status, 16, true}};
+  if (ranges_clash(ranges)) return PA_ERR_INVALID;
+  ReleaseArgs a;
+  a.block_tables = block_tables;
+  a.held_blocks = held_blocks;
+  a.keep_lens = keep_lens;
+  a.free_blocks = free_blocks;
+  a.free_count = free_count;
+  a.status = device_status;
+  a.capacity = capacity;
+  a.num_seqs = num_seqs;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.block_size = block_size;
+  a.num_blocks = num_blocks;
+  return launch_release_blocks(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+pa_status pa_commit_tokens(void* key_cache, void* value_cache, int32_t num_layers,
+                           const int32_t* block_tables, int32_t max_blocks_per_seq,
+                           const int32_t* context_lens, const int32_t* query_lens,
+                           const int32_t* accepted, int32_t max_accepted,
+                           const int32_t* accept_lens, int32_t* new_lens, int32_t num_seqs,
+                           int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                           int32_t num_blocks, int32_t element_bytes, int32_t* device_status,
+                           void* stream) {
+  if (num_seqs < 0 || num_layers < 0 || max_blocks_per_seq < 1 || max_accepted < 1 || num_kv_heads < 1 ||
+      head_dim < 1 || block_size < 1 || num_blocks < 1)
+    return PA_ERR_INVALID;
+  const int64_t row_elems = static_cast<int64_t>(num_kv_heads) * head_dim;
+  if ((element_bytes != 1 && element_bytes != 2) || row_elems > (1 << 20) || row_elems * element_bytes % 16 != 0 ||
+      num_seqs > 65535 || num_layers > 65535)
+    return PA_ERR_UNSUPPORTED;
+  if (num_seqs == 0 || num_layers == 0) return PA_OK;
+  if (!key_cache || !value_cache || !block_tables || !context_lens || !query_lens || !accepted || !accept_lens)
+    return PA_ERR_INVALID;
+  if (!aligned(key_cache, 16) || !aligned(value_cache, 16)) return PA_ERR_INVALID;
+  const void* words[] = {block_tables, context_lens, query_lens, accepted, accept_lens, new_lens, device_status};
+  for (const void* p : words)
+    if (!aligned(p, 4)) return PA_ERR_INVALID;
+  const int64_t layer_chunks = row_elems * element_bytes / 16 * block_size * num_blocks;
+  const size_t s = static_cast<size_t>(num_seqs);
+  const size_t cache_bytes = static_cast<size_t>(layer_chunks) * 16 * num_layers;
+  const Range ranges[] = {{key_cache, cache_bytes, true},
+                          {value_cache, cache_bytes, true},
+                          {block_tables, s * max_blocks_per_seq * 4, false},
+                          {context_lens, s * 4, false},
+                          {query_lens, s * 4, false},
+                          {accepted, s * max_accepted * 4, false},
+                          {accept_lens, s * 4, false},
+                          {new_lens, s * 4, true},
+                          {device_status, 16, true}};
+  if (ranges_clash(ranges)) return PA_ERR_INVALID;
+  CommitArgs a;
+  a.key_cache = static_cast<uint4*>(key_cache);
+  a.value_cache = static_cast<uint4*>(value_cache);
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.query_lens = query_lens;
+  a.accepted = accepted;
+  a.accept_lens = accept_lens;
+  a.new_lens = new_lens;
+  a.status = device_status;
+  a.layer_chunks = layer_chunks;
+  a.row_chunks = static_cast<int>(row_elems * element_bytes / 16);
+  a.num_layers = num_layers;
+  a.num_seqs = num_seqs;
+  a.max_accepted = max_accepted;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.block_size = block_size;
+  a.num_blocks = num_blocks;
+  return launch_commit_tokens(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
 
 }  // extern "C"

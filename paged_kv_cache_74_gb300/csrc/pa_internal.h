@@ -274,4 +274,51 @@ struct NormRopeArgs {
 cudaError_t launch_qk_norm_rope(NormRopeArgs a, int head_dim, bool kv8, bool interleaved,
                                 cudaStream_t stream);
 
+// Blocks, tables, slots and tree masks of a step (step_plan.cu).
+constexpr int kMaxMaskWords = 4;    // 64-bit words of a tree row's mask: 256 nodes
+struct PlanStepArgs {
+  int32_t* block_tables;            // [num_seqs, max_blocks_per_seq]
+  int32_t* held_blocks;             // [num_seqs] valid entries of each row
+  const int32_t* context_lens;      // [num_seqs]
+  const int32_t* query_lens;        // [num_seqs]
+  const int32_t* free_blocks;       // [capacity], free_count of them valid
+  int32_t* free_count;
+  int32_t* query_start_loc;         // [num_seqs + 1]
+  int32_t* seq_lens;                // [num_seqs]
+  int64_t* slot_mapping;            // [max_tokens]
+  int32_t* positions;               // [max_tokens]
+  const int32_t* parents;           // [max_tokens] or nullptr: chains
+  unsigned long long* tree_masks;   // [max_tokens, words], words > 0
+  int32_t* status;
+  int words, capacity, num_seqs, max_tokens, max_blocks_per_seq, block_size, num_blocks;
+};
+cudaError_t launch_plan_step(const PlanStepArgs& a, cudaStream_t stream);
+
+struct ReleaseArgs {
+  const int32_t* block_tables;
+  int32_t* held_blocks;
+  const int32_t* keep_lens;         // [num_seqs] tokens that stay
+  int32_t* free_blocks;
+  int32_t* free_count;
+  int32_t* status;
+  int capacity, num_seqs, max_blocks_per_seq, block_size, num_blocks;
+};
+cudaError_t launch_release_blocks(const ReleaseArgs& a, cudaStream_t stream);
+
+// Accepted tokens moved behind the context (commit_tokens.cu).
+struct CommitArgs {
+  uint4* key_cache;                 // [num_layers][layer_chunks], rows of row_chunks 16-byte chunks
+  uint4* value_cache;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  const int32_t* query_lens;
+  const int32_t* accepted;          // [num_seqs, max_accepted]
+  const int32_t* accept_lens;       // [num_seqs]
+  int32_t* new_lens;                // optional output
+  int32_t* status;
+  int64_t layer_chunks;
+  int row_chunks, num_layers, num_seqs, max_accepted, max_blocks_per_seq, block_size, num_blocks;
+};
+cudaError_t launch_commit_tokens(const CommitArgs& a, cudaStream_t stream);
+
 }  // namespace pa
