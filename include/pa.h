@@ -733,6 +733,65 @@ pa_status pa_release_blocks(const int32_t* block_tables, int32_t max_blocks_per_
                             void* stream);
 
 /*
+ * pa_tree_workspace_size -- bytes of workspace pa_tree_attention needs (status
+ * record and the partial records of units cut between CTAs), on the current device.
+ * No part of it needs initialising.  Returns 0 for invalid arguments.
+ */
+size_t pa_tree_workspace_size(int32_t num_seqs, int32_t total_q, int32_t num_heads,
+                              int32_t num_kv_heads, int32_t head_dim, int32_t max_seq_len);
+
+/*
+ * pa_tree_attention -- attention of the drafted tokens of each request, a tree (or
+ * several) behind its context, over the paged cache: the verification of a
+ * speculative step.  (The pages' batches are chains; the call is
+ * pa_prefill_varlen's neighbour for drafts that branch.)
+ *
+ *   out, q          [total_q, num_heads, head_dim] bf16
+ *   query_start_loc [num_seqs + 1] int32, seq_lens [num_seqs] int32: request r's rows
+ *                   and its keys, the rows' own among them (K and V of all rows must be in
+ *                   the cache, at positions seq_lens[r] - q_len ..: pa_plan_step's slots)
+ *   tree_masks      [total_q, mask_words] 64-bit words, mask_words 1 to 4: bit k of a row:
+ *                   it sees row k of its request.  Any mask is allowed; bits behind
+ *                   the request's rows are ignored
+ *   max_query_len, max_seq_len  host-side upper bounds; max_query_len <= 64 * mask_words
+ * Row i sees keys 0 .. seq_lens[r] - q_len - 1 and those of the rows its mask names
+ * (itself too only if named).  A row that sees no key gives zeros.  Keys that no
+ * row of the request sees may hold anything (NaN and infinities included); V of
+ * a key that some row sees must be finite.  Rows of the batch that no request owns
+ * are left as they are.  Exact attention with fp32 accumulation as pa_prefill_varlen:
+ * tcgen05 products, weights rounded to bf16, one rounding of the result.  Up to 256 query
+ * rows (q_len * num_heads / num_kv_heads) share each read of the keys.
+ * Two kernels on `stream`: the attention, and the merge of what it has cut between
+ * CTAs (not when max_seq_len <= 128).  Results depend on the batch alone.
+ * Block tables, sizes, workspace alignment and errors as pa_prefill_varlen; a request with
+ * q_len > max_query_len, > seq_len or > 64 * mask_words is skipped with
+ * PA_DEV_BAD_QUERY_LEN.
+ */
+pa_status pa_tree_attention(void* out, const void* q, const void* key_cache,
+                            const void* value_cache, const int32_t* query_start_loc,
+                            const int32_t* seq_lens, int32_t num_seqs, int32_t total_q,
+                            int32_t max_query_len, int32_t max_seq_len,
+                            const int32_t* block_tables, int32_t max_blocks_per_seq,
+                            const void* tree_masks, int32_t mask_words, int32_t num_heads,
+                            int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                            int32_t num_blocks, float scale, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/*
+ * pa_tree_attention_fp8 -- pa_tree_attention over e4m3 caches, as pa_prefill_varlen_fp8
+ * is to pa_prefill_varlen (f16 products; q saturates at +-65504).
+ */
+pa_status pa_tree_attention_fp8(void* out, const void* q, const void* key_cache,
+                                const void* value_cache, const int32_t* query_start_loc,
+                                const int32_t* seq_lens, int32_t num_seqs, int32_t total_q,
+                                int32_t max_query_len, int32_t max_seq_len,
+                                const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                const void* tree_masks, int32_t mask_words, int32_t num_heads,
+                                int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                int32_t num_blocks, float scale, float k_scale, float v_scale,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * pa_commit_tokens -- K and V of the accepted rows of a drafted tree moved to the
  * slots behind the context, in the caches of num_layers layers.  (The pages
  * verify no drafts and have no counterpart of this call.)

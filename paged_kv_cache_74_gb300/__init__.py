@@ -12,7 +12,7 @@ from ._binding import (ABI_SYMBOLS, DEVICE_ERRORS, PAError, append_tokens, commi
                       prefill_varlen, prefill_varlen_fp8, prefill_varlen_masked, prefill_varlen_masked_fp8,
                       prefill_workspace_size, qk_norm_rope_append, qk_norm_rope_append_fp8, release_blocks,
                       reshape_and_cache, reshape_and_cache_fp8, reshape_and_cache_xsplit,
-                      reshape_and_cache_xsplit_fp8)
+                      reshape_and_cache_xsplit_fp8, tree_attention, tree_attention_fp8, tree_workspace_size)
 from .builder import build
 
 __all__ = ["ABI_SYMBOLS", "DEVICE_ERRORS", "PAError", "append_tokens", "build", "commit_tokens",
@@ -22,4 +22,5 @@ __all__ = ["ABI_SYMBOLS", "DEVICE_ERRORS", "PAError", "append_tokens", "build", 
            "prefill_masked_workspace_size", "prefill_varlen", "prefill_varlen_fp8", "prefill_varlen_masked",
            "prefill_varlen_masked_fp8", "prefill_workspace_size", "qk_norm_rope_append",
            "qk_norm_rope_append_fp8", "release_blocks", "reshape_and_cache", "reshape_and_cache_fp8",
-           "reshape_and_cache_xsplit", "reshape_and_cache_xsplit_fp8"]
+           "reshape_and_cache_xsplit", "reshape_and_cache_xsplit_fp8",
+           "tree_attention", "tree_attention_fp8", "tree_workspace_size"]

@@ -31,7 +31,8 @@ ABI_SYMBOLS = ("pa_status_string", "pa_abi_version", "pa_reshape_and_cache",
                "pa_reshape_and_cache_xsplit_fp8", "pa_decode_xsplit_fp8", "pa_prefill_varlen_fp8",
                "pa_qk_norm_rope_append", "pa_qk_norm_rope_append_fp8", "pa_decode_masked",
                "pa_decode_masked_fp8", "pa_prefill_masked_workspace_size", "pa_prefill_varlen_masked",
-               "pa_prefill_varlen_masked_fp8", "pa_plan_step", "pa_release_blocks", "pa_commit_tokens")
+               "pa_prefill_varlen_masked_fp8", "pa_plan_step", "pa_release_blocks", "pa_commit_tokens",
+               "pa_tree_workspace_size", "pa_tree_attention", "pa_tree_attention_fp8")
 
 
 class PAError(RuntimeError):
@@ -120,6 +121,13 @@ def _declare(lib):
     lib.pa_release_blocks.argtypes = [_vp, _i32, _vp, _vp, _i32, _vp, _i32, _vp, _i32, _i32, _vp, _vp]
     lib.pa_commit_tokens.restype = ctypes.c_int
     lib.pa_commit_tokens.argtypes = [_vp, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _i32, _vp, _vp] + [_i32] * 6 + [_vp, _vp]
+    lib.pa_tree_workspace_size.restype = _sz
+    lib.pa_tree_workspace_size.argtypes = [_i32] * 6
+    tree = [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _i32, _vp] + [_i32] * 6 + [_f32]
+    lib.pa_tree_attention.restype = ctypes.c_int
+    lib.pa_tree_attention.argtypes = tree + [_vp, _sz, _vp]
+    lib.pa_tree_attention_fp8.restype = ctypes.c_int
+    lib.pa_tree_attention_fp8.argtypes = tree + [_f32, _f32, _vp, _sz, _vp]
     return lib
 
 
@@ -782,6 +790,55 @@ def prefill_varlen_masked_fp8(q, key_cache, value_cache, query_start_loc, seq_le
                            key_cache, value_cache, query_start_loc, seq_lens, block_tables,
                            max_query_len, max_seq_len, scale, softcap, slopes, key_starts, prefix_lens,
                            out, workspace)
+
+
+def tree_workspace_size(num_seqs, total_q, num_heads, num_kv_heads, head_dim, max_seq_len):
+    return int(load_library().pa_tree_workspace_size(num_seqs, total_q, num_heads, num_kv_heads, head_dim,
+                                                     max_seq_len))
+
+
+def _tree_attention(fn, cache_dtype, scales, q, key_cache, value_cache, query_start_loc, seq_lens,
+                    block_tables, tree_masks, max_query_len, max_seq_len, scale, out, workspace):
+    dev, out = _attention_args(q, key_cache, value_cache, cache_dtype, block_tables, seq_lens, out, None,
+                               None, None, workspace, query_start_loc)
+    if not isinstance(tree_masks, torch.Tensor) or tree_masks.dtype is not torch.int64 or \
+            tree_masks.get_device() != dev or not tree_masks.is_contiguous():
+        _refuse("tree_masks", tree_masks, torch.int64, dev)
+    tq, hq, d = q.shape
+    nb, bs, hkv, _ = key_cache.shape
+    S = seq_lens.shape[0]
+    if query_start_loc is None or query_start_loc.numel() != S + 1:
+        raise ValueError(f"query_start_loc must be [{S + 1}]")
+    if tree_masks.dim() not in (1, 2) or tree_masks.shape[0] != tq:
+        raise ValueError(f"tree_masks must be [{tq}, words]")
+    words = tree_masks.shape[1] if tree_masks.dim() == 2 else 1
+    if workspace is None:
+        with torch.cuda.device(dev):
+            workspace = new_workspace(tree_workspace_size(S, tq, hq, hkv, d, max_seq_len), q.device)
+    _launch(fn, dev, out.data_ptr(), q.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
+            query_start_loc.data_ptr(), seq_lens.data_ptr(), S, tq, int(max_query_len), int(max_seq_len),
+            block_tables.data_ptr(), block_tables.shape[1], tree_masks.data_ptr(), words, hq, hkv, d, bs, nb,
+            float(scale), *scales, workspace.data_ptr(), workspace.numel())
+    return out
+
+
+def tree_attention(q, key_cache, value_cache, query_start_loc, seq_lens, block_tables, tree_masks,
+                   max_query_len, max_seq_len, scale, out=None, workspace=None):
+    """Attention of drafted token trees; q [total_q, Hq, d] packed by query_start_loc.
+    A row sees its request's context (the seq_len - q_len keys before the rows') and
+    the rows named by its bits of tree_masks (int64 [total_q, words] or [total_q], as
+    plan_step writes them).  A row that sees no key gives zeros."""
+    return _tree_attention("pa_tree_attention", torch.bfloat16, (), q, key_cache, value_cache,
+                           query_start_loc, seq_lens, block_tables, tree_masks, max_query_len, max_seq_len,
+                           scale, out, workspace)
+
+
+def tree_attention_fp8(q, key_cache, value_cache, query_start_loc, seq_lens, block_tables, tree_masks,
+                       max_query_len, max_seq_len, scale, k_scale, v_scale, out=None, workspace=None):
+    """tree_attention over e4m3 caches (uint8 [nb, bs, Hkv, d]) with their scales."""
+    return _tree_attention("pa_tree_attention_fp8", torch.uint8, (float(k_scale), float(v_scale)), q, key_cache,
+                           value_cache, query_start_loc, seq_lens, block_tables, tree_masks, max_query_len,
+                           max_seq_len, scale, out, workspace)
 
 
 def _lens(S, *named):

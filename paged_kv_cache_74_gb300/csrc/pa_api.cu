@@ -131,17 +131,17 @@ bool make_sw128_map(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// q [rows][heads][head_dim] for the tensor-core decode: box {64, group, 1}
-// (one 128-byte row per q head of a kv head).
+// q [rows][heads][head_dim] for the tensor-core decode: box {64, group, box_rows}
+// (one 128-byte row per q head of a kv head and q row).
 bool make_q_group_map(CUtensorMap* map, const void* q, int rows, int num_heads, int head_dim,
-                      int group) {
+                      int group, int box_rows = 1) {
   EncodeTiledFn enc = encode_tiled_fn();
   if (enc == nullptr) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(num_heads),
                               static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_dim) * 2,
                                  static_cast<cuuint64_t>(num_heads) * head_dim * 2};
-  const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(group), 1u};
+  const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(group), static_cast<cuuint32_t>(box_rows)};
   const cuuint32_t estr[3] = {1u, 1u, 1u};
   std::memset(map, 0, sizeof(*map));
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, estr,
@@ -615,6 +615,93 @@ NormRopeArgs norm_rope_args(void* q_out, const void* q, const void* key, const v
   a.num_blocks = num_blocks;
   a.warps_per_token = 1;
   return a;
+}
+
+// Workspace of pa_tree_attention: status record | cut units | partial (m, l) | partial O.
+struct TreeLayout {
+  int num_ctas = 0;
+  size_t splits_offset = 0, ml_offset = 0, o_offset = 0, total = 0;
+};
+
+TreeLayout tree_layout(int num_seqs, int total_q, int num_heads, int num_kv_heads, int head_dim, int max_seq_len) {
+  TreeLayout L;
+  int sms = sm_count_current_device();
+  if (sms <= 0) sms = 148;
+  // One CTA per SM, no more than there are 128-key steps (slot_nodes nodes a slot, two slots a unit).
+  const int slot_nodes = 128 / (num_heads / num_kv_heads);
+  const int64_t units = (static_cast<int64_t>(num_seqs) + total_q / (2 * slot_nodes)) * num_kv_heads;
+  const int64_t steps = units * ceil_div(max_seq_len, 128);
+  L.num_ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sms, steps)));
+  size_t off = kWorkspaceHeader;
+  L.splits_offset = off;
+  off = align_up(off + static_cast<size_t>(L.num_ctas) * sizeof(TreeSplit), 256);
+  L.ml_offset = off;
+  off = align_up(off + static_cast<size_t>(L.num_ctas) * 2 * 2 * 128 * 2 * sizeof(float), 256);
+  L.o_offset = off;
+  off += static_cast<size_t>(L.num_ctas) * tree_record_floats(head_dim) * sizeof(float);
+  L.total = align_up(off, 256);
+  return L;
+}
+
+pa_status tree_attention_impl(void* out, const void* q, const void* key_cache, const void* value_cache,
+                              const int32_t* query_start_loc, const int32_t* seq_lens, int32_t num_seqs,
+                              int32_t total_q, int32_t max_query_len, int32_t max_seq_len,
+                              const int32_t* block_tables, int32_t max_blocks_per_seq, const void* tree_masks,
+                              int32_t mask_words, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                              int32_t block_size, int32_t num_blocks, float scale, bool kv8, float k_scale,
+                              float v_scale, void* workspace, size_t workspace_bytes, void* stream) {
+  pa_status st = check_decode_args(out, q, key_cache, value_cache, block_tables, max_blocks_per_seq, seq_lens,
+                                   num_seqs, max_seq_len, num_heads, num_kv_heads, head_dim, block_size, num_blocks,
+                                   scale);
+  if (st != PA_OK) return st;
+  if (!query_start_loc || !aligned(query_start_loc, 4) || !tree_masks || !aligned(tree_masks, 8) || total_q < 0 ||
+      max_query_len < 0 || max_query_len > max_seq_len || mask_words < 1)
+    return PA_ERR_INVALID;
+  if (mask_words > kMaxMaskWords) return PA_ERR_UNSUPPORTED;
+  if (max_query_len > 64 * mask_words) return PA_ERR_INVALID;
+  if (num_seqs == 0 || total_q == 0 || max_query_len == 0) return PA_OK;
+  const TreeLayout L = tree_layout(num_seqs, total_q, num_heads, num_kv_heads, head_dim, max_seq_len);
+  if (!workspace || workspace_bytes < L.total) return PA_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return PA_ERR_INVALID;
+  TreeArgs a;
+  a.group = num_heads / num_kv_heads;
+  a.slot_nodes = 128 / a.group;
+  CUtensorMap qmap, kmap, vmap;
+  const int tiles = num_blocks * (block_size / kBlockSize);
+  const bool maps_ok =
+      make_q_group_map(&qmap, q, total_q, num_heads, head_dim, a.group, a.slot_nodes) &&
+      (kv8 ? make_cache_map_e4m3(&kmap, key_cache, tiles, num_kv_heads, head_dim, true) &&
+                 make_cache_map_e4m3(&vmap, value_cache, tiles, num_kv_heads, head_dim, true)
+           : make_kv_group_map(&kmap, key_cache, tiles, num_kv_heads, head_dim) &&
+                 make_kv_group_map(&vmap, value_cache, tiles, num_kv_heads, head_dim));
+  if (!maps_ok) return PA_ERR_CUDA;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.block_tables = block_tables;
+  a.seq_lens = seq_lens;
+  a.query_start_loc = query_start_loc;
+  a.masks = static_cast<const uint32_t*>(tree_masks);
+  a.status = static_cast<int32_t*>(workspace);
+  a.splits = reinterpret_cast<TreeSplit*>(ws + L.splits_offset);
+  a.part_ml = reinterpret_cast<float*>(ws + L.ml_offset);
+  a.part_o = reinterpret_cast<float*>(ws + L.o_offset);
+  a.words32 = 2 * mask_words;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.num_seqs = num_seqs;
+  a.num_heads = num_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.max_seq_len = max_seq_len;
+  a.max_query_len = max_query_len;
+  a.num_blocks = num_blocks;
+  a.block_size = block_size;
+  a.tile_shift = tile_shift_of(block_size);
+  a.total_q = total_q;
+  a.num_ctas = L.num_ctas;
+  a.scale_log2 = scale * k_scale * 1.4426950408889634f;
+  a.o_scale = v_scale;
+  return launch_tree_attention(a, qmap, kmap, vmap, head_dim, kv8, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
 }
 
 // Whether any of the written ranges shares bytes with another range.
@@ -1401,6 +1488,45 @@ pa_status pa_commit_tokens(void* key_cache, void* value_cache, int32_t num_layer
   a.block_size = block_size;
   a.num_blocks = num_blocks;
   return launch_commit_tokens(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+size_t pa_tree_workspace_size(int32_t num_seqs, int32_t total_q, int32_t num_heads,
+                              int32_t num_kv_heads, int32_t head_dim, int32_t max_seq_len) {
+  if (num_seqs < 0 || num_seqs > 65535 || total_q < 0 || max_seq_len < 1) return 0;
+  if (check_attention_shape(num_heads, num_kv_heads, head_dim, 16, 1) != PA_OK) return 0;
+  return tree_layout(num_seqs, total_q, num_heads, num_kv_heads, head_dim, max_seq_len).total;
+}
+
+pa_status pa_tree_attention(void* out, const void* q, const void* key_cache,
+                            const void* value_cache, const int32_t* query_start_loc,
+                            const int32_t* seq_lens, int32_t num_seqs, int32_t total_q,
+                            int32_t max_query_len, int32_t max_seq_len,
+                            const int32_t* block_tables, int32_t max_blocks_per_seq,
+                            const void* tree_masks, int32_t mask_words, int32_t num_heads,
+                            int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                            int32_t num_blocks, float scale, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  return tree_attention_impl(out, q, key_cache, value_cache, query_start_loc, seq_lens, num_seqs, total_q,
+                             max_query_len, max_seq_len, block_tables, max_blocks_per_seq, tree_masks, mask_words,
+                             num_heads, num_kv_heads, head_dim, block_size, num_blocks, scale, false, 1.f, 1.f,
+                             workspace, workspace_bytes, stream);
+}
+
+pa_status pa_tree_attention_fp8(void* out, const void* q, const void* key_cache,
+                                const void* value_cache, const int32_t* query_start_loc,
+                                const int32_t* seq_lens, int32_t num_seqs, int32_t total_q,
+                                int32_t max_query_len, int32_t max_seq_len,
+                                const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                const void* tree_masks, int32_t mask_words, int32_t num_heads,
+                                int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                int32_t num_blocks, float scale, float k_scale, float v_scale,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+  if (!(std::isfinite(k_scale) && k_scale > 0.f && std::isfinite(v_scale) && v_scale > 0.f))
+    return PA_ERR_INVALID;
+  return tree_attention_impl(out, q, key_cache, value_cache, query_start_loc, seq_lens, num_seqs, total_q,
+                             max_query_len, max_seq_len, block_tables, max_blocks_per_seq, tree_masks, mask_words,
+                             num_heads, num_kv_heads, head_dim, block_size, num_blocks, scale, true, k_scale,
+                             v_scale, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

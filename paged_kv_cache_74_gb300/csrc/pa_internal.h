@@ -305,6 +305,31 @@ struct ReleaseArgs {
 };
 cudaError_t launch_release_blocks(const ReleaseArgs& a, cudaStream_t stream);
 
+// Attention of drafted token trees (tree_attention.cu).  qmap = q as {head_dim, heads,
+// rows} with a {64, group, slot_nodes} box, kmap and vmap as the prefill's.
+struct TreeSplit {                  // the unit that a CTA begins and later ones finish
+  int c1;                           // its last CTA; -1: none
+  int row0, nodes, kvh;             // its first q row, nodes and kv head
+};
+struct TreeArgs {
+  __nv_bfloat16* out;               // [total_q, num_heads, D]
+  const int32_t* block_tables;
+  const int32_t* seq_lens;
+  const int32_t* query_start_loc;
+  const uint32_t* masks;            // [total_q, words32] ancestors' bits
+  int32_t* status;
+  TreeSplit* splits;                // [num_ctas]
+  float* part_ml;                   // [num_ctas][2 pieces][2 slots][128 rows][2]  (m in log2 units, l)
+  float* part_o;                    // [num_ctas][2][2][D / 4][128][4]  unnormalised O
+  int words32, max_blocks_per_seq, num_seqs, num_heads, num_kv_heads, group;
+  int slot_nodes;                   // nodes of a 128-row tile: 128 / group
+  int max_seq_len, max_query_len, num_blocks, block_size, tile_shift, total_q, num_ctas;
+  float scale_log2, o_scale;        // as PrefillArgs
+};
+size_t tree_record_floats(int head_dim);  // of part_o, per CTA
+cudaError_t launch_tree_attention(const TreeArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
+                                  const CUtensorMap& vmap, int head_dim, bool kv8, cudaStream_t stream);
+
 // Accepted tokens moved behind the context (commit_tokens.cu).
 struct CommitArgs {
   uint4* key_cache;                 // [num_layers][layer_chunks], rows of row_chunks 16-byte chunks

@@ -1,0 +1,973 @@
+// tree_attention.cu -- attention of drafted token trees over the paged cache, on
+// the sm_103a tensor cores (tcgen05).
+//
+// Request r has n new tokens (the nodes of its trees) behind a context of c tokens,
+// K and V of all of them in the cache.  Node i sees keys 0 .. c - 1 and the keys c + k
+// of the nodes k that its mask names:
+//   O_i = sum_j w_ij v_j / sum_j w_ij,  w_ij = exp(scale q_i . k_j) over the seen keys j,
+// 128 keys at a time with an online softmax (m, l, O) per row; S and P never
+// reach HBM.  Pieces of a row's keys computed by different CTAs are merged by
+// m = max m_p, O = sum O_p 2^(m_p - m), l = sum l_p 2^(m_p - m).
+//
+// What bounds it.  Each K/V byte serves all nodes and all q heads of its kv head,
+// n * group query rows.  A 128-key step reads 64 KB at head_dim 128 in bf16 (1.47 us of an SM's
+// share of the copy bandwidth) and takes 0.33 us of the SM's tensor core per 128 rows for each
+// of the two products: up to 256 rows a kv head the keys' bytes are the bound.
+// So the design reads the keys once for all rows:
+// * The rows of a kv head are packed, row = node * group + head: one TMA box
+//   {64, group, 128 / group} of q lands as the 128-row operand of the products.  A
+//   tile of rows is one slot, up to two slots share every K/V step of a work
+//   unit (request, kv head, two tiles of rows).
+// * A unit of one tile would leave the softmax of its only slot between its two
+//   products; there both slots take the same rows and alternate key steps, each with
+//   its own (m, l, O) in TMEM, joined at the end.
+// * Persistent grid, one CTA per SM: the 128-key steps of all units are numbered
+//   (request, kv head, tile pair, step) and cut into equal contiguous ranges by
+//   cost (a unit's start counts kUnitCost / kStepCost steps).  A unit that a range boundary
+//   cuts leaves its pieces as fp32 records, which a second kernel merges with the whole
+//   device: the last contributor alone would read up to 152 records of 64 KB by itself
+//   where few long contexts are split over every SM.
+// * Warps: 0 range walk, Q and K copies (TMA); 10 V copies; 1 MMA issue; 2-5
+//   softmax of slot 0, 6-9 of slot 1 (thread = row); over e4m3 caches 11-14 turn
+//   landed K and V steps into f16 in place.
+// A step that holds nodes takes its mask from the row's words; V of keys that no
+// row of the unit sees is zeroed before the product (a zero weight does not
+// cancel a NaN inside the MMA).  Every wait is bounded; a timeout records
+// PA_DEV_WAIT_TIMEOUT.
+#include <algorithm>
+
+#include "pa_internal.h"
+#include "pa_ptx.cuh"
+#include "work_split.cuh"
+
+namespace pa {
+namespace {
+
+constexpr float kLowest = -1e30f;     // finite stand-in for -inf in running maxima
+constexpr float kRescaleSlack = 8.0f;  // log2 units: the reference of a row moves lazily
+constexpr long long kStepCost = 4;
+constexpr long long kUnitCost = 10;
+
+// How a segment's result is written.
+constexpr int kWhole = 0;  // the whole unit: bf16 output
+constexpr int kHead = 1;   // continues a unit begun by an earlier CTA: record 0
+constexpr int kTail = 2;   // begins a unit finished by later CTAs: record 1
+constexpr int kEnd = 3;    // no more work
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+template <int D, bool KV8>
+struct TreeCfg {
+  static constexpr int BM = 128, BN = 128;          // rows of a slot, keys of a step
+  static constexpr int HALVES = D / 64;             // 128-byte column chunks of head_dim
+  static constexpr int CHUNK = 128 * 128;
+  static constexpr int QBYTES = HALVES * CHUNK;     // Q of one slot
+  static constexpr int TBYTES = HALVES * CHUNK;     // K (or V) of one step
+  static constexpr int BLOCK_BYTES = HALVES * 16 * 128;  // K (or V) of 16 tokens
+  // 16-token blocks land as [8-key group][head_dim half][8 keys][128 B].
+  static constexpr int GSTRIDE = HALVES * 1024;
+  // A V stage is held from its copy to the end of its step, a K stage only to S.
+  static constexpr int NK = D == 128 ? 2 : 5;
+  static constexpr int NV = D == 128 ? 3 : 6;
+  // e4m3: a step's bytes land in the upper half of the f16 stage.
+  static constexpr int RAW_BLOCK = 16 * D;
+  static constexpr int RAW_OFF = TBYTES / 2;
+  static constexpr int SEGS = 4;                    // segment records in flight
+  static constexpr int OFF_Q = 0;                   // [2 slots]
+  static constexpr int OFF_K = 2 * QBYTES;
+  static constexpr int OFF_V = OFF_K + NK * TBYTES;
+  static constexpr int OFF_SEG = OFF_V + NV * TBYTES;
+  static constexpr int OFF_XCH = OFF_SEG + SEGS * 64;   // [2 slots][128 rows] (m, l)
+  static constexpr int OFF_BAR = OFF_XCH + 2 * 128 * 8;
+  // Barriers
+  static constexpr int KFULL = 0;                // [NK] K step landed (e4m3: converted)
+  static constexpr int KFREE = KFULL + NK;       // [NK] the S products that read it are done
+  static constexpr int VFULL = KFREE + NK;       // [NV]
+  static constexpr int VFREE = VFULL + NV;       // [NV] the P.V products that read it are done
+  static constexpr int QFULL = VFREE + NV;       // [2] Q of a slot landed
+  static constexpr int QFREE = QFULL + 2;        // the last S product of a segment is done
+  static constexpr int SFULL = QFREE + 1;        // [2] S of a slot in TMEM
+  static constexpr int PFULL = SFULL + 2;        // [2] P of a slot in TMEM (4 warps)
+  static constexpr int OFULL = PFULL + 2;        // the last P.V product of a segment is done
+  static constexpr int OFREE = OFULL + 1;        // O read at a segment's end (8 warps)
+  static constexpr int SEGFULL = OFREE + 1;      // [SEGS]
+  static constexpr int SEGFREE = SEGFULL + SEGS; // [SEGS] every role is done with it
+  static constexpr int SYNC = SEGFREE + SEGS;    // the 8 softmax warps
+  static constexpr int DRAIN = SYNC + 1;         // the MMA warp's last commit
+  static constexpr int QCONV = DRAIN + 1;        // e4m3: Q turned into f16 (8 warps)
+  static constexpr int KRAW = QCONV + 1;         // [NK] e4m3 step landed
+  static constexpr int VRAW = KRAW + NK;         // [NV]
+  static constexpr int NBAR = VRAW + NV;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+  static constexpr int SMEM = OFF_MISC + 64;
+  static constexpr int CONVERTERS = KV8 ? 4 : 0;    // two warps for K, two for V, steps in turn
+  static constexpr int THREADS = (11 + CONVERTERS) * 32;
+  static constexpr int SEG_USERS = 10 + CONVERTERS;  // MMA, 8 softmax, V producer
+  static constexpr uint32_t TMEM_COLS = 512;        // S0 0, S1 128, O0 256, O1 256 + D
+  static constexpr int W = KV8 ? 32 : 64;           // score columns in registers at once
+  static constexpr uint32_t IDESC_S = KV8 ? idesc_f16_f32(BM, BN, 0) : idesc_bf16_f32(BM, BN, 0);
+  static constexpr uint32_t IDESC_O = KV8 ? idesc_f16_f32(BM, D, 1) : idesc_bf16_f32(BM, D, 1);
+  static_assert(SMEM <= 227 * 1024 && OFF_BAR % 8 == 0, "shared memory");
+};
+
+// A request's rows, or tiles = 0 where it has none or a length is out of range.
+struct TreeReq {
+  int q0, n, len, tiles;
+};
+
+__device__ __forceinline__ TreeReq make_req(const TreeArgs& a, int q0, int q1, int len) {
+  TreeReq p{0, 0, 0, 0};
+  const int n = q1 - q0;
+  if (n < 1 || n > len || n > a.max_query_len || n > 32 * a.words32 || q0 < 0 || q0 > a.total_q - n ||
+      len > a.max_seq_len || len > a.max_blocks_per_seq * a.block_size)
+    return p;
+  p.q0 = q0;
+  p.n = n;
+  p.len = len;
+  p.tiles = (n + 2 * a.slot_nodes - 1) / (2 * a.slot_nodes);
+  return p;
+}
+
+__device__ __forceinline__ TreeReq tree_req(const TreeArgs& a, int r) {
+  if (r >= a.num_seqs) return TreeReq{0, 0, 0, 0};
+  return make_req(a, __ldg(a.query_start_loc + r), __ldg(a.query_start_loc + r + 1), __ldg(a.seq_lens + r));
+}
+
+__device__ __forceinline__ int req_steps(const TreeReq& p) { return (p.len + 127) / 128; }
+
+__device__ void report_bad_requests(const TreeArgs& a, int lane) {
+  for (int r = lane; r < a.num_seqs; r += 32) {
+    const int q0 = __ldg(a.query_start_loc + r), n = __ldg(a.query_start_loc + r + 1) - q0;
+    const int len = __ldg(a.seq_lens + r);
+    if (n == 0) continue;
+    if (n < 0 || n > len || n > a.max_query_len || n > 32 * a.words32 || q0 < 0 || q0 > a.total_q - n)
+      record_error(a.status, PA_DEV_BAD_QUERY_LEN, r, n);
+    else if (len > a.max_seq_len || len > a.max_blocks_per_seq * a.block_size)
+      record_error(a.status, PA_DEV_BAD_SEQ_LEN, r, len);
+  }
+}
+
+__device__ __forceinline__ long long warp_sum64(long long v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Holds the registers of an asynchronous TMEM load until its wait.
+template <int N>
+__device__ __forceinline__ void pin(uint32_t (&r)[N]) {
+#pragma unroll
+  for (int e = 0; e < N; e += 8)
+    asm volatile("" : "+r"(r[e]), "+r"(r[e + 1]), "+r"(r[e + 2]), "+r"(r[e + 3]), "+r"(r[e + 4]),
+                      "+r"(r[e + 5]), "+r"(r[e + 6]), "+r"(r[e + 7]));
+}
+
+// A segment: steps [j0, j1) of one unit inside this CTA's range.
+struct TreeSeg {
+  int r, q0, node0, nodes;  // q0: the request's first row; the unit's nodes
+  int ctx, n_new, j0, j1;
+  int kvh, kind, c0, c1;
+  int pad[4];
+};
+static_assert(sizeof(TreeSeg) == 64, "segment record");
+
+// 32 bits of a row's view of the keys from 32 * i behind the context on: the
+// context (i < 0), the nodes its mask names, nothing behind the last one.
+__device__ __forceinline__ uint32_t view_word(const uint32_t* mask, int words32, int n_new, int i) {
+  if (i < 0) return 0xffffffffu;
+  const int left = n_new - 32 * i;
+  if (left <= 0 || i >= words32) return 0u;
+  return __ldg(mask + i) & (left >= 32 ? 0xffffffffu : (1u << left) - 1u);
+}
+
+// An e4m3 step (nb landed 16-token blocks of head_dim bytes at RAW_OFF of the
+// stage) turned in place into the f16 operand layout of the bf16 copies
+// ([8-key group][head_dim half][8 keys][128 B], 128-byte swizzle), exactly.  Run by one
+// warp, the groups in order: group g's output [g GSTRIDE, (g + 1) GSTRIDE) covers raw
+// rows of groups up to g alone (raw row t sits at RAW_OFF + t D with GSTRIDE = 16 D and
+// RAW_OFF = 128 D, so below (g + 1) GSTRIDE are rows t < 16 g - 112 <= 8 g + 8 for
+// g < 16), and each group is read whole before it is written.
+template <int D, bool KV8>
+__device__ __forceinline__ void convert_step(uint32_t stage, int nb, int lane) {
+  using C = TreeCfg<D, KV8>;
+  constexpr int CPR = D / 16;     // 16-byte raw chunks per key row
+  constexpr int KPI = 32 / CPR;   // key rows per warp-wide load
+  constexpr int NLD = 8 / KPI;    // loads per lane per 8-key group
+  static_assert(C::GSTRIDE == 16 * D && C::RAW_OFF == 128 * D, "in-place conversion order");
+  const int c = lane % CPR;
+  const uint32_t half = (c / 4) * 1024;
+  const int cc = 2 * (c % 4);
+#pragma unroll 1
+  for (int g8 = 0; g8 < 2 * nb; ++g8) {
+    uint4 w[NLD];
+#pragma unroll
+    for (int k = 0; k < NLD; ++k)
+      w[k] = ld_shared_v4(stage + C::RAW_OFF + (g8 * 8 + lane / CPR + KPI * k) * D + c * 16);
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < NLD; ++k) {
+      const int r = lane / CPR + KPI * k;
+      const uint32_t row = stage + g8 * C::GSTRIDE + half + r * 128;
+      st_shared_v4(row + ((cc ^ r) * 16),
+                   make_uint4(e4m3x2_to_f16x2(w[k].x), e4m3x2_to_f16x2(w[k].x >> 16),
+                              e4m3x2_to_f16x2(w[k].y), e4m3x2_to_f16x2(w[k].y >> 16)));
+      st_shared_v4(row + (((cc + 1) ^ r) * 16),
+                   make_uint4(e4m3x2_to_f16x2(w[k].z), e4m3x2_to_f16x2(w[k].z >> 16),
+                              e4m3x2_to_f16x2(w[k].w), e4m3x2_to_f16x2(w[k].w >> 16)));
+    }
+    __syncwarp();
+  }
+}
+
+// Records of a cut unit: (CTA, piece, slot) holds (m, l) of 128 rows and their
+// unnormalised O as [D / 4][128 rows][4 columns], so that a warp's 16-byte accesses to
+// one column group are 512 contiguous bytes.  Piece 1: a unit's first CTA, else 0.
+__device__ __forceinline__ size_t record_of(int cta, int piece, int slot) {
+  return (static_cast<size_t>(cta) * 2 + piece) * 2 + slot;
+}
+
+template <int D, bool KV8>
+__global__ void __launch_bounds__(TreeCfg<D, KV8>::THREADS, 1)
+tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                      const __grid_constant__ CUtensorMap vmap, const TreeArgs a) {
+  using C = TreeCfg<D, KV8>;
+  const int cta = blockIdx.x;
+  const int tid = threadIdx.x;
+  const int warp = tid >> 5;
+  const int lane = tid & 31;
+
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t q_s = sbase + C::OFF_Q;
+  const uint32_t k_s = sbase + C::OFF_K;
+  const uint32_t v_s = sbase + C::OFF_V;
+  const uint32_t bar0 = sbase + C::OFF_BAR;
+  auto bar = [&](int k) -> uint32_t { return bar0 + 8 * k; };
+  TreeSeg* segs = reinterpret_cast<TreeSeg*>(smem + C::OFF_SEG);
+  float2* xch = reinterpret_cast<float2*>(smem + C::OFF_XCH);
+  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC);
+  volatile int* fail_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+  volatile int* n_k_issued = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 8);
+  volatile int* n_v_issued = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 12);
+  volatile int* n_q_issued = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 16);  // [2]
+
+  // The swizzled copies need 1024-byte aligned tiles; the dynamic shared-memory base
+  // always is on this GPU, but never issue a copy if it were not.
+  if (sbase & 1023) {
+    griddep_wait();
+    if (tid == 0) record_error(a.status, PA_DEV_WAIT_TIMEOUT, cta, 6);
+    if (tid == 0) a.splits[cta].c1 = -1;
+    return;
+  }
+  if (tid == 0) {
+    for (int k = 0; k < C::NBAR; ++k) {
+      int count = 1;
+      if (k == C::PFULL || k == C::PFULL + 1) count = 4;
+      if (k == C::OFREE || k == C::SYNC || k == C::QCONV) count = 8;
+      if (k >= C::SEGFREE && k < C::SEGFREE + C::SEGS) count = C::SEG_USERS;
+      mbar_init(bar(k), count);
+    }
+    *fail_flag = 0;
+    *n_k_issued = 0;
+    *n_v_issued = 0;
+    n_q_issued[0] = 0;
+    n_q_issued[1] = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(const_cast<uint32_t*>(tmem_slot)), C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  griddep_wait();  // the cache write of this step's tokens
+  griddep_launch_dependents();
+  const uint32_t tmem = *tmem_slot;
+  const int G = a.group, NPS = a.slot_nodes;
+  auto give_up = [&](int where) {
+    record_error(a.status, PA_DEV_WAIT_TIMEOUT, cta, where);
+    *fail_flag = 1;
+  };
+  // A wait by the whole warp (the same answer for all its lanes).
+  auto warp_wait = [&](int k, uint32_t parity, int where) -> bool {
+    if (*fail_flag) return false;
+    const bool good = __all_sync(0xffffffffu, mbar_wait(bar(k), parity) ? 1 : 0) != 0;
+    if (!good && lane == 0) give_up(where);
+    return good;
+  };
+  // Cache row of 16-token tile t8 + lane (lane < 8) of request r; an id outside the
+  // pool is reported (if `report`) and read as wholly out of bounds (zeros).
+  auto tile_rows = [&](int r, int t8, int nblk, bool report) -> int {
+    const int t16 = t8 + lane;
+    if (lane >= 8 || t16 >= nblk) return 0;
+    const int id = __ldg(a.block_tables + static_cast<size_t>(r) * a.max_blocks_per_seq + (t16 >> a.tile_shift));
+    if (static_cast<unsigned>(id) >= static_cast<unsigned>(a.num_blocks)) {
+      if (report) record_error(a.status, PA_DEV_BAD_BLOCK_ID, r, id);
+      return a.num_blocks * a.block_size;
+    }
+    return id * a.block_size + (t16 & ((1 << a.tile_shift) - 1)) * kBlockSize;
+  };
+
+  if (warp == 0) {
+    // ====================================== range walk, Q and K producer
+    if (cta == 0) report_bad_requests(a, lane);
+    const uint64_t policy = l2_policy_evict_first();
+    if (lane == 0) {
+      tma_prefetch_desc(&qmap);
+      tma_prefetch_desc(&kmap);
+      a.splits[cta].c1 = -1;  // no unit cut at the end of this range so far
+    }
+    const int H = a.num_kv_heads;
+    long long st = 0, un = 0;
+    for (int r = lane; r < a.num_seqs; r += 32) {
+      const TreeReq p = tree_req(a, r);
+      un += p.tiles;
+      st += static_cast<long long>(p.tiles) * req_steps(p);
+    }
+    const long long n_steps = warp_sum64(st) * H, n_units = warp_sum64(un) * H;
+    const long long Cw = kStepCost * n_steps + kUnitCost * n_units;
+    // By cost only where every share holds a unit's start and a step, so that every
+    // CTA between a unit's first and last has one of its steps; else by steps.
+    const bool by_cost = div_ll(Cw, a.num_ctas) >= kStepCost + kUnitCost;
+    const long long CT = by_cost ? kStepCost : 1, CS = by_cost ? kUnitCost : 0;
+    const long long Ctot = by_cost ? Cw : n_steps;
+    const long long x0 = Ctot > 0 ? range_lo(Ctot, a.num_ctas, cta) : 0;
+    const long long x1 = Ctot > 0 ? range_lo(Ctot, a.num_ctas, cta + 1) : 0;
+    int seg = 0, g = 0, nq[2] = {0, 0};
+    bool ok = true;
+    // Steps [j, ..) of a unit whose cost starts at cb: step j starts at cb + CS + CT j.
+    auto first_step_at = [&](long long cb, long long x) -> long long {
+      return x <= cb + CS ? 0 : div_ll(x - cb - CS + CT - 1, CT);
+    };
+    if (x0 < x1) {
+      // The request that holds x0, and the cost before it.
+      int r = -1;
+      long long cb = 0;
+      for (int rc = 0; rc < a.num_seqs && r < 0; rc += 32) {
+        const TreeReq p = tree_req(a, rc + lane);
+        const long long cost = (CS + CT * req_steps(p)) * p.tiles * H;
+        long long incl = cost;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += v;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, cb + incl > x0);
+        if (hit != 0) {
+          const int first = __ffs(hit) - 1;
+          cb += __shfl_sync(0xffffffffu, incl - cost, first);
+          r = rc + first;
+        } else {
+          cb += __shfl_sync(0xffffffffu, incl, 31);
+        }
+      }
+      TreeReq p = tree_req(a, r);
+      int n_u = req_steps(p);
+      int u = static_cast<int>(div_ll(x0 - cb, CS + CT * n_u));  // unit: kv head, then tile pair
+      cb += u * (CS + CT * n_u);
+      long long j = first_step_at(cb, x0);
+      while (ok) {
+        if (j >= n_u) {  // no step of this unit starts in the range: the next one
+          cb += CS + CT * n_u;
+          j = 0;
+          if (++u == H * p.tiles) {
+            u = 0;
+            do {
+              p = tree_req(a, ++r);
+            } while (p.tiles == 0 && r < a.num_seqs);
+            if (p.tiles == 0) break;  // no more work
+            n_u = req_steps(p);
+          }
+        }
+        if (cb + CS + CT * j >= x1) break;
+        const int j0 = static_cast<int>(j);
+        const int j1 = static_cast<int>(min(static_cast<long long>(n_u), first_step_at(cb, x1)));
+        const int kvh = u / p.tiles, node0 = (u - kvh * p.tiles) * 2 * NPS;
+        const int nodes = min(2 * NPS, p.n - node0);
+        const int nsl = nodes > NPS ? 2 : 1;
+        if (seg >= C::SEGS && !(ok = warp_wait(C::SEGFREE + seg % C::SEGS, ((seg / C::SEGS) - 1) & 1, 60))) break;
+        if (lane == 0) {
+          TreeSeg sg{};
+          sg.r = r;
+          sg.q0 = p.q0;
+          sg.node0 = node0;
+          sg.nodes = nodes;
+          sg.ctx = p.len - p.n;
+          sg.n_new = p.n;
+          sg.j0 = j0;
+          sg.j1 = j1;
+          sg.kvh = kvh;
+          sg.kind = (j0 == 0 && j1 == n_u) ? kWhole : (j0 > 0 ? kHead : kTail);
+          segs[seg % C::SEGS] = sg;
+          mbar_arrive(bar(C::SEGFULL + seg % C::SEGS));
+          if (sg.kind == kTail) {
+            TreeSplit sp;
+            sp.c1 = cta_of_tile(Ctot, a.num_ctas, cb + CS + CT * (n_u - 1));
+            sp.row0 = p.q0 + node0;
+            sp.nodes = nodes;
+            sp.kvh = kvh;
+            a.splits[cta] = sp;
+          }
+        }
+        // Q of both slots, once the last S product of the previous segment is done.
+        if (seg > 0 && !(ok = warp_wait(C::QFREE, (seg - 1) & 1, 61))) break;
+        if (lane == 0) {
+          for (int b = 0; b < nsl; ++b) {
+            mbar_arrive_expect_tx(bar(C::QFULL + b), C::HALVES * G * NPS * 128);
+#pragma unroll
+            for (int h = 0; h < C::HALVES; ++h)
+              tma_load_3d(q_s + b * C::QBYTES + h * C::CHUNK, &qmap, bar(C::QFULL + b), 64 * h, kvh * G,
+                          p.q0 + node0 + b * NPS, policy);
+            n_q_issued[b] = ++nq[b];
+          }
+        }
+        __syncwarp();
+        const int nblk = (p.len + kBlockSize - 1) / kBlockSize;
+        int rowc = tile_rows(r, j0 * 8, nblk, true);
+        for (int jj = j0; jj < j1; ++jj) {
+          const int stg = g % C::NK;
+          if (g >= C::NK && !(ok = warp_wait(C::KFREE + stg, ((g / C::NK) - 1) & 1, 62))) break;
+          const int nb = min(8, nblk - jj * 8);
+          const int full = (KV8 ? C::KRAW : C::KFULL) + stg;
+          if (lane == 0) mbar_arrive_expect_tx(bar(full), nb * (KV8 ? C::RAW_BLOCK : C::BLOCK_BYTES));
+          __syncwarp();
+          if (lane < nb) {
+            if constexpr (KV8)
+              tma_load_3d(k_s + stg * C::TBYTES + C::RAW_OFF + lane * C::RAW_BLOCK, &kmap, bar(full), 0, kvh, rowc,
+                          policy);
+            else
+              tma_load_5d(k_s + stg * C::TBYTES + lane * C::BLOCK_BYTES, &kmap, bar(full), 0, 0, 0, rowc / 8, kvh,
+                          policy);
+          }
+          ++g;
+          if (lane == 0) *n_k_issued = g;
+          if (jj + 1 < j1) rowc = tile_rows(r, (jj + 1) * 8, nblk, true);
+        }
+        ++seg;
+        if (!ok || j1 < n_u) break;  // the range ends inside this unit
+        j = n_u;
+      }
+    }
+    if (ok && seg >= C::SEGS) ok = warp_wait(C::SEGFREE + seg % C::SEGS, ((seg / C::SEGS) - 1) & 1, 67);
+    if (ok && lane == 0) {
+      segs[seg % C::SEGS].kind = kEnd;
+      mbar_arrive(bar(C::SEGFULL + seg % C::SEGS));
+    }
+    if (!ok && lane == 0) *fail_flag = 1;
+  } else if (warp == 10) {
+    // =========================================================== V producer
+    const uint64_t policy = l2_policy_evict_first();
+    if (lane == 0) tma_prefetch_desc(&vmap);
+    bool ok = true;
+    int g = 0;
+    for (int seg = 0; ok; ++seg) {
+      const int slot = seg % C::SEGS;
+      if (!(ok = warp_wait(C::SEGFULL + slot, (seg / C::SEGS) & 1, 63))) break;
+      const TreeSeg sg = segs[slot];
+      if (sg.kind == kEnd) break;
+      const int nblk = (sg.ctx + sg.n_new + kBlockSize - 1) / kBlockSize;
+      int rowc = tile_rows(sg.r, sg.j0 * 8, nblk, false);
+      for (int jj = sg.j0; jj < sg.j1; ++jj) {
+        const int stg = g % C::NV;
+        if (g >= C::NV && !(ok = warp_wait(C::VFREE + stg, ((g / C::NV) - 1) & 1, 64))) break;
+        const int nb = min(8, nblk - jj * 8);
+        const int full = (KV8 ? C::VRAW : C::VFULL) + stg;
+        if (lane == 0) mbar_arrive_expect_tx(bar(full), nb * (KV8 ? C::RAW_BLOCK : C::BLOCK_BYTES));
+        __syncwarp();
+        if (lane < nb) {
+          if constexpr (KV8)
+            tma_load_3d(v_s + stg * C::TBYTES + C::RAW_OFF + lane * C::RAW_BLOCK, &vmap, bar(full), 0, sg.kvh, rowc,
+                        policy);
+          else
+            tma_load_5d(v_s + stg * C::TBYTES + lane * C::BLOCK_BYTES, &vmap, bar(full), 0, 0, 0, rowc / 8, sg.kvh,
+                        policy);
+        }
+        ++g;
+        if (lane == 0) *n_v_issued = g;
+        if (jj + 1 < sg.j1) rowc = tile_rows(sg.r, (jj + 1) * 8, nblk, false);
+      }
+      __syncwarp();
+      if (ok && lane == 0) mbar_arrive(bar(C::SEGFREE + slot));
+    }
+    if (!ok && lane == 0) *fail_flag = 1;
+  } else if (warp == 1) {
+    // ========================================================== MMA issuer
+    if (lane == 0) {
+      bool ok = true;
+      int g = 0, pc[2] = {0, 0}, qc[2] = {0, 0};
+      auto wait = [&](int k, uint32_t parity, int where) -> bool {
+        if (*fail_flag) return false;
+        if (!mbar_wait(bar(k), parity)) {
+          give_up(where);
+          return false;
+        }
+        return true;
+      };
+      // S of slot b = Q (buffer qb) K^T of K step gk, into TMEM columns 128 b ..
+      auto issue_s = [&](int b, int qb, int gk) {
+        const uint32_t kst = k_s + (gk % C::NK) * C::TBYTES;
+        const uint32_t qst = q_s + qb * C::QBYTES;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t qoff = (ks / 4) * C::CHUNK + (ks % 4) * 32;
+          const uint32_t koff = (ks / 4) * 1024 + (ks % 4) * 32;
+          umma_bf16(tmem + b * C::BN, sdesc_sw128(qst + qoff, 16, 1024), sdesc_sw128(kst + koff, 16, C::GSTRIDE),
+                    C::IDESC_S, ks > 0);
+        }
+        umma_commit(bar(C::SFULL + b));
+      };
+      // O of slot b += P V of V step gv (P: 16 bits in TMEM columns 128 b ..).
+      auto issue_pv = [&](int b, int gv, bool acc) {
+        const uint32_t vst = v_s + (gv % C::NV) * C::TBYTES;
+#pragma unroll
+        for (int ks = 0; ks < C::BN / 16; ++ks)
+          umma_tmem_a(tmem + 256 + b * D, tmem + b * C::BN + ks * 8,
+                      sdesc_sw128(vst + ks * C::BLOCK_BYTES, 1024, C::GSTRIDE), C::IDESC_O,
+                      (acc || ks > 0) ? 1u : 0u);
+      };
+      auto k_landed = [&](int gk) -> bool {
+        const bool good = wait(C::KFULL + gk % C::NK, (gk / C::NK) & 1, 72);
+        tc_fence_after();
+        return good;
+      };
+      for (int seg = 0; ok; ++seg) {
+        const int slot = seg % C::SEGS;
+        if (!(ok = wait(C::SEGFULL + slot, (seg / C::SEGS) & 1, 70))) break;
+        const TreeSeg sg = segs[slot];
+        if (sg.kind == kEnd) break;
+        const int n = sg.j1 - sg.j0;
+        const bool two = sg.nodes > NPS;
+        if constexpr (KV8) {
+          ok = wait(C::QCONV, seg & 1, 71);
+        } else {
+          for (int b = 0; b < (two ? 2 : 1) && ok; ++b) ok = wait(C::QFULL + b, qc[b]++ & 1, 71);
+        }
+        if (!ok) break;
+        // Step k of slot b: (two tiles) both slots take every step, or (one tile) they
+        // take steps in turn.
+        if (two) {
+          if (!(ok = k_landed(g))) break;
+          issue_s(0, 0, g);
+          issue_s(1, 1, g);
+          umma_commit(bar(C::KFREE + g % C::NK));
+          if (n == 1) umma_commit(bar(C::QFREE));
+        } else {
+          for (int k = 0; k < min(n, 2) && ok; ++k) {
+            if (!(ok = k_landed(g + k))) break;
+            issue_s(k, 0, g + k);
+            umma_commit(bar(C::KFREE + (g + k) % C::NK));
+          }
+          if (!ok) break;
+          if (n <= 2) umma_commit(bar(C::QFREE));
+        }
+        for (int k = 0; k < n && ok; ++k) {
+          const int gk = g + k;
+          if (!(ok = wait(C::VFULL + gk % C::NV, (gk / C::NV) & 1, 73))) break;
+          if (k == 0 && seg > 0 && !(ok = wait(C::OFREE, (seg - 1) & 1, 76))) break;
+          if (two) {
+            for (int b = 0; b < 2 && ok; ++b) {
+              if (!(ok = wait(C::PFULL + b, pc[b]++ & 1, 75))) break;
+              tc_fence_after();
+              issue_pv(b, gk, k > 0);
+              if (k + 1 < n) {
+                if (b == 0 && !(ok = k_landed(gk + 1))) break;
+                issue_s(b, b, gk + 1);
+              }
+            }
+            if (!ok) break;
+            umma_commit(bar(C::VFREE + gk % C::NV));
+            if (k + 1 < n) umma_commit(bar(C::KFREE + (gk + 1) % C::NK));
+            if (k + 2 == n) umma_commit(bar(C::QFREE));
+          } else {
+            const int b = k & 1;
+            if (!(ok = wait(C::PFULL + b, pc[b]++ & 1, 75))) break;
+            tc_fence_after();
+            issue_pv(b, gk, k > 1);
+            umma_commit(bar(C::VFREE + gk % C::NV));
+            if (k + 2 < n) {
+              if (!(ok = k_landed(gk + 2))) break;
+              issue_s(b, 0, gk + 2);
+              umma_commit(bar(C::KFREE + (gk + 2) % C::NK));
+              if (k + 3 == n) umma_commit(bar(C::QFREE));
+            }
+          }
+        }
+        if (!ok) break;
+        umma_commit(bar(C::OFULL));
+        g += n;
+        mbar_arrive(bar(C::SEGFREE + slot));
+      }
+      if (!ok) *fail_flag = 1;
+      // Every MMA issued has completed before TMEM can be released.
+      umma_commit(bar(C::DRAIN));
+      (void)mbar_wait(bar(C::DRAIN), 0);
+    }
+    __syncwarp();
+  } else if (warp >= 11) {
+    // =================================================== e4m3 -> f16 (KV8)
+    if constexpr (KV8) {
+      const bool is_v = warp >= 13;
+      const int turn = (warp - 11) & 1;
+      const int NS = is_v ? C::NV : C::NK;
+      const int raw = is_v ? C::VRAW : C::KRAW, full = is_v ? C::VFULL : C::KFULL;
+      const uint32_t base = is_v ? v_s : k_s;
+      bool ok = true;
+      int g = 0;
+      for (int seg = 0; ok; ++seg) {
+        const int slot = seg % C::SEGS;
+        if (!(ok = warp_wait(C::SEGFULL + slot, (seg / C::SEGS) & 1, 68))) break;
+        const TreeSeg sg = segs[slot];
+        if (sg.kind == kEnd) break;
+        const int nblk = (sg.ctx + sg.n_new + kBlockSize - 1) / kBlockSize;
+        for (int jj = sg.j0; jj < sg.j1; ++jj, ++g) {
+          if ((g & 1) != turn) continue;
+          const int stg = g % NS;
+          if (!(ok = warp_wait(raw + stg, (g / NS) & 1, is_v ? 66 : 65))) break;
+          convert_step<D, KV8>(base + stg * C::TBYTES, min(8, nblk - jj * 8), lane);
+          fence_proxy_async_smem();  // read by the tensor core
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(full + stg));
+        }
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(bar(C::SEGFREE + slot));
+      }
+      if (!ok && lane == 0) *fail_flag = 1;
+    }
+  } else {
+    // ============================================================ softmax
+    // Warps 2-5 serve slot 0, 6-9 slot 1; warp w owns TMEM lanes 32 (w % 4) .. + 31.
+    const int b = warp < 6 ? 0 : 1;
+    const int i_row = (warp & 3) * 32 + lane;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t tm_s = lane_base + b * C::BN;
+    const uint32_t tm_o = lane_base + 256;
+    const float sl2 = a.scale_log2;
+    bool ok = true;
+    int sc = 0, g = 0, qn[2] = {0, 0};
+    uint32_t sync_phase = 0;
+    for (int seg = 0; ok; ++seg) {
+      const int slot = seg % C::SEGS;
+      if (!(ok = warp_wait(C::SEGFULL + slot, (seg / C::SEGS) & 1, 81))) break;
+      const volatile TreeSeg& sg = segs[slot];
+      if (sg.kind == kEnd) break;
+      const int n = sg.j1 - sg.j0;
+      const int nodes = sg.nodes, ctx = sg.ctx, n_new = sg.n_new;
+      const bool two = nodes > NPS;
+      if constexpr (KV8) {
+        // Q to f16 in place (same layout), before the segment's first S product.
+        for (int qb = 0; qb < (two ? 2 : 1) && ok; ++qb) {
+          if (!(ok = warp_wait(C::QFULL + qb, qn[qb]++ & 1, 79))) break;
+          const uint32_t qst = q_s + qb * C::QBYTES;
+          for (int i = tid - 64; i < C::QBYTES / 16; i += 256) {
+            const uint4 w = ld_shared_v4(qst + i * 16);
+            st_shared_v4(qst + i * 16, make_uint4(bf16x2_to_f16x2(w.x), bf16x2_to_f16x2(w.y),
+                                                  bf16x2_to_f16x2(w.z), bf16x2_to_f16x2(w.w)));
+          }
+        }
+        if (!ok) break;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::QCONV));
+      }
+      const int node_b = two && b ? NPS : 0;                           // first node of this slot in the unit
+      const int rows = (two ? (b ? nodes - NPS : NPS) : nodes) * G;    // rows of this slot
+      const bool mine = i_row < rows;
+      const bool live = (warp & 3) * 32 < rows;                        // some row of this warp
+      const int node = node_b + i_row / G;                             // in the unit
+      const uint32_t* mask = a.masks + static_cast<size_t>(sg.q0 + sg.node0 + (mine ? node : 0)) * a.words32;
+      float m_ref = kLowest, l_run = 0.f;
+      bool first = true;
+      for (int k = two ? 0 : b; k < n; k += two ? 1 : 2) {
+        const int key0 = (sg.j0 + k) * C::BN;
+        if (!(ok = warp_wait(C::SFULL + b, sc++ & 1, 82))) break;
+        tc_fence_after();
+        const bool masked = key0 + C::BN > ctx;  // the step holds nodes, or ends behind the keys
+        const int off = key0 - ctx;
+        const int sh = off & 31, w0 = off >> 5;
+        if (live) {
+          uint32_t seen[4];
+          if (masked) {
+            uint32_t w[5];
+#pragma unroll
+            for (int i = 0; i < 5; ++i) w[i] = view_word(mask, a.words32, n_new, w0 + i);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) seen[i] = __funnelshift_r(w[i], w[i + 1], sh);
+          }
+          constexpr int W = C::W;
+          auto load = [&](int c, uint32_t (&sr)[W]) {
+#pragma unroll
+            for (int i = 0; i < W; i += 32) tmem_ld32_async(tm_s + c * W + i, sr + i);
+            tmem_wait_ld();
+            pin(sr);
+            if (masked) {
+#pragma unroll
+              for (int i = 0; i < W; i += 32) {
+                uint32_t word = seen[0];
+                if ((c * W + i) / 32 == 1) word = seen[1];
+                if ((c * W + i) / 32 == 2) word = seen[2];
+                if ((c * W + i) / 32 == 3) word = seen[3];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) sr[i + e] = word >> e & 1u ? sr[i + e] : 0xff800000u;  // -inf
+              }
+            }
+          };
+          // Pass 1: the row's maximum; the reference moves before any weight.
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < C::BN / W; ++c) {
+            uint32_t sr[W];
+            load(c, sr);
+#pragma unroll
+            for (int e = 0; e < W; e += 2)
+              mx[(e / 2) % 4] = fmax3(mx[(e / 2) % 4], __uint_as_float(sr[e]), __uint_as_float(sr[e + 1]));
+          }
+          const float m_tile = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+          const bool moved = m_tile > m_ref + kRescaleSlack;
+          float alpha = 1.f;
+          if (moved) {
+            alpha = fast_exp2(m_ref - m_tile);
+            l_run *= alpha;
+            m_ref = m_tile;
+          }
+          // Pass 2: the weights, 16 bits each, over columns that have been read.
+          const float2 sl = make_float2(sl2, sl2), mm = make_float2(-m_ref, -m_ref);
+          float2 sum[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int c = 0; c < C::BN / W; ++c) {
+            uint32_t sr[W], pk[W / 2];
+            load(c, sr);
+#pragma unroll
+            for (int e = 0; e < W; e += 2) {
+              const float2 x = __ffma2_rn(make_float2(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])), sl, mm);
+              const float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
+              pk[e / 2] = KV8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+              sum[(e / 2) % 4] = __fadd2_rn(sum[(e / 2) % 4], make_float2(p0, p1));
+            }
+#pragma unroll
+            for (int i = 0; i < W / 2; i += 16) tmem_st16_async(tm_s + c * (W / 2) + i, pk + i);
+          }
+          const float2 ps = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
+          l_run += ps.x + ps.y;
+          if (__any_sync(0xffffffffu, moved) && !first) {
+            // S of this step is done, so the slot's P V before it is too.
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+              float ov[16];
+              tmem_ld16(tm_o + b * D + c * 16, ov);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) ov[e] *= alpha;
+              tmem_st16(tm_o + b * D + c * 16, ov);
+            }
+          }
+        }
+        first = false;
+        // V of keys that no row of the unit sees may hold anything: zeros instead, before the
+        // first product that reads the step.
+        if (masked && (b == 0 || !two)) {
+          uint32_t any[5] = {0, 0, 0, 0, 0};
+          const uint32_t* mk = a.masks + static_cast<size_t>(sg.q0 + sg.node0) * a.words32;
+          for (int i = lane; i < nodes; i += 32)
+#pragma unroll
+            for (int w = 0; w < 5; ++w) any[w] |= view_word(mk + static_cast<size_t>(i) * a.words32, a.words32, n_new, w0 + w);
+#pragma unroll
+          for (int w = 0; w < 5; ++w) any[w] = __reduce_or_sync(0xffffffffu, any[w]);
+          const int stg = (g + k) % C::NV;
+          if (!(ok = warp_wait(C::VFULL + stg, ((g + k) / C::NV) & 1, 83))) break;
+          uint32_t lo = any[0], hi = any[1];  // of this warp's 32 keys
+          if ((warp & 3) == 1) lo = any[1], hi = any[2];
+          if ((warp & 3) == 2) lo = any[2], hi = any[3];
+          if ((warp & 3) == 3) lo = any[3], hi = any[4];
+          // (slot 0's warps 2 - 5 and slot 1's 6 - 9: warp & 3 names every quarter once)
+          if (!(__funnelshift_r(lo, hi, sh) >> lane & 1u)) {
+#pragma unroll
+            for (int c = 0; c < C::HALVES * 8; ++c)
+              st_shared_v4(v_s + stg * C::TBYTES + (i_row >> 4) * C::BLOCK_BYTES + ((i_row >> 3) & 1) * C::GSTRIDE +
+                               (c >> 3) * 1024 + (i_row & 7) * 128 + (c & 7) * 16,
+                           make_uint4(0u, 0u, 0u, 0u));
+          }
+          fence_proxy_async_smem();
+        }
+        tmem_wait_st();
+        tc_fence_before();  // P and O precede the next products
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::PFULL + b));
+      }
+      if (!ok) break;
+      g += n;
+      // ---- the segment's end
+      if (!(ok = warp_wait(C::OFULL, seg & 1, 84))) break;
+      tc_fence_after();
+      const int kind = sg.kind;
+      const int kvh = sg.kvh;
+      // One tile: (m, l) of the two halves of its keys, joined.
+      float w_own = 1.f, w_other = 0.f;
+      if (!two) {
+        xch[b * 128 + i_row] = make_float2(m_ref, l_run);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::SYNC));
+        if (!(ok = warp_wait(C::SYNC, sync_phase++ & 1, 80))) break;
+        const float2 other = xch[(b ^ 1) * 128 + i_row];
+        const float m = fmaxf(m_ref, other.x);
+        w_own = fast_exp2(m_ref - m);
+        w_other = fast_exp2(other.x - m);
+        m_ref = m;
+        l_run = l_run * w_own + other.y * w_other;
+      }
+      if (live) {
+        const float inv = kind != kWhole ? 1.f : (l_run > 0.f ? a.o_scale / l_run : 0.f);
+        const int out_slot = two ? b : 0;
+        const size_t rec = record_of(cta, kind == kTail ? 1 : 0, out_slot);
+        const int i_node = i_row / G;
+        __nv_bfloat16* dst = a.out + (static_cast<size_t>(sg.q0 + sg.node0 + node_b + i_node) * a.num_heads +
+                                      kvh * G + (i_row - i_node * G)) * D;
+        float4* part = reinterpret_cast<float4*>(a.part_o + rec * (D * 128)) + i_row;
+        if (kind != kWhole && mine && (two || b == 0))
+          *reinterpret_cast<float2*>(a.part_ml + (rec * 128 + i_row) * 2) = make_float2(m_ref, l_run);
+        // Two tiles: the slot's columns; one: half the columns each.
+        const int c0 = two ? 0 : b * (D / 2), c1 = two ? D : c0 + D / 2;
+        const float f_own = w_own * inv, f_other = w_other * inv;
+#pragma unroll 1
+        for (int c = c0; c < c1; c += 16) {
+          float o[16];
+          tmem_ld16(tm_o + b * D + c, o);
+          // (slot 1 has no O of its own where the segment is one step long)
+          const bool own_there = two || b == 0 || n > 1, other_there = !two && (b == 1 || n > 1);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] = own_there ? o[e] * f_own : 0.f;
+          if (other_there) {
+            float x[16];
+            tmem_ld16(tm_o + (b ^ 1) * D + c, x);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = fmaf(x[e], f_other, o[e]);
+          }
+          if (!mine) continue;
+          if (kind == kWhole) {
+#pragma unroll
+            for (int e = 0; e < 16; e += 8)
+              *reinterpret_cast<uint4*>(dst + c + e) =
+                  make_uint4(pack_bf16x2(o[e], o[e + 1]), pack_bf16x2(o[e + 2], o[e + 3]),
+                             pack_bf16x2(o[e + 4], o[e + 5]), pack_bf16x2(o[e + 6], o[e + 7]));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+              part[((c + e) / 4) * 128] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar(C::OFREE));
+        mbar_arrive(bar(C::SEGFREE + slot));
+      }
+    }
+    if (!ok && lane == 0) *fail_flag = 1;
+  }
+
+  __syncthreads();
+  if (*fail_flag && tid == 0) {
+    // Let copies still in flight land before TMEM is released and the CTA leaves (bounded).
+    const int nk = *n_k_issued, nv = *n_v_issued;
+    const int kb = KV8 ? C::KRAW : C::KFULL, vb = KV8 ? C::VRAW : C::VFULL;
+    for (int i = max(0, nk - C::NK); i < nk; ++i) (void)mbar_wait(bar(kb + i % C::NK), (i / C::NK) & 1);
+    for (int i = max(0, nv - C::NV); i < nv; ++i) (void)mbar_wait(bar(vb + i % C::NV), (i / C::NV) & 1);
+    for (int b = 0; b < 2; ++b)
+      if (n_q_issued[b] > 0) (void)mbar_wait(bar(C::QFULL + b), (n_q_issued[b] - 1) & 1);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+// Merges the units that range boundaries cut.  Block (c, b, z): slot b of the unit
+// that CTA c began and did not finish.  A warp takes 8 rows x 16 columns at a time,
+// a thread 4 columns, over the contributors in order.
+constexpr int kMergeWarps = 8;
+constexpr int kMergeBlocks = 4;
+template <int D>
+__global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const TreeArgs a) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int c0 = blockIdx.x, b = blockIdx.y;
+  const int4 rec = __ldcg(reinterpret_cast<const int4*>(a.splits + c0));
+  const int c1 = rec.x, row0 = rec.y, nodes = rec.z, kvh = rec.w;
+  if (c1 < 0) return;
+  const int NPS = a.slot_nodes, G = a.group;
+  const bool two = nodes > NPS;
+  if (b == 1 && !two) return;
+  const int rows = (two ? (b ? nodes - NPS : NPS) : nodes) * G;
+  const int lane = threadIdx.x & 31;
+  constexpr int kCols = D / 16;
+  const int tasks = (rows + 7) / 8 * kCols;
+  for (int t = blockIdx.z * kMergeWarps + (threadIdx.x >> 5); t < tasks; t += kMergeBlocks * kMergeWarps) {
+    const int i = t / kCols * 8 + (lane & 7);
+    const int c4 = t % kCols * 4 + (lane >> 3);  // column group of 4
+    if (i >= rows) continue;
+    auto ml_of = [&](int c) -> float2 {
+      return __ldcg(reinterpret_cast<const float2*>(a.part_ml + (record_of(c, c == c0 ? 1 : 0, b) * 128 + i) * 2));
+    };
+    float m = kLowest;
+#pragma unroll 4
+    for (int c = c0; c <= c1; ++c) m = fmaxf(m, ml_of(c).x);
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int c = c0; c <= c1; ++c) {
+      const float2 ml = ml_of(c);
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part_o + record_of(c, c == c0 ? 1 : 0, b) * (D * 128)) +
+                              c4 * 128 + i);
+      const float w = fast_exp2(ml.x - m);
+      l = fmaf(ml.y, w, l);
+      o.x = fmaf(x.x, w, o.x);
+      o.y = fmaf(x.y, w, o.y);
+      o.z = fmaf(x.z, w, o.z);
+      o.w = fmaf(x.w, w, o.w);
+    }
+    const float inv = l > 0.f ? a.o_scale / l : 0.f;
+    const int node = i / G;
+    __nv_bfloat16* dst = a.out + (static_cast<size_t>(row0 + (two && b ? NPS : 0) + node) * a.num_heads + kvh * G +
+                                  (i - node * G)) * D + c4 * 4;
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+  }
+}
+
+template <int D, bool KV8>
+cudaError_t launch_impl(const TreeArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                        cudaStream_t stream) {
+  using C = TreeCfg<D, KV8>;
+  static bool attr_set[64] = {false};  // per device: set once
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!attr_set[dev]) {
+    const cudaError_t err =
+        cudaFuncSetAttribute(tree_attention_kernel<D, KV8>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (err != cudaSuccess) return err;
+    attr_set[dev] = true;
+  }
+  const cudaError_t err = launch_overlapped(tree_attention_kernel<D, KV8>, dim3(a.num_ctas), dim3(C::THREADS), C::SMEM,
+                                            stream, qmap, kmap, vmap, a);
+  // Units of one step are never cut.
+  if (err != cudaSuccess || a.max_seq_len <= 128) return err;
+  return launch_overlapped(tree_merge_kernel<D>, dim3(a.num_ctas, 2, kMergeBlocks), dim3(kMergeWarps * 32), 0, stream,
+                           a);
+}
+
+}  // namespace
+
+size_t tree_record_floats(int head_dim) { return 4 * 128 * static_cast<size_t>(head_dim); }
+
+cudaError_t launch_tree_attention(const TreeArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
+                                  const CUtensorMap& vmap, int head_dim, bool kv8, cudaStream_t stream) {
+  if (head_dim == 128)
+    return kv8 ? launch_impl<128, true>(a, qmap, kmap, vmap, stream) : launch_impl<128, false>(a, qmap, kmap, vmap, stream);
+  return kv8 ? launch_impl<64, true>(a, qmap, kmap, vmap, stream) : launch_impl<64, false>(a, qmap, kmap, vmap, stream);
+}
+
+}  // namespace pa
