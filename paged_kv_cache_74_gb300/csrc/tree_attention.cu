@@ -27,9 +27,10 @@
 //   cuts leaves its pieces as fp32 records, which a second kernel merges with the whole
 //   device: the last contributor alone would read up to 152 records of 64 KB by itself
 //   where few long contexts are split over every SM.
-// * Warps: 0 range walk, Q and K copies (TMA); 10 V copies; 1 MMA issue; 2-5
-//   softmax of slot 0, 6-9 of slot 1 (thread = row); over e4m3 caches 11-14 turn
-//   landed K and V steps into f16 in place.
+// * Warps: 0-3 softmax of slot 0, 4-7 of slot 1 (thread = row, its 128 scores of a
+//   step in registers, which the other warps give up: setmaxnreg); 8 range walk, Q
+//   and K copies (TMA); 9 MMA issue; 10 V copies; over e4m3 caches 12-13 turn landed
+//   K steps into f16, 14-15 V steps.
 // A step that holds nodes takes its mask from the row's words; V of keys that no
 // row of the unit sees is zeroed before the product (a zero weight does not
 // cancel a NaN inside the MMA).  Every wait is bounded; a timeout records
@@ -70,16 +71,19 @@ struct TreeCfg {
   // 16-token blocks land as [8-key group][head_dim half][8 keys][128 B].
   static constexpr int GSTRIDE = HALVES * 1024;
   // A V stage is held from its copy to the end of its step, a K stage only to S.
-  static constexpr int NK = D == 128 ? 2 : 5;
-  static constexpr int NV = D == 128 ? 3 : 6;
-  // e4m3: a step's bytes land in the upper half of the f16 stage.
+  // e4m3: landed bytes have stages of their own, free again once converted.
+  static constexpr int NK = KV8 ? (D == 128 ? 1 : 2) : (D == 128 ? 2 : 5);
+  static constexpr int NV = KV8 ? (D == 128 ? 2 : 3) : (D == 128 ? 3 : 6);
+  static constexpr int NR = KV8 ? (D == 128 ? 2 : 4) : 0;  // raw K stages = raw V stages
   static constexpr int RAW_BLOCK = 16 * D;
-  static constexpr int RAW_OFF = TBYTES / 2;
+  static constexpr int RAW_BYTES = 128 * D;
   static constexpr int SEGS = 4;                    // segment records in flight
   static constexpr int OFF_Q = 0;                   // [2 slots]
   static constexpr int OFF_K = 2 * QBYTES;
   static constexpr int OFF_V = OFF_K + NK * TBYTES;
-  static constexpr int OFF_SEG = OFF_V + NV * TBYTES;
+  static constexpr int OFF_KRAW = OFF_V + NV * TBYTES;
+  static constexpr int OFF_VRAW = OFF_KRAW + NR * RAW_BYTES;
+  static constexpr int OFF_SEG = OFF_VRAW + NR * RAW_BYTES;
   static constexpr int OFF_XCH = OFF_SEG + SEGS * 64;   // [2 slots][128 rows] (m, l)
   static constexpr int OFF_BAR = OFF_XCH + 2 * 128 * 8;
   // Barriers
@@ -98,19 +102,26 @@ struct TreeCfg {
   static constexpr int SYNC = SEGFREE + SEGS;    // the 8 softmax warps
   static constexpr int DRAIN = SYNC + 1;         // the MMA warp's last commit
   static constexpr int QCONV = DRAIN + 1;        // e4m3: Q turned into f16 (8 warps)
-  static constexpr int KRAW = QCONV + 1;         // [NK] e4m3 step landed
-  static constexpr int VRAW = KRAW + NK;         // [NV]
-  static constexpr int NBAR = VRAW + NV;
+  static constexpr int KRAW = QCONV + 1;         // [NR] e4m3 step landed
+  static constexpr int VRAW = KRAW + NR;         // [NR]
+  static constexpr int KRAWFREE = VRAW + NR;     // [NR] ... and read by its two warps
+  static constexpr int VRAWFREE = KRAWFREE + NR; // [NR]
+  static constexpr int NBAR = VRAWFREE + NR;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int SMEM = OFF_MISC + 64;
-  static constexpr int CONVERTERS = KV8 ? 4 : 0;    // two warps for K, two for V, steps in turn
-  static constexpr int THREADS = (11 + CONVERTERS) * 32;
+  static constexpr int CONVERTERS = KV8 ? 4 : 0;    // two warps for K, two for V, half a step each
+  static constexpr int THREADS = (12 + CONVERTERS) * 32;
   static constexpr int SEG_USERS = 10 + CONVERTERS;  // MMA, 8 softmax, V producer
+  // Registers of the softmax warps and of the others; their sum is within what a
+  // block is launched with (checked before the launch).
+  static constexpr int REGS_SOFTMAX = KV8 ? 184 : 200;
+  static constexpr int REGS_OTHER = KV8 ? 72 : 96;
+  static constexpr int REGS_SUM = 256 * REGS_SOFTMAX + (THREADS - 256) * REGS_OTHER;
   static constexpr uint32_t TMEM_COLS = 512;        // S0 0, S1 128, O0 256, O1 256 + D
-  static constexpr int W = KV8 ? 32 : 64;           // score columns in registers at once
   static constexpr uint32_t IDESC_S = KV8 ? idesc_f16_f32(BM, BN, 0) : idesc_bf16_f32(BM, BN, 0);
   static constexpr uint32_t IDESC_O = KV8 ? idesc_f16_f32(BM, D, 1) : idesc_bf16_f32(BM, D, 1);
   static_assert(SMEM <= 227 * 1024 && OFF_BAR % 8 == 0, "shared memory");
+  static_assert(REGS_SUM <= 65536 && REGS_SOFTMAX % 8 == 0 && REGS_OTHER % 8 == 0, "registers");
 };
 
 // A request's rows, or tiles = 0 where it has none or a length is out of range.
@@ -183,43 +194,53 @@ __device__ __forceinline__ uint32_t view_word(const uint32_t* mask, int words32,
   return __ldg(mask + i) & (left >= 32 ? 0xffffffffu : (1u << left) - 1u);
 }
 
-// An e4m3 step (nb landed 16-token blocks of head_dim bytes at RAW_OFF of the
-// stage) turned in place into the f16 operand layout of the bf16 copies
-// ([8-key group][head_dim half][8 keys][128 B], 128-byte swizzle), exactly.  Run by one
-// warp, the groups in order: group g's output [g GSTRIDE, (g + 1) GSTRIDE) covers raw
-// rows of groups up to g alone (raw row t sits at RAW_OFF + t D with GSTRIDE = 16 D and
-// RAW_OFF = 128 D, so below (g + 1) GSTRIDE are rows t < 16 g - 112 <= 8 g + 8 for
-// g < 16), and each group is read whole before it is written.
+// Half of an e4m3 step (16-token blocks [b0, b1) of head_dim bytes a token at `raw`)
+// written as f16, exactly, in the operand layout of the bf16 copies ([8-key
+// group][head_dim half][8 keys][128 B], 128-byte swizzle).  Run by one warp, four
+// 8-key groups of loads in flight.  A raw 16-byte chunk becomes two f16 chunks; lanes
+// of the upper head_dim half store them in the other order, so that the eight lanes
+// of a key hit eight bank groups.
 template <int D, bool KV8>
-__device__ __forceinline__ void convert_step(uint32_t stage, int nb, int lane) {
+__device__ __forceinline__ void convert_half(uint32_t raw, uint32_t stage, int b0, int b1, int lane) {
   using C = TreeCfg<D, KV8>;
   constexpr int CPR = D / 16;     // 16-byte raw chunks per key row
   constexpr int KPI = 32 / CPR;   // key rows per warp-wide load
   constexpr int NLD = 8 / KPI;    // loads per lane per 8-key group
-  static_assert(C::GSTRIDE == 16 * D && C::RAW_OFF == 128 * D, "in-place conversion order");
   const int c = lane % CPR;
   const uint32_t half = (c / 4) * 1024;
-  const int cc = 2 * (c % 4);
+  const int cc = 2 * (c % 4), swap = c / 4;
 #pragma unroll 1
-  for (int g8 = 0; g8 < 2 * nb; ++g8) {
-    uint4 w[NLD];
+  for (int g8 = 2 * b0; g8 < 2 * b1; g8 += 4) {
+    uint4 w[4][NLD];
 #pragma unroll
-    for (int k = 0; k < NLD; ++k)
-      w[k] = ld_shared_v4(stage + C::RAW_OFF + (g8 * 8 + lane / CPR + KPI * k) * D + c * 16);
-    __syncwarp();
+    for (int g = 0; g < 4; ++g)
 #pragma unroll
-    for (int k = 0; k < NLD; ++k) {
-      const int r = lane / CPR + KPI * k;
-      const uint32_t row = stage + g8 * C::GSTRIDE + half + r * 128;
-      st_shared_v4(row + ((cc ^ r) * 16),
-                   make_uint4(e4m3x2_to_f16x2(w[k].x), e4m3x2_to_f16x2(w[k].x >> 16),
-                              e4m3x2_to_f16x2(w[k].y), e4m3x2_to_f16x2(w[k].y >> 16)));
-      st_shared_v4(row + (((cc + 1) ^ r) * 16),
-                   make_uint4(e4m3x2_to_f16x2(w[k].z), e4m3x2_to_f16x2(w[k].z >> 16),
-                              e4m3x2_to_f16x2(w[k].w), e4m3x2_to_f16x2(w[k].w >> 16)));
-    }
-    __syncwarp();
+      for (int k = 0; k < NLD; ++k)  // (an odd last block's second half: the stage's next bytes, unused)
+        if (g8 + g < 2 * b1) w[g][k] = ld_shared_v4(raw + ((g8 + g) * 8 + lane / CPR + KPI * k) * D + c * 16);
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+#pragma unroll
+      for (int k = 0; k < NLD; ++k) {
+        if (g8 + g >= 2 * b1) continue;
+        const int r = lane / CPR + KPI * k;
+        const uint32_t row = stage + (g8 + g) * C::GSTRIDE + half + r * 128;
+        const uint4 lo = make_uint4(e4m3x2_to_f16x2(w[g][k].x), e4m3x2_to_f16x2(w[g][k].x >> 16),
+                                    e4m3x2_to_f16x2(w[g][k].y), e4m3x2_to_f16x2(w[g][k].y >> 16));
+        const uint4 hi = make_uint4(e4m3x2_to_f16x2(w[g][k].z), e4m3x2_to_f16x2(w[g][k].z >> 16),
+                                    e4m3x2_to_f16x2(w[g][k].w), e4m3x2_to_f16x2(w[g][k].w >> 16));
+        st_shared_v4(row + (((cc + swap) ^ r) * 16), swap ? hi : lo);
+        st_shared_v4(row + (((cc + 1 - swap) ^ r) * 16), swap ? lo : hi);
+      }
   }
+}
+
+template <int N>
+__device__ __forceinline__ void take_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void give_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // Records of a cut unit: (CTA, piece, slot) holds (m, l) of 128 rows and their
@@ -266,6 +287,9 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
     for (int k = 0; k < C::NBAR; ++k) {
       int count = 1;
       if (k == C::PFULL || k == C::PFULL + 1) count = 4;
+      if (KV8 && ((k >= C::KFULL && k < C::KFULL + C::NK) || (k >= C::VFULL && k < C::VFULL + C::NV) ||
+                  k >= C::KRAWFREE))
+        count = 2;
       if (k == C::OFREE || k == C::SYNC || k == C::QCONV) count = 8;
       if (k >= C::SEGFREE && k < C::SEGFREE + C::SEGS) count = C::SEG_USERS;
       mbar_init(bar(k), count);
@@ -277,7 +301,7 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
     n_q_issued[1] = 0;
     fence_mbar_init();
   }
-  if (warp == 1) {
+  if (warp == 9) {
     tmem_alloc(smem_u32(const_cast<uint32_t*>(tmem_slot)), C::TMEM_COLS);
     tmem_relinquish();
   }
@@ -312,335 +336,12 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
     return id * a.block_size + (t16 & ((1 << a.tile_shift) - 1)) * kBlockSize;
   };
 
-  if (warp == 0) {
-    // ====================================== range walk, Q and K producer
-    if (cta == 0) report_bad_requests(a, lane);
-    const uint64_t policy = l2_policy_evict_first();
-    if (lane == 0) {
-      tma_prefetch_desc(&qmap);
-      tma_prefetch_desc(&kmap);
-      a.splits[cta].c1 = -1;  // no unit cut at the end of this range so far
-    }
-    const int H = a.num_kv_heads;
-    long long st = 0, un = 0;
-    for (int r = lane; r < a.num_seqs; r += 32) {
-      const TreeReq p = tree_req(a, r);
-      un += p.tiles;
-      st += static_cast<long long>(p.tiles) * req_steps(p);
-    }
-    const long long n_steps = warp_sum64(st) * H, n_units = warp_sum64(un) * H;
-    const long long Cw = kStepCost * n_steps + kUnitCost * n_units;
-    // By cost only where every share holds a unit's start and a step, so that every
-    // CTA between a unit's first and last has one of its steps; else by steps.
-    const bool by_cost = div_ll(Cw, a.num_ctas) >= kStepCost + kUnitCost;
-    const long long CT = by_cost ? kStepCost : 1, CS = by_cost ? kUnitCost : 0;
-    const long long Ctot = by_cost ? Cw : n_steps;
-    const long long x0 = Ctot > 0 ? range_lo(Ctot, a.num_ctas, cta) : 0;
-    const long long x1 = Ctot > 0 ? range_lo(Ctot, a.num_ctas, cta + 1) : 0;
-    int seg = 0, g = 0, nq[2] = {0, 0};
-    bool ok = true;
-    // Steps [j, ..) of a unit whose cost starts at cb: step j starts at cb + CS + CT j.
-    auto first_step_at = [&](long long cb, long long x) -> long long {
-      return x <= cb + CS ? 0 : div_ll(x - cb - CS + CT - 1, CT);
-    };
-    if (x0 < x1) {
-      // The request that holds x0, and the cost before it.
-      int r = -1;
-      long long cb = 0;
-      for (int rc = 0; rc < a.num_seqs && r < 0; rc += 32) {
-        const TreeReq p = tree_req(a, rc + lane);
-        const long long cost = (CS + CT * req_steps(p)) * p.tiles * H;
-        long long incl = cost;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += v;
-        }
-        const unsigned hit = __ballot_sync(0xffffffffu, cb + incl > x0);
-        if (hit != 0) {
-          const int first = __ffs(hit) - 1;
-          cb += __shfl_sync(0xffffffffu, incl - cost, first);
-          r = rc + first;
-        } else {
-          cb += __shfl_sync(0xffffffffu, incl, 31);
-        }
-      }
-      TreeReq p = tree_req(a, r);
-      int n_u = req_steps(p);
-      int u = static_cast<int>(div_ll(x0 - cb, CS + CT * n_u));  // unit: kv head, then tile pair
-      cb += u * (CS + CT * n_u);
-      long long j = first_step_at(cb, x0);
-      while (ok) {
-        if (j >= n_u) {  // no step of this unit starts in the range: the next one
-          cb += CS + CT * n_u;
-          j = 0;
-          if (++u == H * p.tiles) {
-            u = 0;
-            do {
-              p = tree_req(a, ++r);
-            } while (p.tiles == 0 && r < a.num_seqs);
-            if (p.tiles == 0) break;  // no more work
-            n_u = req_steps(p);
-          }
-        }
-        if (cb + CS + CT * j >= x1) break;
-        const int j0 = static_cast<int>(j);
-        const int j1 = static_cast<int>(min(static_cast<long long>(n_u), first_step_at(cb, x1)));
-        const int kvh = u / p.tiles, node0 = (u - kvh * p.tiles) * 2 * NPS;
-        const int nodes = min(2 * NPS, p.n - node0);
-        const int nsl = nodes > NPS ? 2 : 1;
-        if (seg >= C::SEGS && !(ok = warp_wait(C::SEGFREE + seg % C::SEGS, ((seg / C::SEGS) - 1) & 1, 60))) break;
-        if (lane == 0) {
-          TreeSeg sg{};
-          sg.r = r;
-          sg.q0 = p.q0;
-          sg.node0 = node0;
-          sg.nodes = nodes;
-          sg.ctx = p.len - p.n;
-          sg.n_new = p.n;
-          sg.j0 = j0;
-          sg.j1 = j1;
-          sg.kvh = kvh;
-          sg.kind = (j0 == 0 && j1 == n_u) ? kWhole : (j0 > 0 ? kHead : kTail);
-          segs[seg % C::SEGS] = sg;
-          mbar_arrive(bar(C::SEGFULL + seg % C::SEGS));
-          if (sg.kind == kTail) {
-            TreeSplit sp;
-            sp.c1 = cta_of_tile(Ctot, a.num_ctas, cb + CS + CT * (n_u - 1));
-            sp.row0 = p.q0 + node0;
-            sp.nodes = nodes;
-            sp.kvh = kvh;
-            a.splits[cta] = sp;
-          }
-        }
-        // Q of both slots, once the last S product of the previous segment is done.
-        if (seg > 0 && !(ok = warp_wait(C::QFREE, (seg - 1) & 1, 61))) break;
-        if (lane == 0) {
-          for (int b = 0; b < nsl; ++b) {
-            mbar_arrive_expect_tx(bar(C::QFULL + b), C::HALVES * G * NPS * 128);
-#pragma unroll
-            for (int h = 0; h < C::HALVES; ++h)
-              tma_load_3d(q_s + b * C::QBYTES + h * C::CHUNK, &qmap, bar(C::QFULL + b), 64 * h, kvh * G,
-                          p.q0 + node0 + b * NPS, policy);
-            n_q_issued[b] = ++nq[b];
-          }
-        }
-        __syncwarp();
-        const int nblk = (p.len + kBlockSize - 1) / kBlockSize;
-        int rowc = tile_rows(r, j0 * 8, nblk, true);
-        for (int jj = j0; jj < j1; ++jj) {
-          const int stg = g % C::NK;
-          if (g >= C::NK && !(ok = warp_wait(C::KFREE + stg, ((g / C::NK) - 1) & 1, 62))) break;
-          const int nb = min(8, nblk - jj * 8);
-          const int full = (KV8 ? C::KRAW : C::KFULL) + stg;
-          if (lane == 0) mbar_arrive_expect_tx(bar(full), nb * (KV8 ? C::RAW_BLOCK : C::BLOCK_BYTES));
-          __syncwarp();
-          if (lane < nb) {
-            if constexpr (KV8)
-              tma_load_3d(k_s + stg * C::TBYTES + C::RAW_OFF + lane * C::RAW_BLOCK, &kmap, bar(full), 0, kvh, rowc,
-                          policy);
-            else
-              tma_load_5d(k_s + stg * C::TBYTES + lane * C::BLOCK_BYTES, &kmap, bar(full), 0, 0, 0, rowc / 8, kvh,
-                          policy);
-          }
-          ++g;
-          if (lane == 0) *n_k_issued = g;
-          if (jj + 1 < j1) rowc = tile_rows(r, (jj + 1) * 8, nblk, true);
-        }
-        ++seg;
-        if (!ok || j1 < n_u) break;  // the range ends inside this unit
-        j = n_u;
-      }
-    }
-    if (ok && seg >= C::SEGS) ok = warp_wait(C::SEGFREE + seg % C::SEGS, ((seg / C::SEGS) - 1) & 1, 67);
-    if (ok && lane == 0) {
-      segs[seg % C::SEGS].kind = kEnd;
-      mbar_arrive(bar(C::SEGFULL + seg % C::SEGS));
-    }
-    if (!ok && lane == 0) *fail_flag = 1;
-  } else if (warp == 10) {
-    // =========================================================== V producer
-    const uint64_t policy = l2_policy_evict_first();
-    if (lane == 0) tma_prefetch_desc(&vmap);
-    bool ok = true;
-    int g = 0;
-    for (int seg = 0; ok; ++seg) {
-      const int slot = seg % C::SEGS;
-      if (!(ok = warp_wait(C::SEGFULL + slot, (seg / C::SEGS) & 1, 63))) break;
-      const TreeSeg sg = segs[slot];
-      if (sg.kind == kEnd) break;
-      const int nblk = (sg.ctx + sg.n_new + kBlockSize - 1) / kBlockSize;
-      int rowc = tile_rows(sg.r, sg.j0 * 8, nblk, false);
-      for (int jj = sg.j0; jj < sg.j1; ++jj) {
-        const int stg = g % C::NV;
-        if (g >= C::NV && !(ok = warp_wait(C::VFREE + stg, ((g / C::NV) - 1) & 1, 64))) break;
-        const int nb = min(8, nblk - jj * 8);
-        const int full = (KV8 ? C::VRAW : C::VFULL) + stg;
-        if (lane == 0) mbar_arrive_expect_tx(bar(full), nb * (KV8 ? C::RAW_BLOCK : C::BLOCK_BYTES));
-        __syncwarp();
-        if (lane < nb) {
-          if constexpr (KV8)
-            tma_load_3d(v_s + stg * C::TBYTES + C::RAW_OFF + lane * C::RAW_BLOCK, &vmap, bar(full), 0, sg.kvh, rowc,
-                        policy);
-          else
-            tma_load_5d(v_s + stg * C::TBYTES + lane * C::BLOCK_BYTES, &vmap, bar(full), 0, 0, 0, rowc / 8, sg.kvh,
-                        policy);
-        }
-        ++g;
-        if (lane == 0) *n_v_issued = g;
-        if (jj + 1 < sg.j1) rowc = tile_rows(sg.r, (jj + 1) * 8, nblk, false);
-      }
-      __syncwarp();
-      if (ok && lane == 0) mbar_arrive(bar(C::SEGFREE + slot));
-    }
-    if (!ok && lane == 0) *fail_flag = 1;
-  } else if (warp == 1) {
-    // ========================================================== MMA issuer
-    if (lane == 0) {
-      bool ok = true;
-      int g = 0, pc[2] = {0, 0}, qc[2] = {0, 0};
-      auto wait = [&](int k, uint32_t parity, int where) -> bool {
-        if (*fail_flag) return false;
-        if (!mbar_wait(bar(k), parity)) {
-          give_up(where);
-          return false;
-        }
-        return true;
-      };
-      // S of slot b = Q (buffer qb) K^T of K step gk, into TMEM columns 128 b ..
-      auto issue_s = [&](int b, int qb, int gk) {
-        const uint32_t kst = k_s + (gk % C::NK) * C::TBYTES;
-        const uint32_t qst = q_s + qb * C::QBYTES;
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t qoff = (ks / 4) * C::CHUNK + (ks % 4) * 32;
-          const uint32_t koff = (ks / 4) * 1024 + (ks % 4) * 32;
-          umma_bf16(tmem + b * C::BN, sdesc_sw128(qst + qoff, 16, 1024), sdesc_sw128(kst + koff, 16, C::GSTRIDE),
-                    C::IDESC_S, ks > 0);
-        }
-        umma_commit(bar(C::SFULL + b));
-      };
-      // O of slot b += P V of V step gv (P: 16 bits in TMEM columns 128 b ..).
-      auto issue_pv = [&](int b, int gv, bool acc) {
-        const uint32_t vst = v_s + (gv % C::NV) * C::TBYTES;
-#pragma unroll
-        for (int ks = 0; ks < C::BN / 16; ++ks)
-          umma_tmem_a(tmem + 256 + b * D, tmem + b * C::BN + ks * 8,
-                      sdesc_sw128(vst + ks * C::BLOCK_BYTES, 1024, C::GSTRIDE), C::IDESC_O,
-                      (acc || ks > 0) ? 1u : 0u);
-      };
-      auto k_landed = [&](int gk) -> bool {
-        const bool good = wait(C::KFULL + gk % C::NK, (gk / C::NK) & 1, 72);
-        tc_fence_after();
-        return good;
-      };
-      for (int seg = 0; ok; ++seg) {
-        const int slot = seg % C::SEGS;
-        if (!(ok = wait(C::SEGFULL + slot, (seg / C::SEGS) & 1, 70))) break;
-        const TreeSeg sg = segs[slot];
-        if (sg.kind == kEnd) break;
-        const int n = sg.j1 - sg.j0;
-        const bool two = sg.nodes > NPS;
-        if constexpr (KV8) {
-          ok = wait(C::QCONV, seg & 1, 71);
-        } else {
-          for (int b = 0; b < (two ? 2 : 1) && ok; ++b) ok = wait(C::QFULL + b, qc[b]++ & 1, 71);
-        }
-        if (!ok) break;
-        // Step k of slot b: (two tiles) both slots take every step, or (one tile) they
-        // take steps in turn.
-        if (two) {
-          if (!(ok = k_landed(g))) break;
-          issue_s(0, 0, g);
-          issue_s(1, 1, g);
-          umma_commit(bar(C::KFREE + g % C::NK));
-          if (n == 1) umma_commit(bar(C::QFREE));
-        } else {
-          for (int k = 0; k < min(n, 2) && ok; ++k) {
-            if (!(ok = k_landed(g + k))) break;
-            issue_s(k, 0, g + k);
-            umma_commit(bar(C::KFREE + (g + k) % C::NK));
-          }
-          if (!ok) break;
-          if (n <= 2) umma_commit(bar(C::QFREE));
-        }
-        for (int k = 0; k < n && ok; ++k) {
-          const int gk = g + k;
-          if (!(ok = wait(C::VFULL + gk % C::NV, (gk / C::NV) & 1, 73))) break;
-          if (k == 0 && seg > 0 && !(ok = wait(C::OFREE, (seg - 1) & 1, 76))) break;
-          if (two) {
-            for (int b = 0; b < 2 && ok; ++b) {
-              if (!(ok = wait(C::PFULL + b, pc[b]++ & 1, 75))) break;
-              tc_fence_after();
-              issue_pv(b, gk, k > 0);
-              if (k + 1 < n) {
-                if (b == 0 && !(ok = k_landed(gk + 1))) break;
-                issue_s(b, b, gk + 1);
-              }
-            }
-            if (!ok) break;
-            umma_commit(bar(C::VFREE + gk % C::NV));
-            if (k + 1 < n) umma_commit(bar(C::KFREE + (gk + 1) % C::NK));
-            if (k + 2 == n) umma_commit(bar(C::QFREE));
-          } else {
-            const int b = k & 1;
-            if (!(ok = wait(C::PFULL + b, pc[b]++ & 1, 75))) break;
-            tc_fence_after();
-            issue_pv(b, gk, k > 1);
-            umma_commit(bar(C::VFREE + gk % C::NV));
-            if (k + 2 < n) {
-              if (!(ok = k_landed(gk + 2))) break;
-              issue_s(b, 0, gk + 2);
-              umma_commit(bar(C::KFREE + (gk + 2) % C::NK));
-              if (k + 3 == n) umma_commit(bar(C::QFREE));
-            }
-          }
-        }
-        if (!ok) break;
-        umma_commit(bar(C::OFULL));
-        g += n;
-        mbar_arrive(bar(C::SEGFREE + slot));
-      }
-      if (!ok) *fail_flag = 1;
-      // Every MMA issued has completed before TMEM can be released.
-      umma_commit(bar(C::DRAIN));
-      (void)mbar_wait(bar(C::DRAIN), 0);
-    }
-    __syncwarp();
-  } else if (warp >= 11) {
-    // =================================================== e4m3 -> f16 (KV8)
-    if constexpr (KV8) {
-      const bool is_v = warp >= 13;
-      const int turn = (warp - 11) & 1;
-      const int NS = is_v ? C::NV : C::NK;
-      const int raw = is_v ? C::VRAW : C::KRAW, full = is_v ? C::VFULL : C::KFULL;
-      const uint32_t base = is_v ? v_s : k_s;
-      bool ok = true;
-      int g = 0;
-      for (int seg = 0; ok; ++seg) {
-        const int slot = seg % C::SEGS;
-        if (!(ok = warp_wait(C::SEGFULL + slot, (seg / C::SEGS) & 1, 68))) break;
-        const TreeSeg sg = segs[slot];
-        if (sg.kind == kEnd) break;
-        const int nblk = (sg.ctx + sg.n_new + kBlockSize - 1) / kBlockSize;
-        for (int jj = sg.j0; jj < sg.j1; ++jj, ++g) {
-          if ((g & 1) != turn) continue;
-          const int stg = g % NS;
-          if (!(ok = warp_wait(raw + stg, (g / NS) & 1, is_v ? 66 : 65))) break;
-          convert_step<D, KV8>(base + stg * C::TBYTES, min(8, nblk - jj * 8), lane);
-          fence_proxy_async_smem();  // read by the tensor core
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(full + stg));
-        }
-        __syncwarp();
-        if (ok && lane == 0) mbar_arrive(bar(C::SEGFREE + slot));
-      }
-      if (!ok && lane == 0) *fail_flag = 1;
-    }
-  } else {
+  // (The warps of a warpgroup change their registers together.)
+  if (warp < 8) {
+    take_registers<C::REGS_SOFTMAX>();
     // ============================================================ softmax
-    // Warps 2-5 serve slot 0, 6-9 slot 1; warp w owns TMEM lanes 32 (w % 4) .. + 31.
-    const int b = warp < 6 ? 0 : 1;
+    // Warps 0-3 serve slot 0, 4-7 slot 1; warp w owns TMEM lanes 32 (w % 4) .. + 31.
+    const int b = warp >> 2;
     const int i_row = (warp & 3) * 32 + lane;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t tm_s = lane_base + b * C::BN;
@@ -662,7 +363,7 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         for (int qb = 0; qb < (two ? 2 : 1) && ok; ++qb) {
           if (!(ok = warp_wait(C::QFULL + qb, qn[qb]++ & 1, 79))) break;
           const uint32_t qst = q_s + qb * C::QBYTES;
-          for (int i = tid - 64; i < C::QBYTES / 16; i += 256) {
+          for (int i = tid; i < C::QBYTES / 16; i += 256) {
             const uint4 w = ld_shared_v4(qst + i * 16);
             st_shared_v4(qst + i * 16, make_uint4(bf16x2_to_f16x2(w.x), bf16x2_to_f16x2(w.y),
                                                   bf16x2_to_f16x2(w.z), bf16x2_to_f16x2(w.w)));
@@ -697,34 +398,20 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
 #pragma unroll
             for (int i = 0; i < 4; ++i) seen[i] = __funnelshift_r(w[i], w[i + 1], sh);
           }
-          constexpr int W = C::W;
-          auto load = [&](int c, uint32_t (&sr)[W]) {
+          uint32_t sr[C::BN];
 #pragma unroll
-            for (int i = 0; i < W; i += 32) tmem_ld32_async(tm_s + c * W + i, sr + i);
-            tmem_wait_ld();
-            pin(sr);
-            if (masked) {
+          for (int i = 0; i < C::BN; i += 32) tmem_ld32_async(tm_s + i, sr + i);
+          tmem_wait_ld();
+          pin(sr);
+          if (masked) {
 #pragma unroll
-              for (int i = 0; i < W; i += 32) {
-                uint32_t word = seen[0];
-                if ((c * W + i) / 32 == 1) word = seen[1];
-                if ((c * W + i) / 32 == 2) word = seen[2];
-                if ((c * W + i) / 32 == 3) word = seen[3];
-#pragma unroll
-                for (int e = 0; e < 32; ++e) sr[i + e] = word >> e & 1u ? sr[i + e] : 0xff800000u;  // -inf
-              }
-            }
-          };
-          // Pass 1: the row's maximum; the reference moves before any weight.
+            for (int e = 0; e < C::BN; ++e) sr[e] = seen[e / 32] >> (e % 32) & 1u ? sr[e] : 0xff800000u;  // -inf
+          }
+          // The row's maximum; the reference moves before any weight.
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int c = 0; c < C::BN / W; ++c) {
-            uint32_t sr[W];
-            load(c, sr);
-#pragma unroll
-            for (int e = 0; e < W; e += 2)
-              mx[(e / 2) % 4] = fmax3(mx[(e / 2) % 4], __uint_as_float(sr[e]), __uint_as_float(sr[e + 1]));
-          }
+          for (int e = 0; e < C::BN; e += 2)
+            mx[(e / 2) % 4] = fmax3(mx[(e / 2) % 4], __uint_as_float(sr[e]), __uint_as_float(sr[e + 1]));
           const float m_tile = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
           const bool moved = m_tile > m_ref + kRescaleSlack;
           float alpha = 1.f;
@@ -733,22 +420,20 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
             l_run *= alpha;
             m_ref = m_tile;
           }
-          // Pass 2: the weights, 16 bits each, over columns that have been read.
+          // The weights, 16 bits each, over the scores' columns.
           const float2 sl = make_float2(sl2, sl2), mm = make_float2(-m_ref, -m_ref);
           float2 sum[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-          for (int c = 0; c < C::BN / W; ++c) {
-            uint32_t sr[W], pk[W / 2];
-            load(c, sr);
+          for (int c = 0; c < C::BN; c += 32) {
+            uint32_t pk[16];
 #pragma unroll
-            for (int e = 0; e < W; e += 2) {
+            for (int e = c; e < c + 32; e += 2) {
               const float2 x = __ffma2_rn(make_float2(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])), sl, mm);
               const float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
-              pk[e / 2] = KV8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+              pk[(e - c) / 2] = KV8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
               sum[(e / 2) % 4] = __fadd2_rn(sum[(e / 2) % 4], make_float2(p0, p1));
             }
-#pragma unroll
-            for (int i = 0; i < W / 2; i += 16) tmem_st16_async(tm_s + c * (W / 2) + i, pk + i);
+            tmem_st16_async(tm_s + c / 2, pk);
           }
           const float2 ps = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
           l_run += ps.x + ps.y;
@@ -781,7 +466,6 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
           if ((warp & 3) == 1) lo = any[1], hi = any[2];
           if ((warp & 3) == 2) lo = any[2], hi = any[3];
           if ((warp & 3) == 3) lo = any[3], hi = any[4];
-          // (slot 0's warps 2 - 5 and slot 1's 6 - 9: warp & 3 names every quarter once)
           if (!(__funnelshift_r(lo, hi, sh) >> lane & 1u)) {
 #pragma unroll
             for (int c = 0; c < C::HALVES * 8; ++c)
@@ -866,6 +550,347 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
       }
     }
     if (!ok && lane == 0) *fail_flag = 1;
+  } else {
+    give_registers<C::REGS_OTHER>();
+    if (warp == 8) {
+      // ====================================== range walk, Q and K producer
+      if (cta == 0) report_bad_requests(a, lane);
+      const uint64_t policy = l2_policy_evict_first();
+      if (lane == 0) {
+        tma_prefetch_desc(&qmap);
+        tma_prefetch_desc(&kmap);
+        a.splits[cta].c1 = -1;  // no unit cut at the end of this range so far
+      }
+      const int H = a.num_kv_heads;
+      long long st = 0, un = 0;
+      for (int r = lane; r < a.num_seqs; r += 32) {
+        const TreeReq p = tree_req(a, r);
+        un += p.tiles;
+        st += static_cast<long long>(p.tiles) * req_steps(p);
+      }
+      const long long n_steps = warp_sum64(st) * H, n_units = warp_sum64(un) * H;
+      const long long Cw = kStepCost * n_steps + kUnitCost * n_units;
+      // By cost only where every share holds a unit's start and a step, so that every
+      // CTA between a unit's first and last has one of its steps; else by steps.
+      const bool by_cost = div_ll(Cw, a.num_ctas) >= kStepCost + kUnitCost;
+      const long long CT = by_cost ? kStepCost : 1, CS = by_cost ? kUnitCost : 0;
+      const long long Ctot = by_cost ? Cw : n_steps;
+      const long long x0 = Ctot > 0 ? range_lo(Ctot, a.num_ctas, cta) : 0;
+      const long long x1 = Ctot > 0 ? range_lo(Ctot, a.num_ctas, cta + 1) : 0;
+      int seg = 0, g = 0, nq[2] = {0, 0};
+      bool ok = true;
+      // Steps [j, ..) of a unit whose cost starts at cb: step j starts at cb + CS + CT j.
+      auto first_step_at = [&](long long cb, long long x) -> long long {
+        return x <= cb + CS ? 0 : div_ll(x - cb - CS + CT - 1, CT);
+      };
+      if (x0 < x1) {
+        // The request that holds x0, and the cost before it.
+        int r = -1;
+        long long cb = 0;
+        for (int rc = 0; rc < a.num_seqs && r < 0; rc += 32) {
+          const TreeReq p = tree_req(a, rc + lane);
+          const long long cost = (CS + CT * req_steps(p)) * p.tiles * H;
+          long long incl = cost;
+  #pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+          }
+          const unsigned hit = __ballot_sync(0xffffffffu, cb + incl > x0);
+          if (hit != 0) {
+            const int first = __ffs(hit) - 1;
+            cb += __shfl_sync(0xffffffffu, incl - cost, first);
+            r = rc + first;
+          } else {
+            cb += __shfl_sync(0xffffffffu, incl, 31);
+          }
+        }
+        TreeReq p = tree_req(a, r);
+        int n_u = req_steps(p);
+        int u = static_cast<int>(div_ll(x0 - cb, CS + CT * n_u));  // unit: kv head, then tile pair
+        cb += u * (CS + CT * n_u);
+        long long j = first_step_at(cb, x0);
+        while (ok) {
+          if (j >= n_u) {  // no step of this unit starts in the range: the next one
+            cb += CS + CT * n_u;
+            j = 0;
+            if (++u == H * p.tiles) {
+              u = 0;
+              do {
+                p = tree_req(a, ++r);
+              } while (p.tiles == 0 && r < a.num_seqs);
+              if (p.tiles == 0) break;  // no more work
+              n_u = req_steps(p);
+            }
+          }
+          if (cb + CS + CT * j >= x1) break;
+          const int j0 = static_cast<int>(j);
+          const int j1 = static_cast<int>(min(static_cast<long long>(n_u), first_step_at(cb, x1)));
+          const int kvh = u / p.tiles, node0 = (u - kvh * p.tiles) * 2 * NPS;
+          const int nodes = min(2 * NPS, p.n - node0);
+          const int nsl = nodes > NPS ? 2 : 1;
+          if (seg >= C::SEGS && !(ok = warp_wait(C::SEGFREE + seg % C::SEGS, ((seg / C::SEGS) - 1) & 1, 60))) break;
+          if (lane == 0) {
+            TreeSeg sg{};
+            sg.r = r;
+            sg.q0 = p.q0;
+            sg.node0 = node0;
+            sg.nodes = nodes;
+            sg.ctx = p.len - p.n;
+            sg.n_new = p.n;
+            sg.j0 = j0;
+            sg.j1 = j1;
+            sg.kvh = kvh;
+            sg.kind = (j0 == 0 && j1 == n_u) ? kWhole : (j0 > 0 ? kHead : kTail);
+            segs[seg % C::SEGS] = sg;
+            mbar_arrive(bar(C::SEGFULL + seg % C::SEGS));
+            if (sg.kind == kTail) {
+              TreeSplit sp;
+              sp.c1 = cta_of_tile(Ctot, a.num_ctas, cb + CS + CT * (n_u - 1));
+              sp.row0 = p.q0 + node0;
+              sp.nodes = nodes;
+              sp.kvh = kvh;
+              a.splits[cta] = sp;
+            }
+          }
+          // Q of both slots, once the last S product of the previous segment is done.
+          if (seg > 0 && !(ok = warp_wait(C::QFREE, (seg - 1) & 1, 61))) break;
+          if (lane == 0) {
+            for (int b = 0; b < nsl; ++b) {
+              mbar_arrive_expect_tx(bar(C::QFULL + b), C::HALVES * G * NPS * 128);
+  #pragma unroll
+              for (int h = 0; h < C::HALVES; ++h)
+                tma_load_3d(q_s + b * C::QBYTES + h * C::CHUNK, &qmap, bar(C::QFULL + b), 64 * h, kvh * G,
+                            p.q0 + node0 + b * NPS, policy);
+              n_q_issued[b] = ++nq[b];
+            }
+          }
+          __syncwarp();
+          const int nblk = (p.len + kBlockSize - 1) / kBlockSize;
+          int rowc = tile_rows(r, j0 * 8, nblk, true);
+          for (int jj = j0; jj < j1; ++jj) {
+            constexpr int NS = KV8 ? C::NR : C::NK;
+            const int stg = g % NS;
+            if (g >= NS && !(ok = warp_wait((KV8 ? C::KRAWFREE : C::KFREE) + stg, ((g / NS) - 1) & 1, 62))) break;
+            const int nb = min(8, nblk - jj * 8);
+            const int full = (KV8 ? C::KRAW : C::KFULL) + stg;
+            if (lane == 0) mbar_arrive_expect_tx(bar(full), nb * (KV8 ? C::RAW_BLOCK : C::BLOCK_BYTES));
+            __syncwarp();
+            if (lane < nb) {
+              if constexpr (KV8)
+                tma_load_3d(sbase + C::OFF_KRAW + stg * C::RAW_BYTES + lane * C::RAW_BLOCK, &kmap, bar(full), 0, kvh,
+                            rowc, policy);
+              else
+                tma_load_5d(k_s + stg * C::TBYTES + lane * C::BLOCK_BYTES, &kmap, bar(full), 0, 0, 0, rowc / 8, kvh,
+                            policy);
+            }
+            ++g;
+            if (lane == 0) *n_k_issued = g;
+            if (jj + 1 < j1) rowc = tile_rows(r, (jj + 1) * 8, nblk, true);
+          }
+          ++seg;
+          if (!ok || j1 < n_u) break;  // the range ends inside this unit
+          j = n_u;
+        }
+      }
+      if (ok && seg >= C::SEGS) ok = warp_wait(C::SEGFREE + seg % C::SEGS, ((seg / C::SEGS) - 1) & 1, 67);
+      if (ok && lane == 0) {
+        segs[seg % C::SEGS].kind = kEnd;
+        mbar_arrive(bar(C::SEGFULL + seg % C::SEGS));
+      }
+      if (!ok && lane == 0) *fail_flag = 1;
+    } else if (warp == 10) {
+      // =========================================================== V producer
+      const uint64_t policy = l2_policy_evict_first();
+      if (lane == 0) tma_prefetch_desc(&vmap);
+      bool ok = true;
+      int g = 0;
+      for (int seg = 0; ok; ++seg) {
+        const int slot = seg % C::SEGS;
+        if (!(ok = warp_wait(C::SEGFULL + slot, (seg / C::SEGS) & 1, 63))) break;
+        const TreeSeg sg = segs[slot];
+        if (sg.kind == kEnd) break;
+        const int nblk = (sg.ctx + sg.n_new + kBlockSize - 1) / kBlockSize;
+        int rowc = tile_rows(sg.r, sg.j0 * 8, nblk, false);
+        for (int jj = sg.j0; jj < sg.j1; ++jj) {
+          constexpr int NS = KV8 ? C::NR : C::NV;
+          const int stg = g % NS;
+          if (g >= NS && !(ok = warp_wait((KV8 ? C::VRAWFREE : C::VFREE) + stg, ((g / NS) - 1) & 1, 64))) break;
+          const int nb = min(8, nblk - jj * 8);
+          const int full = (KV8 ? C::VRAW : C::VFULL) + stg;
+          if (lane == 0) mbar_arrive_expect_tx(bar(full), nb * (KV8 ? C::RAW_BLOCK : C::BLOCK_BYTES));
+          __syncwarp();
+          if (lane < nb) {
+            if constexpr (KV8)
+              tma_load_3d(sbase + C::OFF_VRAW + stg * C::RAW_BYTES + lane * C::RAW_BLOCK, &vmap, bar(full), 0, sg.kvh,
+                          rowc, policy);
+            else
+              tma_load_5d(v_s + stg * C::TBYTES + lane * C::BLOCK_BYTES, &vmap, bar(full), 0, 0, 0, rowc / 8, sg.kvh,
+                          policy);
+          }
+          ++g;
+          if (lane == 0) *n_v_issued = g;
+          if (jj + 1 < sg.j1) rowc = tile_rows(sg.r, (jj + 1) * 8, nblk, false);
+        }
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(bar(C::SEGFREE + slot));
+      }
+      if (!ok && lane == 0) *fail_flag = 1;
+    } else if (warp == 9) {
+      // ========================================================== MMA issuer
+      if (lane == 0) {
+        bool ok = true;
+        int g = 0, pc[2] = {0, 0}, qc[2] = {0, 0};
+        auto wait = [&](int k, uint32_t parity, int where) -> bool {
+          if (*fail_flag) return false;
+          if (!mbar_wait(bar(k), parity)) {
+            give_up(where);
+            return false;
+          }
+          return true;
+        };
+        // Operand descriptors differ by their start addresses alone, the low word's low
+        // bits: one is built for each operand, offsets are added.  (Built anew for every
+        // product, the issue of the 32 of a step took longer than the tensor core.)
+        const uint64_t qd = sdesc_sw128(q_s, 16, 1024);
+        const uint64_t kd = sdesc_sw128(k_s, 16, C::GSTRIDE);
+        const uint64_t vd = sdesc_sw128(v_s, 1024, C::GSTRIDE);
+        // S of slot b = Q (buffer qb) K^T of K step gk, into TMEM columns 128 b ..
+        auto issue_s = [&](int b, int qb, int gk) {
+          const uint64_t q0 = qd + qb * (C::QBYTES >> 4), k0 = kd + (gk % C::NK) * (C::TBYTES >> 4);
+          const uint32_t ts = tmem + b * C::BN;
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks)
+            umma_bf16(ts, q0 + (((ks / 4) * C::CHUNK + (ks % 4) * 32) >> 4),
+                      k0 + (((ks / 4) * 1024 + (ks % 4) * 32) >> 4), C::IDESC_S, ks > 0);
+          umma_commit(bar(C::SFULL + b));
+        };
+        // O of slot b += P V of V step gv (P: 16 bits in TMEM columns 128 b ..).
+        auto issue_pv = [&](int b, int gv, bool acc) {
+          const uint64_t v0 = vd + (gv % C::NV) * (C::TBYTES >> 4);
+          const uint32_t to = tmem + 256 + b * D, tp = tmem + b * C::BN;
+          umma_tmem_a(to, tp, v0, C::IDESC_O, acc ? 1u : 0u);
+#pragma unroll
+          for (int ks = 1; ks < C::BN / 16; ++ks)
+            umma_tmem_a(to, tp + ks * 8, v0 + ((ks * C::BLOCK_BYTES) >> 4), C::IDESC_O, 1u);
+        };
+        auto k_landed = [&](int gk) -> bool {
+          const bool good = wait(C::KFULL + gk % C::NK, (gk / C::NK) & 1, 72);
+          tc_fence_after();
+          return good;
+        };
+        for (int seg = 0; ok; ++seg) {
+          const int slot = seg % C::SEGS;
+          if (!(ok = wait(C::SEGFULL + slot, (seg / C::SEGS) & 1, 70))) break;
+          const TreeSeg sg = segs[slot];
+          if (sg.kind == kEnd) break;
+          const int n = sg.j1 - sg.j0;
+          const bool two = sg.nodes > NPS;
+          if constexpr (KV8) {
+            ok = wait(C::QCONV, seg & 1, 71);
+          } else {
+            for (int b = 0; b < (two ? 2 : 1) && ok; ++b) ok = wait(C::QFULL + b, qc[b]++ & 1, 71);
+          }
+          if (!ok) break;
+          // Step k of slot b: (two tiles) both slots take every step, or (one tile) they
+          // take steps in turn.
+          if (two) {
+            if (!(ok = k_landed(g))) break;
+            issue_s(0, 0, g);
+            issue_s(1, 1, g);
+            umma_commit(bar(C::KFREE + g % C::NK));
+            if (n == 1) umma_commit(bar(C::QFREE));
+          } else {
+            for (int k = 0; k < min(n, 2) && ok; ++k) {
+              if (!(ok = k_landed(g + k))) break;
+              issue_s(k, 0, g + k);
+              umma_commit(bar(C::KFREE + (g + k) % C::NK));
+            }
+            if (!ok) break;
+            if (n <= 2) umma_commit(bar(C::QFREE));
+          }
+          for (int k = 0; k < n && ok; ++k) {
+            const int gk = g + k;
+            if (!(ok = wait(C::VFULL + gk % C::NV, (gk / C::NV) & 1, 73))) break;
+            if (k == 0 && seg > 0 && !(ok = wait(C::OFREE, (seg - 1) & 1, 76))) break;
+            if (two) {
+              for (int b = 0; b < 2 && ok; ++b) {
+                if (!(ok = wait(C::PFULL + b, pc[b]++ & 1, 75))) break;
+                tc_fence_after();
+                issue_pv(b, gk, k > 0);
+                if (k + 1 < n) {
+                  if (b == 0 && !(ok = k_landed(gk + 1))) break;
+                  issue_s(b, b, gk + 1);
+                }
+              }
+              if (!ok) break;
+              umma_commit(bar(C::VFREE + gk % C::NV));
+              if (k + 1 < n) umma_commit(bar(C::KFREE + (gk + 1) % C::NK));
+              if (k + 2 == n) umma_commit(bar(C::QFREE));
+            } else {
+              const int b = k & 1;
+              if (!(ok = wait(C::PFULL + b, pc[b]++ & 1, 75))) break;
+              tc_fence_after();
+              issue_pv(b, gk, k > 1);
+              umma_commit(bar(C::VFREE + gk % C::NV));
+              if (k + 2 < n) {
+                if (!(ok = k_landed(gk + 2))) break;
+                issue_s(b, 0, gk + 2);
+                umma_commit(bar(C::KFREE + (gk + 2) % C::NK));
+                if (k + 3 == n) umma_commit(bar(C::QFREE));
+              }
+            }
+          }
+          if (!ok) break;
+          umma_commit(bar(C::OFULL));
+          g += n;
+          mbar_arrive(bar(C::SEGFREE + slot));
+        }
+        if (!ok) *fail_flag = 1;
+        // Every MMA issued has completed before TMEM can be released.
+        umma_commit(bar(C::DRAIN));
+        (void)mbar_wait(bar(C::DRAIN), 0);
+      }
+      __syncwarp();
+    } else if (warp >= 11) {
+      // =================================================== e4m3 -> f16 (KV8)
+      if constexpr (KV8) {
+        if (warp >= 12) {
+          const bool is_v = warp >= 14;
+          const int half = warp & 1;
+          const int NS = is_v ? C::NV : C::NK;
+          const int raw = is_v ? C::VRAW : C::KRAW, raw_free = is_v ? C::VRAWFREE : C::KRAWFREE;
+          const int full = is_v ? C::VFULL : C::KFULL, free = is_v ? C::VFREE : C::KFREE;
+          const uint32_t base = is_v ? v_s : k_s;
+          const uint32_t raw_base = sbase + (is_v ? C::OFF_VRAW : C::OFF_KRAW);
+          bool ok = true;
+          int g = 0;
+          for (int seg = 0; ok; ++seg) {
+            const int slot = seg % C::SEGS;
+            if (!(ok = warp_wait(C::SEGFULL + slot, (seg / C::SEGS) & 1, 68))) break;
+            const TreeSeg sg = segs[slot];
+            if (sg.kind == kEnd) break;
+            const int nblk = (sg.ctx + sg.n_new + kBlockSize - 1) / kBlockSize;
+            for (int jj = sg.j0; jj < sg.j1; ++jj, ++g) {
+              const int rs = g % C::NR, stg = g % NS;
+              if (!(ok = warp_wait(raw + rs, (g / C::NR) & 1, is_v ? 66 : 65))) break;
+              if (g >= NS && !(ok = warp_wait(free + stg, ((g / NS) - 1) & 1, 69))) break;
+              convert_half<D, KV8>(raw_base + rs * C::RAW_BYTES, base + stg * C::TBYTES, 4 * half,
+                                   min(4 * half + 4, nblk - jj * 8), lane);
+              fence_proxy_async_smem();  // the f16 step is read by the tensor core, the raw one overwritten by a copy
+              __syncwarp();
+              if (lane == 0) {
+                mbar_arrive(bar(full + stg));
+                mbar_arrive(bar(raw_free + rs));
+              }
+            }
+            __syncwarp();
+            if (ok && lane == 0) mbar_arrive(bar(C::SEGFREE + slot));
+          }
+          if (!ok && lane == 0) *fail_flag = 1;
+        }
+      }
+    }
   }
 
   __syncthreads();
@@ -873,14 +898,15 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
     // Let copies still in flight land before TMEM is released and the CTA leaves (bounded).
     const int nk = *n_k_issued, nv = *n_v_issued;
     const int kb = KV8 ? C::KRAW : C::KFULL, vb = KV8 ? C::VRAW : C::VFULL;
-    for (int i = max(0, nk - C::NK); i < nk; ++i) (void)mbar_wait(bar(kb + i % C::NK), (i / C::NK) & 1);
-    for (int i = max(0, nv - C::NV); i < nv; ++i) (void)mbar_wait(bar(vb + i % C::NV), (i / C::NV) & 1);
+    constexpr int SK = KV8 ? C::NR : C::NK, SV = KV8 ? C::NR : C::NV;
+    for (int i = max(0, nk - SK); i < nk; ++i) (void)mbar_wait(bar(kb + i % SK), (i / SK) & 1);
+    for (int i = max(0, nv - SV); i < nv; ++i) (void)mbar_wait(bar(vb + i % SV), (i / SV) & 1);
     for (int b = 0; b < 2; ++b)
       if (n_q_issued[b] > 0) (void)mbar_wait(bar(C::QFULL + b), (n_q_issued[b] - 1) & 1);
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) {
+  if (warp == 9) {
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM_COLS);
   }
@@ -949,6 +975,10 @@ cudaError_t launch_impl(const TreeArgs& a, const CUtensorMap& qmap, const CUtens
     const cudaError_t err =
         cudaFuncSetAttribute(tree_attention_kernel<D, KV8>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (err != cudaSuccess) return err;
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, tree_attention_kernel<D, KV8>) != cudaSuccess ||
+        fa.numRegs * C::THREADS < C::REGS_SUM)
+      return cudaErrorInvalidConfiguration;
     attr_set[dev] = true;
   }
   const cudaError_t err = launch_overlapped(tree_attention_kernel<D, KV8>, dim3(a.num_ctas), dim3(C::THREADS), C::SMEM,
