@@ -29,7 +29,7 @@
 //   where few long contexts are split over every SM.
 // * Warps: 0-3 softmax of slot 0, 4-7 of slot 1 (thread = row, its 128 scores of a
 //   step in registers, which the other warps give up: setmaxnreg); 8 range walk, Q
-//   and K copies (TMA); 9 MMA issue; 10 V copies; over e4m3 caches 12-13 turn landed
+//   and K copies (TMA); 9 and 11 MMA issue of a slot each; 10 V copies; over e4m3 caches 12-13 turn landed
 //   K steps into f16, 14-15 V steps.
 // A step that holds nodes takes its mask from the row's words; V of keys that no
 // row of the unit sees is zeroed before the product (a zero weight does not
@@ -72,15 +72,19 @@ struct TreeCfg {
   static constexpr int GSTRIDE = HALVES * 1024;
   // A V stage is held from its copy to the end of its step, a K stage only to S.
   // e4m3: landed bytes have stages of their own, free again once converted.
-  static constexpr int NK = KV8 ? (D == 128 ? 1 : 2) : (D == 128 ? 2 : 5);
+  // NK is even (see the MMA issue).
+  static constexpr int NK = KV8 ? 2 : (D == 128 ? 2 : 4);
   static constexpr int NV = KV8 ? (D == 128 ? 2 : 3) : (D == 128 ? 3 : 6);
+  // e4m3 at head_dim 128: one K stage has room of its own; the other is slot 1's Q
+  // buffer, which a unit of one tile does not need (two tiles: one stage).
+  static constexpr bool ALIAS = KV8 && D == 128;
   static constexpr int NR = KV8 ? (D == 128 ? 2 : 4) : 0;  // raw K stages = raw V stages
   static constexpr int RAW_BLOCK = 16 * D;
   static constexpr int RAW_BYTES = 128 * D;
   static constexpr int SEGS = 4;                    // segment records in flight
   static constexpr int OFF_Q = 0;                   // [2 slots]
   static constexpr int OFF_K = 2 * QBYTES;
-  static constexpr int OFF_V = OFF_K + NK * TBYTES;
+  static constexpr int OFF_V = OFF_K + (ALIAS ? 1 : NK) * TBYTES;
   static constexpr int OFF_KRAW = OFF_V + NV * TBYTES;
   static constexpr int OFF_VRAW = OFF_KRAW + NR * RAW_BYTES;
   static constexpr int OFF_SEG = OFF_VRAW + NR * RAW_BYTES;
@@ -88,7 +92,7 @@ struct TreeCfg {
   static constexpr int OFF_BAR = OFF_XCH + 2 * 128 * 8;
   // Barriers
   static constexpr int KFULL = 0;                // [NK] K step landed (e4m3: converted)
-  static constexpr int KFREE = KFULL + NK;       // [NK] the S products that read it are done
+  static constexpr int KFREE = KFULL + NK;       // [NK] the S products that read it are done (both slots)
   static constexpr int VFULL = KFREE + NK;       // [NV]
   static constexpr int VFREE = VFULL + NV;       // [NV] the P.V products that read it are done
   static constexpr int QFULL = VFREE + NV;       // [2] Q of a slot landed
@@ -100,8 +104,8 @@ struct TreeCfg {
   static constexpr int SEGFULL = OFREE + 1;      // [SEGS]
   static constexpr int SEGFREE = SEGFULL + SEGS; // [SEGS] every role is done with it
   static constexpr int SYNC = SEGFREE + SEGS;    // the 8 softmax warps
-  static constexpr int DRAIN = SYNC + 1;         // the MMA warp's last commit
-  static constexpr int QCONV = DRAIN + 1;        // e4m3: Q turned into f16 (8 warps)
+  static constexpr int DRAIN = SYNC + 1;         // [2] an MMA warp's last commit
+  static constexpr int QCONV = DRAIN + 2;        // e4m3: Q turned into f16 (8 warps)
   static constexpr int KRAW = QCONV + 1;         // [NR] e4m3 step landed
   static constexpr int VRAW = KRAW + NR;         // [NR]
   static constexpr int KRAWFREE = VRAW + NR;     // [NR] ... and read by its two warps
@@ -111,7 +115,7 @@ struct TreeCfg {
   static constexpr int SMEM = OFF_MISC + 64;
   static constexpr int CONVERTERS = KV8 ? 4 : 0;    // two warps for K, two for V, half a step each
   static constexpr int THREADS = (12 + CONVERTERS) * 32;
-  static constexpr int SEG_USERS = 10 + CONVERTERS;  // MMA, 8 softmax, V producer
+  static constexpr int SEG_USERS = 11 + CONVERTERS;  // 2 MMA, 8 softmax, V producer
   // Registers of the softmax warps and of the others; their sum is within what a
   // block is launched with (checked before the launch).
   static constexpr int REGS_SOFTMAX = KV8 ? 184 : 200;
@@ -120,7 +124,7 @@ struct TreeCfg {
   static constexpr uint32_t TMEM_COLS = 512;        // S0 0, S1 128, O0 256, O1 256 + D
   static constexpr uint32_t IDESC_S = KV8 ? idesc_f16_f32(BM, BN, 0) : idesc_bf16_f32(BM, BN, 0);
   static constexpr uint32_t IDESC_O = KV8 ? idesc_f16_f32(BM, D, 1) : idesc_bf16_f32(BM, D, 1);
-  static_assert(SMEM <= 227 * 1024 && OFF_BAR % 8 == 0, "shared memory");
+  static_assert(SMEM <= 227 * 1024 && OFF_BAR % 8 == 0 && NK % 2 == 0, "shared memory");
   static_assert(REGS_SUM <= 65536 && REGS_SOFTMAX % 8 == 0 && REGS_OTHER % 8 == 0, "registers");
 };
 
@@ -234,6 +238,25 @@ __device__ __forceinline__ void convert_half(uint32_t raw, uint32_t stage, int b
   }
 }
 
+// The f16 K stages in the order of a CTA's steps: which one a step uses, and how many
+// steps have used it before.  `g`: steps before the segment.
+template <bool ALIAS, int NK>
+struct KStages {
+  int used[2] = {0, 0};  // ALIAS: before the segment
+  __device__ __forceinline__ int stage(int gk, bool two) const { return ALIAS ? (two ? 0 : gk & 1) : gk % NK; }
+  __device__ __forceinline__ int uses(int gk, int g, bool two) const {
+    if constexpr (!ALIAS) return gk / NK;
+    if (two) return used[0] + gk - g;
+    return (gk & 1 ? used[1] : used[0]) + ((gk - g) >> 1);
+  }
+  __device__ __forceinline__ void end_segment(int g, int n, bool two) {
+    if constexpr (ALIAS) {
+      used[0] += two ? n : (n + 1 - (g & 1)) >> 1;
+      used[1] += two ? 0 : (n + (g & 1)) >> 1;
+    }
+  }
+};
+
 template <int N>
 __device__ __forceinline__ void take_registers() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -291,6 +314,9 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
                   k >= C::KRAWFREE))
         count = 2;
       if (k == C::OFREE || k == C::SYNC || k == C::QCONV) count = 8;
+      if ((k >= C::KFREE && k < C::KFREE + C::NK) || (k >= C::VFREE && k < C::VFREE + C::NV) || k == C::QFREE ||
+          k == C::OFULL)
+        count = 2;  // both slots
       if (k >= C::SEGFREE && k < C::SEGFREE + C::SEGS) count = C::SEG_USERS;
       mbar_init(bar(k), count);
     }
@@ -382,7 +408,8 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
       const uint32_t* mask = a.masks + static_cast<size_t>(sg.q0 + sg.node0 + (mine ? node : 0)) * a.words32;
       float m_ref = kLowest, l_run = 0.f;
       bool first = true;
-      for (int k = two ? 0 : b; k < n; k += two ? 1 : 2) {
+      const int k0 = two ? 0 : (g ^ b) & 1;  // this slot's first step
+      for (int k = k0; k < n; k += two ? 1 : 2) {
         const int key0 = (sg.j0 + k) * C::BN;
         if (!(ok = warp_wait(C::SFULL + b, sc++ & 1, 82))) break;
         tc_fence_after();
@@ -451,8 +478,8 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         }
         first = false;
         // V of keys that no row of the unit sees may hold anything: zeros instead, before the
-        // first product that reads the step.
-        if (masked && (b == 0 || !two)) {
+        // slot's product reads the step.  (Two tiles: by each slot, for its own product.)
+        if (masked) {
           uint32_t any[5] = {0, 0, 0, 0, 0};
           const uint32_t* mk = a.masks + static_cast<size_t>(sg.q0 + sg.node0) * a.words32;
           for (int i = lane; i < nodes; i += 32)
@@ -518,8 +545,8 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         for (int c = c0; c < c1; c += 16) {
           float o[16];
           tmem_ld16(tm_o + b * D + c, o);
-          // (slot 1 has no O of its own where the segment is one step long)
-          const bool own_there = two || b == 0 || n > 1, other_there = !two && (b == 1 || n > 1);
+          // (one of the slots has no O where the segment is one step long)
+          const bool own_there = k0 < n, other_there = !two && (k0 ^ 1) < n;
 #pragma unroll
           for (int e = 0; e < 16; ++e) o[e] = own_there ? o[e] * f_own : 0.f;
           if (other_there) {
@@ -736,11 +763,14 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         if (ok && lane == 0) mbar_arrive(bar(C::SEGFREE + slot));
       }
       if (!ok && lane == 0) *fail_flag = 1;
-    } else if (warp == 9) {
-      // ========================================================== MMA issuer
+    } else if (warp == 9 || warp == 11) {
+      // =========================== MMA issue of slot 0 (warp 9) and 1 (warp 11)
+      // A warp each: one thread that issues for both slots is busy longer with its
+      // waits, fences and commits than the tensor core with the products.
       if (lane == 0) {
+        const int b = warp == 9 ? 0 : 1;
         bool ok = true;
-        int g = 0, pc[2] = {0, 0}, qc[2] = {0, 0};
+        int g = 0, pc = 0, qc[2] = {0, 0};
         auto wait = [&](int k, uint32_t parity, int where) -> bool {
           if (*fail_flag) return false;
           if (!mbar_wait(bar(k), parity)) {
@@ -750,34 +780,41 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
           return true;
         };
         // Operand descriptors differ by their start addresses alone, the low word's low
-        // bits: one is built for each operand, offsets are added.  (Built anew for every
-        // product, the issue of the 32 of a step took longer than the tensor core.)
+        // bits: one is built for each operand, offsets are added.
         const uint64_t qd = sdesc_sw128(q_s, 16, 1024);
         const uint64_t kd = sdesc_sw128(k_s, 16, C::GSTRIDE);
+        const uint64_t kd1 = sdesc_sw128(C::ALIAS ? q_s + C::QBYTES : k_s + C::TBYTES, 16, C::GSTRIDE);
+        KStages<C::ALIAS, C::NK> ks_of;
         const uint64_t vd = sdesc_sw128(v_s, 1024, C::GSTRIDE);
-        // S of slot b = Q (buffer qb) K^T of K step gk, into TMEM columns 128 b ..
-        auto issue_s = [&](int b, int qb, int gk) {
-          const uint64_t q0 = qd + qb * (C::QBYTES >> 4), k0 = kd + (gk % C::NK) * (C::TBYTES >> 4);
-          const uint32_t ts = tmem + b * C::BN;
+        const uint32_t ts = tmem + b * C::BN, to = tmem + 256 + b * D;
+        // S = Q (buffer qb) K^T of K step gk, into the slot's columns.  `both`: the
+        // other slot reads the step as well; else this warp frees it for both.
+        auto issue_s = [&](int qb, int gk, bool both) -> bool {
+          const int st = ks_of.stage(gk, both);
+          if (!wait(C::KFULL + st, ks_of.uses(gk, g, both) & 1, 72)) return false;
+          tc_fence_after();
+          const uint64_t q0 = qd + qb * (C::QBYTES >> 4);
+          const uint64_t k0 = C::ALIAS ? (st ? kd1 : kd) : kd + st * (C::TBYTES >> 4);
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks)
             umma_bf16(ts, q0 + (((ks / 4) * C::CHUNK + (ks % 4) * 32) >> 4),
                       k0 + (((ks / 4) * 1024 + (ks % 4) * 32) >> 4), C::IDESC_S, ks > 0);
           umma_commit(bar(C::SFULL + b));
+          umma_commit(bar(C::KFREE + st));
+          if (!both) mbar_arrive(bar(C::KFREE + st));  // (the other slot never reads this stage)
+          return true;
         };
-        // O of slot b += P V of V step gv (P: 16 bits in TMEM columns 128 b ..).
-        auto issue_pv = [&](int b, int gv, bool acc) {
+        // O += P V of V step gv (P: 16 bits in the slot's S columns).
+        auto issue_pv = [&](int gv, bool acc) -> bool {
+          if (!wait(C::VFULL + gv % C::NV, (gv / C::NV) & 1, 73) || !wait(C::PFULL + b, pc++ & 1, 75)) return false;
+          tc_fence_after();
           const uint64_t v0 = vd + (gv % C::NV) * (C::TBYTES >> 4);
-          const uint32_t to = tmem + 256 + b * D, tp = tmem + b * C::BN;
-          umma_tmem_a(to, tp, v0, C::IDESC_O, acc ? 1u : 0u);
+          umma_tmem_a(to, ts, v0, C::IDESC_O, acc ? 1u : 0u);
 #pragma unroll
           for (int ks = 1; ks < C::BN / 16; ++ks)
-            umma_tmem_a(to, tp + ks * 8, v0 + ((ks * C::BLOCK_BYTES) >> 4), C::IDESC_O, 1u);
-        };
-        auto k_landed = [&](int gk) -> bool {
-          const bool good = wait(C::KFULL + gk % C::NK, (gk / C::NK) & 1, 72);
-          tc_fence_after();
-          return good;
+            umma_tmem_a(to, ts + ks * 8, v0 + ((ks * C::BLOCK_BYTES) >> 4), C::IDESC_O, 1u);
+          umma_commit(bar(C::VFREE + gv % C::NV));
+          return true;
         };
         for (int seg = 0; ok; ++seg) {
           const int slot = seg % C::SEGS;
@@ -786,109 +823,97 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
           if (sg.kind == kEnd) break;
           const int n = sg.j1 - sg.j0;
           const bool two = sg.nodes > NPS;
-          if constexpr (KV8) {
-            ok = wait(C::QCONV, seg & 1, 71);
-          } else {
-            for (int b = 0; b < (two ? 2 : 1) && ok; ++b) ok = wait(C::QFULL + b, qc[b]++ & 1, 71);
-          }
+          // Two tiles: both slots take every step; one: those of their parity (of the
+          // CTA's step count g + k, so that a K stage always has the same owner).  Both
+          // slots wait for and free every V step, in order: a barrier's parity names a
+          // phase only to who has seen the one before.  A slot without a step still waits
+          // for the segment's Q and the end of the one before, so that its arrivals
+          // count for this one.
+          const int k0 = two ? 0 : (g ^ b) & 1, dk = two ? 1 : 2;
+          const int qb = two ? b : 0;
+          ok = KV8 ? wait(C::QCONV, seg & 1, 71) : wait(C::QFULL + qb, qc[qb] & 1, 71);
+          ++qc[0];
+          if (two) ++qc[1];
           if (!ok) break;
-          // Step k of slot b: (two tiles) both slots take every step, or (one tile) they
-          // take steps in turn.
-          if (two) {
-            if (!(ok = k_landed(g))) break;
-            issue_s(0, 0, g);
-            issue_s(1, 1, g);
-            umma_commit(bar(C::KFREE + g % C::NK));
-            if (n == 1) umma_commit(bar(C::QFREE));
-          } else {
-            for (int k = 0; k < min(n, 2) && ok; ++k) {
-              if (!(ok = k_landed(g + k))) break;
-              issue_s(k, 0, g + k);
-              umma_commit(bar(C::KFREE + (g + k) % C::NK));
-            }
-            if (!ok) break;
-            if (n <= 2) umma_commit(bar(C::QFREE));
+          if (k0 < n && !(ok = issue_s(qb, g + k0, two))) break;
+          if (k0 + dk >= n) {  // the last S of the segment
+            if (k0 < n)
+              umma_commit(bar(C::QFREE));
+            else
+              mbar_arrive(bar(C::QFREE));
           }
-          for (int k = 0; k < n && ok; ++k) {
-            const int gk = g + k;
-            if (!(ok = wait(C::VFULL + gk % C::NV, (gk / C::NV) & 1, 73))) break;
-            if (k == 0 && seg > 0 && !(ok = wait(C::OFREE, (seg - 1) & 1, 76))) break;
-            if (two) {
-              for (int b = 0; b < 2 && ok; ++b) {
-                if (!(ok = wait(C::PFULL + b, pc[b]++ & 1, 75))) break;
-                tc_fence_after();
-                issue_pv(b, gk, k > 0);
-                if (k + 1 < n) {
-                  if (b == 0 && !(ok = k_landed(gk + 1))) break;
-                  issue_s(b, b, gk + 1);
-                }
-              }
-              if (!ok) break;
-              umma_commit(bar(C::VFREE + gk % C::NV));
-              if (k + 1 < n) umma_commit(bar(C::KFREE + (gk + 1) % C::NK));
-              if (k + 2 == n) umma_commit(bar(C::QFREE));
-            } else {
-              const int b = k & 1;
-              if (!(ok = wait(C::PFULL + b, pc[b]++ & 1, 75))) break;
-              tc_fence_after();
-              issue_pv(b, gk, k > 1);
-              umma_commit(bar(C::VFREE + gk % C::NV));
-              if (k + 2 < n) {
-                if (!(ok = k_landed(gk + 2))) break;
-                issue_s(b, 0, gk + 2);
-                umma_commit(bar(C::KFREE + (gk + 2) % C::NK));
-                if (k + 3 == n) umma_commit(bar(C::QFREE));
-              }
+          if (seg > 0 && !(ok = wait(C::OFREE, (seg - 1) & 1, 76))) break;
+          for (int k = 0; k < n; ++k) {
+            if (!two && ((k ^ k0) & 1)) {
+              if (!(ok = wait(C::VFULL + (g + k) % C::NV, ((g + k) / C::NV) & 1, 74))) break;
+              mbar_arrive(bar(C::VFREE + (g + k) % C::NV));
+              continue;
+            }
+            if (!(ok = issue_pv(g + k, k > k0))) break;
+            if (k + dk < n) {
+              if (!(ok = issue_s(qb, g + k + dk, two))) break;
+              if (k + 2 * dk >= n) umma_commit(bar(C::QFREE));
             }
           }
           if (!ok) break;
-          umma_commit(bar(C::OFULL));
+          if (k0 < n)
+            umma_commit(bar(C::OFULL));
+          else
+            mbar_arrive(bar(C::OFULL));
+          ks_of.end_segment(g, n, two);
           g += n;
           mbar_arrive(bar(C::SEGFREE + slot));
         }
         if (!ok) *fail_flag = 1;
         // Every MMA issued has completed before TMEM can be released.
-        umma_commit(bar(C::DRAIN));
-        (void)mbar_wait(bar(C::DRAIN), 0);
+        umma_commit(bar(C::DRAIN + b));
+        (void)mbar_wait(bar(C::DRAIN + b), 0);
       }
       __syncwarp();
-    } else if (warp >= 11) {
+    } else if (warp >= 12) {
       // =================================================== e4m3 -> f16 (KV8)
       if constexpr (KV8) {
-        if (warp >= 12) {
-          const bool is_v = warp >= 14;
-          const int half = warp & 1;
-          const int NS = is_v ? C::NV : C::NK;
-          const int raw = is_v ? C::VRAW : C::KRAW, raw_free = is_v ? C::VRAWFREE : C::KRAWFREE;
-          const int full = is_v ? C::VFULL : C::KFULL, free = is_v ? C::VFREE : C::KFREE;
-          const uint32_t base = is_v ? v_s : k_s;
-          const uint32_t raw_base = sbase + (is_v ? C::OFF_VRAW : C::OFF_KRAW);
-          bool ok = true;
-          int g = 0;
-          for (int seg = 0; ok; ++seg) {
-            const int slot = seg % C::SEGS;
-            if (!(ok = warp_wait(C::SEGFULL + slot, (seg / C::SEGS) & 1, 68))) break;
-            const TreeSeg sg = segs[slot];
-            if (sg.kind == kEnd) break;
-            const int nblk = (sg.ctx + sg.n_new + kBlockSize - 1) / kBlockSize;
-            for (int jj = sg.j0; jj < sg.j1; ++jj, ++g) {
-              const int rs = g % C::NR, stg = g % NS;
-              if (!(ok = warp_wait(raw + rs, (g / C::NR) & 1, is_v ? 66 : 65))) break;
-              if (g >= NS && !(ok = warp_wait(free + stg, ((g / NS) - 1) & 1, 69))) break;
-              convert_half<D, KV8>(raw_base + rs * C::RAW_BYTES, base + stg * C::TBYTES, 4 * half,
-                                   min(4 * half + 4, nblk - jj * 8), lane);
-              fence_proxy_async_smem();  // the f16 step is read by the tensor core, the raw one overwritten by a copy
-              __syncwarp();
-              if (lane == 0) {
-                mbar_arrive(bar(full + stg));
-                mbar_arrive(bar(raw_free + rs));
-              }
-            }
+        const bool is_v = warp >= 14;
+        const int half = warp & 1;
+        const int raw = is_v ? C::VRAW : C::KRAW, raw_free = is_v ? C::VRAWFREE : C::KRAWFREE;
+        const int full = is_v ? C::VFULL : C::KFULL, free = is_v ? C::VFREE : C::KFREE;
+        const uint32_t raw_base = sbase + (is_v ? C::OFF_VRAW : C::OFF_KRAW);
+        KStages<C::ALIAS, C::NK> ks_of;
+        bool ok = true, was_two = false;
+        int g = 0;
+        for (int seg = 0; ok; ++seg) {
+          const int slot = seg % C::SEGS;
+          if (!(ok = warp_wait(C::SEGFULL + slot, (seg / C::SEGS) & 1, 68))) break;
+          const TreeSeg sg = segs[slot];
+          if (sg.kind == kEnd) break;
+          const int nblk = (sg.ctx + sg.n_new + kBlockSize - 1) / kBlockSize, n = sg.j1 - sg.j0;
+          const bool two = sg.nodes > NPS;
+          // Slot 1's Q buffer becomes a K stage: its last reader is done first.
+          if (C::ALIAS && !is_v && was_two && !two && !(ok = warp_wait(C::QFREE, (seg - 1) & 1, 78))) break;
+          for (int k = 0; k < n; ++k) {
+            const int gk = g + k, rs = gk % C::NR;
+            const int st = is_v ? gk % C::NV : ks_of.stage(gk, two);
+            const int uses = is_v ? gk / C::NV : ks_of.uses(gk, g, two);
+            const uint32_t dst = is_v ? v_s + st * C::TBYTES
+                                      : (C::ALIAS && st ? q_s + C::QBYTES : k_s + st * C::TBYTES);
+            if (!(ok = warp_wait(raw + rs, (gk / C::NR) & 1, is_v ? 66 : 65))) break;
+            if (uses > 0 && !(ok = warp_wait(free + st, (uses - 1) & 1, 69))) break;
+            convert_half<D, KV8>(raw_base + rs * C::RAW_BYTES, dst, 4 * half,
+                                 min(4 * half + 4, nblk - (sg.j0 + k) * 8), lane);
+            fence_proxy_async_smem();  // the f16 step is read by the tensor core, the raw one overwritten by a copy
             __syncwarp();
-            if (ok && lane == 0) mbar_arrive(bar(C::SEGFREE + slot));
+            if (lane == 0) {
+              mbar_arrive(bar(full + st));
+              mbar_arrive(bar(raw_free + rs));
+            }
           }
-          if (!ok && lane == 0) *fail_flag = 1;
+          ks_of.end_segment(g, n, two);
+          g += n;
+          was_two = two;
+          __syncwarp();
+          if (ok && lane == 0) mbar_arrive(bar(C::SEGFREE + slot));
         }
+        if (!ok && lane == 0) *fail_flag = 1;
       }
     }
   }
