@@ -106,7 +106,8 @@ struct TreeCfg {
   static constexpr int SYNC = SEGFREE + SEGS;    // the 8 softmax warps
   static constexpr int DRAIN = SYNC + 1;         // [2] an MMA warp's last commit
   static constexpr int QCONV = DRAIN + 2;        // e4m3: Q turned into f16 (8 warps)
-  static constexpr int KRAW = QCONV + 1;         // [NR] e4m3 step landed
+  static constexpr int TURN = QCONV + 1;         // [2] a slot's turn to issue (two tiles)
+  static constexpr int KRAW = TURN + 2;          // [NR] e4m3 step landed
   static constexpr int VRAW = KRAW + NR;         // [NR]
   static constexpr int KRAWFREE = VRAW + NR;     // [NR] ... and read by its two warps
   static constexpr int VRAWFREE = KRAWFREE + NR; // [NR]
@@ -171,6 +172,10 @@ __device__ __forceinline__ long long warp_sum64(long long v) {
   return v;
 }
 
+__device__ __forceinline__ void prefetch_l1(const void* p) {
+  asm volatile("prefetch.global.L1 [%0];" ::"l"(p));
+}
+
 // Holds the registers of an asynchronous TMEM load until its wait.
 template <int N>
 __device__ __forceinline__ void pin(uint32_t (&r)[N]) {
@@ -228,12 +233,14 @@ __device__ __forceinline__ void convert_half(uint32_t raw, uint32_t stage, int b
         if (g8 + g >= 2 * b1) continue;
         const int r = lane / CPR + KPI * k;
         const uint32_t row = stage + (g8 + g) * C::GSTRIDE + half + r * 128;
-        const uint4 lo = make_uint4(e4m3x2_to_f16x2(w[g][k].x), e4m3x2_to_f16x2(w[g][k].x >> 16),
-                                    e4m3x2_to_f16x2(w[g][k].y), e4m3x2_to_f16x2(w[g][k].y >> 16));
-        const uint4 hi = make_uint4(e4m3x2_to_f16x2(w[g][k].z), e4m3x2_to_f16x2(w[g][k].z >> 16),
-                                    e4m3x2_to_f16x2(w[g][k].w), e4m3x2_to_f16x2(w[g][k].w >> 16));
-        st_shared_v4(row + (((cc + swap) ^ r) * 16), swap ? hi : lo);
-        st_shared_v4(row + (((cc + 1 - swap) ^ r) * 16), swap ? lo : hi);
+        const uint4 x = w[g][k];
+        const uint32_t a0 = swap ? x.z : x.x, a1 = swap ? x.w : x.y, b0w = swap ? x.x : x.z, b1w = swap ? x.y : x.w;
+        st_shared_v4(row + (((cc + swap) ^ r) * 16),
+                     make_uint4(e4m3x2_to_f16x2(a0), e4m3x2_to_f16x2(a0 >> 16), e4m3x2_to_f16x2(a1),
+                                e4m3x2_to_f16x2(a1 >> 16)));
+        st_shared_v4(row + (((cc + 1 - swap) ^ r) * 16),
+                     make_uint4(e4m3x2_to_f16x2(b0w), e4m3x2_to_f16x2(b0w >> 16), e4m3x2_to_f16x2(b1w),
+                                e4m3x2_to_f16x2(b1w >> 16)));
       }
   }
 }
@@ -400,12 +407,10 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(C::QCONV));
       }
-      const int node_b = two && b ? NPS : 0;                           // first node of this slot in the unit
-      const int rows = (two ? (b ? nodes - NPS : NPS) : nodes) * G;    // rows of this slot
-      const bool mine = i_row < rows;
-      const bool live = (warp & 3) * 32 < rows;                        // some row of this warp
-      const int node = node_b + i_row / G;                             // in the unit
-      const uint32_t* mask = a.masks + static_cast<size_t>(sg.q0 + sg.node0 + (mine ? node : 0)) * a.words32;
+      // Rows of this slot; whether this warp has some.
+      const bool live = (warp & 3) * 32 < (two ? (b ? nodes - NPS : NPS) : nodes) * G;
+      for (int i = lane; i < nodes; i += 32)  // read in the last steps
+        prefetch_l1(a.masks + static_cast<size_t>(sg.q0 + sg.node0 + i) * a.words32);
       float m_ref = kLowest, l_run = 0.f;
       bool first = true;
       const int k0 = two ? 0 : (g ^ b) & 1;  // this slot's first step
@@ -419,6 +424,9 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         if (live) {
           uint32_t seen[4];
           if (masked) {
+            // (rows behind the slot's last take the unit's last node)
+            const int node = min((two && b ? NPS : 0) + i_row / G, nodes - 1);
+            const uint32_t* mask = a.masks + static_cast<size_t>(sg.q0 + sg.node0 + node) * a.words32;
             uint32_t w[5];
 #pragma unroll
             for (int i = 0; i < 5; ++i) w[i] = view_word(mask, a.words32, n_new, w0 + i);
@@ -512,11 +520,14 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
       // ---- the segment's end
       if (!(ok = warp_wait(C::OFULL, seg & 1, 84))) break;
       tc_fence_after();
-      const int kind = sg.kind;
-      const int kvh = sg.kvh;
+      // (What the loop needed of the record is read again here: registers.)
+      const int kind = sg.kind, e_nodes = sg.nodes, e_n = sg.j1 - sg.j0;
+      const bool e_two = e_nodes > NPS;
+      const bool has_own = !first;                          // this slot took a step
+      const bool has_other = !e_two && (e_n > 1 || first);  // ... and the other one, of the same rows
       // One tile: (m, l) of the two halves of its keys, joined.
-      float w_own = 1.f, w_other = 0.f;
-      if (!two) {
+      float w_other = 0.f, w_own = 1.f;
+      if (!e_two) {
         xch[b * 128 + i_row] = make_float2(m_ref, l_run);
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(C::SYNC));
@@ -528,44 +539,48 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         m_ref = m;
         l_run = l_run * w_own + other.y * w_other;
       }
-      if (live) {
-        const float inv = kind != kWhole ? 1.f : (l_run > 0.f ? a.o_scale / l_run : 0.f);
-        const int out_slot = two ? b : 0;
-        const size_t rec = record_of(cta, kind == kTail ? 1 : 0, out_slot);
+      const int e_rows = (e_two ? (b ? e_nodes - NPS : NPS) : e_nodes) * G;
+      if ((warp & 3) * 32 < e_rows) {
+        const bool mine = i_row < e_rows;
+        const size_t rec = record_of(cta, kind == kTail ? 1 : 0, e_two ? b : 0);
         const int i_node = i_row / G;
-        __nv_bfloat16* dst = a.out + (static_cast<size_t>(sg.q0 + sg.node0 + node_b + i_node) * a.num_heads +
-                                      kvh * G + (i_row - i_node * G)) * D;
+        __nv_bfloat16* dst = a.out + (static_cast<size_t>(sg.q0 + sg.node0 + (e_two && b ? NPS : 0) + i_node) * a.num_heads +
+                                      sg.kvh * G + (i_row - i_node * G)) * D;
         float4* part = reinterpret_cast<float4*>(a.part_o + rec * (D * 128)) + i_row;
-        if (kind != kWhole && mine && (two || b == 0))
+        if (kind != kWhole && mine && (e_two || b == 0))
           *reinterpret_cast<float2*>(a.part_ml + (rec * 128 + i_row) * 2) = make_float2(m_ref, l_run);
-        // Two tiles: the slot's columns; one: half the columns each.
-        const int c0 = two ? 0 : b * (D / 2), c1 = two ? D : c0 + D / 2;
+        const float inv = kind != kWhole ? 1.f : (l_run > 0.f ? a.o_scale / l_run : 0.f);
         const float f_own = w_own * inv, f_other = w_other * inv;
+        // Two tiles: the slot's columns; one: half the columns each, of both slots' O.
+        constexpr int E = 32;
+        const int c_first = e_two ? 0 : b * (D / 2);
 #pragma unroll 1
-        for (int c = c0; c < c1; c += 16) {
-          float o[16];
-          tmem_ld16(tm_o + b * D + c, o);
-          // (one of the slots has no O where the segment is one step long)
-          const bool own_there = k0 < n, other_there = !two && (k0 ^ 1) < n;
+        for (int c = c_first; c < (e_two ? D : c_first + D / 2); c += E) {
+          uint32_t o[E];
+          tmem_ld32_async(tm_o + b * D + c, o);
+          uint32_t x[E];
+          if (has_other) tmem_ld32_async(tm_o + (b ^ 1) * D + c, x);
+          tmem_wait_ld();
+          pin(o);
+          if (has_other) pin(x);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = own_there ? o[e] * f_own : 0.f;
-          if (other_there) {
-            float x[16];
-            tmem_ld16(tm_o + (b ^ 1) * D + c, x);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = fmaf(x[e], f_other, o[e]);
+          for (int e = 0; e < E; ++e) {
+            float v = has_own ? __uint_as_float(o[e]) * f_own : 0.f;
+            if (has_other) v = fmaf(__uint_as_float(x[e]), f_other, v);
+            o[e] = __float_as_uint(v);
           }
           if (!mine) continue;
+          auto f = [&](int e) { return __uint_as_float(o[e]); };
           if (kind == kWhole) {
 #pragma unroll
-            for (int e = 0; e < 16; e += 8)
+            for (int e = 0; e < E; e += 8)
               *reinterpret_cast<uint4*>(dst + c + e) =
-                  make_uint4(pack_bf16x2(o[e], o[e + 1]), pack_bf16x2(o[e + 2], o[e + 3]),
-                             pack_bf16x2(o[e + 4], o[e + 5]), pack_bf16x2(o[e + 6], o[e + 7]));
+                  make_uint4(pack_bf16x2(f(e), f(e + 1)), pack_bf16x2(f(e + 2), f(e + 3)),
+                             pack_bf16x2(f(e + 4), f(e + 5)), pack_bf16x2(f(e + 6), f(e + 7)));
           } else {
 #pragma unroll
-            for (int e = 0; e < 16; e += 4)
-              part[((c + e) / 4) * 128] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            for (int e = 0; e < E; e += 4)
+              part[((c + e) / 4) * 128] = make_float4(f(e), f(e + 1), f(e + 2), f(e + 3));
           }
         }
       }
@@ -618,7 +633,7 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
           const TreeReq p = tree_req(a, rc + lane);
           const long long cost = (CS + CT * req_steps(p)) * p.tiles * H;
           long long incl = cost;
-  #pragma unroll
+#pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
             const long long v = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += v;
@@ -685,7 +700,7 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
           if (lane == 0) {
             for (int b = 0; b < nsl; ++b) {
               mbar_arrive_expect_tx(bar(C::QFULL + b), C::HALVES * G * NPS * 128);
-  #pragma unroll
+#pragma unroll
               for (int h = 0; h < C::HALVES; ++h)
                 tma_load_3d(q_s + b * C::QBYTES + h * C::CHUNK, &qmap, bar(C::QFULL + b), 64 * h, kvh * G,
                             p.q0 + node0 + b * NPS, policy);
@@ -770,7 +785,7 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
       if (lane == 0) {
         const int b = warp == 9 ? 0 : 1;
         bool ok = true;
-        int g = 0, pc = 0, qc[2] = {0, 0};
+        int g = 0, pc = 0, qc[2] = {0, 0}, turns = 0;
         auto wait = [&](int k, uint32_t parity, int where) -> bool {
           if (*fail_flag) return false;
           if (!mbar_wait(bar(k), parity)) {
@@ -805,8 +820,9 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
           return true;
         };
         // O += P V of V step gv (P: 16 bits in the slot's S columns).
-        auto issue_pv = [&](int gv, bool acc) -> bool {
+        auto issue_pv = [&](int gv, bool acc, bool in_turn) -> bool {
           if (!wait(C::VFULL + gv % C::NV, (gv / C::NV) & 1, 73) || !wait(C::PFULL + b, pc++ & 1, 75)) return false;
+          if (in_turn && (b == 1 || turns > 0) && !wait(C::TURN + b, (b == 1 ? turns : turns - 1) & 1, 77)) return false;
           tc_fence_after();
           const uint64_t v0 = vd + (gv % C::NV) * (C::TBYTES >> 4);
           umma_tmem_a(to, ts, v0, C::IDESC_O, acc ? 1u : 0u);
@@ -826,7 +842,9 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
           // Two tiles: both slots take every step; one: those of their parity (of the
           // CTA's step count g + k, so that a K stage always has the same owner).  Both
           // slots wait for and free every V step, in order: a barrier's parity names a
-          // phase only to who has seen the one before.  A slot without a step still waits
+          // phase only to who has seen the one before.  With two tiles they issue in turn: at
+          // the same time their products share the tensor core, both softmaxes start
+          // together when they are done, and the core idles meanwhile.  A slot without a step still waits
           // for the segment's Q and the end of the one before, so that its arrivals
           // count for this one.
           const int k0 = two ? 0 : (g ^ b) & 1, dk = two ? 1 : 2;
@@ -849,10 +867,14 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
               mbar_arrive(bar(C::VFREE + (g + k) % C::NV));
               continue;
             }
-            if (!(ok = issue_pv(g + k, k > k0))) break;
+            if (!(ok = issue_pv(g + k, k > k0, two))) break;
             if (k + dk < n) {
               if (!(ok = issue_s(qb, g + k + dk, two))) break;
               if (k + 2 * dk >= n) umma_commit(bar(C::QFREE));
+            }
+            if (two) {
+              mbar_arrive(bar(C::TURN + (b ^ 1)));
+              ++turns;
             }
           }
           if (!ok) break;
