@@ -666,11 +666,12 @@ pa_status tree_attention_impl(void* out, const void* q, const void* key_cache, c
   TreeArgs a;
   a.group = num_heads / num_kv_heads;
   a.slot_nodes = 128 / a.group;
+  a.group_inv = (65536 + a.group - 1) / a.group;
   CUtensorMap qmap, kmap, vmap;
   const int tiles = num_blocks * (block_size / kBlockSize);
   const bool maps_ok =
       make_q_group_map(&qmap, q, total_q, num_heads, head_dim, a.group, a.slot_nodes) &&
-      (kv8 ? make_cache_map_e4m3(&kmap, key_cache, tiles, num_kv_heads, head_dim, true) &&
+      (kv8 ? make_cache_map_e4m3(&kmap, key_cache, tiles, num_kv_heads, head_dim) &&
                  make_cache_map_e4m3(&vmap, value_cache, tiles, num_kv_heads, head_dim, true)
            : make_kv_group_map(&kmap, key_cache, tiles, num_kv_heads, head_dim) &&
                  make_kv_group_map(&vmap, value_cache, tiles, num_kv_heads, head_dim));

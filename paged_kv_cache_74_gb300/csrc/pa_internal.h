@@ -323,6 +323,7 @@ struct TreeArgs {
   float* part_o;                    // [num_ctas][2][2][D / 4][128][4]  unnormalised O
   int words32, max_blocks_per_seq, num_seqs, num_heads, num_kv_heads, group;
   int slot_nodes;                   // nodes of a 128-row tile: 128 / group
+  int group_inv;                    // ceil(2^16 / group): row / group = row * group_inv >> 16 for 128 rows
   int max_seq_len, max_query_len, num_blocks, block_size, tile_shift, total_q, num_ctas;
   float scale_log2, o_scale;        // as PrefillArgs
 };

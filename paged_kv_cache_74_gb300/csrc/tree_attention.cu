@@ -47,7 +47,7 @@ namespace {
 constexpr float kLowest = -1e30f;     // finite stand-in for -inf in running maxima
 constexpr float kRescaleSlack = 8.0f;  // log2 units: the reference of a row moves lazily
 constexpr long long kStepCost = 4;
-constexpr long long kUnitCost = 10;
+constexpr long long kUnitCost = 16;
 
 // How a segment's result is written.
 constexpr int kWhole = 0;  // the whole unit: bf16 output
@@ -71,29 +71,28 @@ struct TreeCfg {
   // 16-token blocks land as [8-key group][head_dim half][8 keys][128 B].
   static constexpr int GSTRIDE = HALVES * 1024;
   // A V stage is held from its copy to the end of its step, a K stage only to S.
-  // e4m3: landed bytes have stages of their own, free again once converted.
-  // NK is even (see the MMA issue).
-  static constexpr int NK = KV8 ? 2 : (D == 128 ? 2 : 4);
-  static constexpr int NV = KV8 ? (D == 128 ? 2 : 3) : (D == 128 ? 3 : 6);
-  // e4m3 at head_dim 128: one K stage has room of its own; the other is slot 1's Q
-  // buffer, which a unit of one tile does not need (two tiles: one stage).
-  static constexpr bool ALIAS = KV8 && D == 128;
-  static constexpr int NR = KV8 ? (D == 128 ? 2 : 4) : 0;  // raw K stages = raw V stages
+  // e4m3: K lands as the operand; landed V bytes have stages of their own, free again
+  // once converted.  NK is even (see the MMA issue).
+  static constexpr int NK = KV8 ? (D == 128 ? 4 : 6) : (D == 128 ? 2 : 4);
+  static constexpr int NV = KV8 ? (D == 128 ? 2 : 4) : (D == 128 ? 3 : 6);
+  static constexpr int NR = KV8 ? (D == 128 ? 2 : 4) : 0;  // raw V stages
   static constexpr int RAW_BLOCK = 16 * D;
   static constexpr int RAW_BYTES = 128 * D;
+  static constexpr int KBYTES = KV8 ? RAW_BYTES : TBYTES;
+  static constexpr int K_BLOCK = KV8 ? RAW_BLOCK : BLOCK_BYTES;
   static constexpr int SEGS = 4;                    // segment records in flight
   static constexpr int OFF_Q = 0;                   // [2 slots]
   static constexpr int OFF_K = 2 * QBYTES;
-  static constexpr int OFF_V = OFF_K + (ALIAS ? 1 : NK) * TBYTES;
-  static constexpr int OFF_KRAW = OFF_V + NV * TBYTES;
-  static constexpr int OFF_VRAW = OFF_KRAW + NR * RAW_BYTES;
+  static constexpr int OFF_V = OFF_K + NK * KBYTES;
+  static constexpr int OFF_VRAW = OFF_V + NV * TBYTES;
   static constexpr int OFF_SEG = OFF_VRAW + NR * RAW_BYTES;
   static constexpr int OFF_XCH = OFF_SEG + SEGS * 64;   // [2 slots][128 rows] (m, l)
-  static constexpr int OFF_BAR = OFF_XCH + 2 * 128 * 8;
+  static constexpr int OFF_EXP = OFF_XCH + 2 * 128 * 8;  // e4m3: [2 slots][128 rows] exponents of q
+  static constexpr int OFF_BAR = OFF_EXP + (KV8 ? 2 * 128 : 0);
   // Barriers
-  static constexpr int KFULL = 0;                // [NK] K step landed (e4m3: converted)
+  static constexpr int KFULL = 0;                // [NK] K step landed
   static constexpr int KFREE = KFULL + NK;       // [NK] the S products that read it are done (both slots)
-  static constexpr int VFULL = KFREE + NK;       // [NV]
+  static constexpr int VFULL = KFREE + NK;       // [NV] V step landed (e4m3: converted)
   static constexpr int VFREE = VFULL + NV;       // [NV] the P.V products that read it are done
   static constexpr int QFULL = VFREE + NV;       // [2] Q of a slot landed
   static constexpr int QFREE = QFULL + 2;        // the last S product of a segment is done
@@ -105,16 +104,15 @@ struct TreeCfg {
   static constexpr int SEGFREE = SEGFULL + SEGS; // [SEGS] every role is done with it
   static constexpr int SYNC = SEGFREE + SEGS;    // the 8 softmax warps
   static constexpr int DRAIN = SYNC + 1;         // [2] an MMA warp's last commit
-  static constexpr int QCONV = DRAIN + 2;        // e4m3: Q turned into f16 (8 warps)
-  static constexpr int TURN = QCONV + 1;         // [2] a slot's turn to issue (two tiles)
-  static constexpr int KRAW = TURN + 2;          // [NR] e4m3 step landed
-  static constexpr int VRAW = KRAW + NR;         // [NR]
-  static constexpr int KRAWFREE = VRAW + NR;     // [NR] ... and read by its two warps
-  static constexpr int VRAWFREE = KRAWFREE + NR; // [NR]
+  static constexpr int TURN = DRAIN + 2;         // [2] a slot's turn to issue (two tiles)
+  static constexpr int QCONV = TURN + 2;         // e4m3: Q split (4 warps)
+  static constexpr int EXPFREE = QCONV + 1;      // e4m3: the rows' exponents read (8 warps)
+  static constexpr int VRAW = EXPFREE + 1;       // [NR] e4m3 step landed
+  static constexpr int VRAWFREE = VRAW + NR;     // [NR] ... and read by the four warps
   static constexpr int NBAR = VRAWFREE + NR;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int SMEM = OFF_MISC + 64;
-  static constexpr int CONVERTERS = KV8 ? 4 : 0;    // two warps for K, two for V, half a step each
+  static constexpr int CONVERTERS = KV8 ? 4 : 0;    // a quarter of a V step each
   static constexpr int THREADS = (12 + CONVERTERS) * 32;
   static constexpr int SEG_USERS = 11 + CONVERTERS;  // 2 MMA, 8 softmax, V producer
   // Registers of the softmax warps and of the others; their sum is within what a
@@ -123,6 +121,7 @@ struct TreeCfg {
   static constexpr int REGS_OTHER = KV8 ? 72 : 96;
   static constexpr int REGS_SUM = 256 * REGS_SOFTMAX + (THREADS - 256) * REGS_OTHER;
   static constexpr uint32_t TMEM_COLS = 512;        // S0 0, S1 128, O0 256, O1 256 + D
+  // (The descriptor bits of e4m3 in kind::f8f6f4 are those of f16 in kind::f16.)
   static constexpr uint32_t IDESC_S = KV8 ? idesc_f16_f32(BM, BN, 0) : idesc_bf16_f32(BM, BN, 0);
   static constexpr uint32_t IDESC_O = KV8 ? idesc_f16_f32(BM, D, 1) : idesc_bf16_f32(BM, D, 1);
   static_assert(SMEM <= 227 * 1024 && OFF_BAR % 8 == 0 && NK % 2 == 0, "shared memory");
@@ -176,6 +175,18 @@ __device__ __forceinline__ void prefetch_l1(const void* p) {
   asm volatile("prefetch.global.L1 [%0];" ::"l"(p));
 }
 
+// Whether a barrier's phase is over, without waiting.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
 // Holds the registers of an asynchronous TMEM load until its wait.
 template <int N>
 __device__ __forceinline__ void pin(uint32_t (&r)[N]) {
@@ -203,14 +214,14 @@ __device__ __forceinline__ uint32_t view_word(const uint32_t* mask, int words32,
   return __ldg(mask + i) & (left >= 32 ? 0xffffffffu : (1u << left) - 1u);
 }
 
-// Half of an e4m3 step (16-token blocks [b0, b1) of head_dim bytes a token at `raw`)
-// written as f16, exactly, in the operand layout of the bf16 copies ([8-key
+// A part of an e4m3 V step (16-token blocks [b0, b1) of head_dim bytes a token at
+// `raw`) written as f16, exactly, in the operand layout of the bf16 copies ([8-key
 // group][head_dim half][8 keys][128 B], 128-byte swizzle).  Run by one warp, four
 // 8-key groups of loads in flight.  A raw 16-byte chunk becomes two f16 chunks; lanes
 // of the upper head_dim half store them in the other order, so that the eight lanes
 // of a key hit eight bank groups.
 template <int D, bool KV8>
-__device__ __forceinline__ void convert_half(uint32_t raw, uint32_t stage, int b0, int b1, int lane) {
+__device__ __forceinline__ void convert_v(uint32_t raw, uint32_t stage, int b0, int b1, int lane) {
   using C = TreeCfg<D, KV8>;
   constexpr int CPR = D / 16;     // 16-byte raw chunks per key row
   constexpr int KPI = 32 / CPR;   // key rows per warp-wide load
@@ -245,24 +256,84 @@ __device__ __forceinline__ void convert_half(uint32_t raw, uint32_t stage, int b
   }
 }
 
-// The f16 K stages in the order of a CTA's steps: which one a step uses, and how many
-// steps have used it before.  `g`: steps before the segment.
-template <bool ALIAS, int NK>
-struct KStages {
-  int used[2] = {0, 0};  // ALIAS: before the segment
-  __device__ __forceinline__ int stage(int gk, bool two) const { return ALIAS ? (two ? 0 : gk & 1) : gk % NK; }
-  __device__ __forceinline__ int uses(int gk, int g, bool two) const {
-    if constexpr (!ALIAS) return gk / NK;
-    if (two) return used[0] + gk - g;
-    return (gk & 1 ? used[1] : used[0]) + ((gk - g) >> 1);
-  }
-  __device__ __forceinline__ void end_segment(int g, int n, bool two) {
-    if constexpr (ALIAS) {
-      used[0] += two ? n : (n + 1 - (g & 1)) >> 1;
-      used[1] += two ? 0 : (n + (g & 1)) >> 1;
+// Two floats rounded to e4m3 (nearest even, saturating), packed low / high.
+__device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// q of a slot as two e4m3 operands, q 2^e = h + l with h = e4m3(q 2^e) and l = e4m3(q 2^e - h):
+// bf16 has eight significant bits, h takes four and what it leaves has at most four.  e is
+// the row's own, its largest value lands in [128, 256); so l is exact for all values down to
+// 2^-9 of the row's largest, and off by at most 2^-10 (2^-17 of the largest) below.  S = h K^T
+// + l K^T then takes K as it lies in the cache, at twice the f16 rate each: K is not converted.
+// In place: h takes the place of the rows' first halves, l of the second (head_dim 64:
+// within the row).  Warp w4 of four, a row by four lanes.
+template <int D, bool KV8>
+__device__ __forceinline__ void split_q(uint32_t q, int8_t* exps, int w4, int lane) {
+  using C = TreeCfg<D, KV8>;
+  constexpr int NCH = D / 32;  // 16-byte chunks of a lane
+  const int part = lane >> 3;
+#pragma unroll 1
+  for (int r0 = w4 * 8; r0 < 128; r0 += 32) {
+    const int r = r0 + (lane & 7), sw = lane & 7;
+    const uint32_t row = q + r * 128;
+    uint4 w[NCH];
+    uint32_t m2 = 0;
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) {
+      w[c] = ld_shared_v4(row + (D == 128 ? (part >> 1) * C::CHUNK + ((((part & 1) * 4 + c) ^ sw) * 16) : ((2 * part + c) ^ sw) * 16));
+      m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(w[c].x & 0x7fff7fffu, w[c].y & 0x7fff7fffu),
+                                 __vmaxu2(w[c].z & 0x7fff7fffu, w[c].w & 0x7fff7fffu)));
+    }
+    m2 = max(m2 & 0xffffu, m2 >> 16);
+    m2 = max(m2, __shfl_xor_sync(0xffffffffu, m2, 8));
+    m2 = max(m2, __shfl_xor_sync(0xffffffffu, m2, 16));  // (all of the warp's rows are read)
+    // (Beyond 2^47 a row saturates; rows of zeros and of values below 2^-93 take the last step.)
+    const int e = min(max(134 - static_cast<int>(m2 >> 7), -40), 100);
+    const float s = __int_as_float((e + 127) << 23);
+    if (part == 0) exps[r] = static_cast<int8_t>(e);
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < NCH; c += 2) {
+      uint32_t h[4], l[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 x = w[c + i / 2];
+        const uint32_t p0 = i % 2 ? x.z : x.x, p1 = i % 2 ? x.w : x.y;
+        const float a = bf16_lo(p0) * s, b = bf16_hi(p0) * s, c2 = bf16_lo(p1) * s, d = bf16_hi(p1) * s;
+        const uint32_t h0 = pack_e4m3x2(a, b), h1 = pack_e4m3x2(c2, d);
+        const uint32_t f0 = e4m3x2_to_f16x2(h0), f1 = e4m3x2_to_f16x2(h1);
+        const float2 g0 = __half22float2(*reinterpret_cast<const __half2*>(&f0));
+        const float2 g1 = __half22float2(*reinterpret_cast<const __half2*>(&f1));
+        h[i] = h0 | h1 << 16;
+        l[i] = pack_e4m3x2(a - g0.x, b - g0.y) | pack_e4m3x2(c2 - g1.x, d - g1.y) << 16;
+      }
+      const int at = part * (NCH / 2) + c / 2;  // chunk of the row's e4m3 values
+      st_shared_v4(row + (at ^ sw) * 16, make_uint4(h[0], h[1], h[2], h[3]));
+      st_shared_v4(D == 128 ? row + C::CHUNK + (at ^ sw) * 16 : row + ((4 + at) ^ sw) * 16,
+                   make_uint4(l[0], l[1], l[2], l[3]));
     }
   }
-};
+}
+
+// D (TMEM) = A * B (+ D if accumulate), e4m3 operands in shared memory, 32 of K.
+__device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// sdesc_sw128's neighbour for rows of 64 bytes (64-byte swizzle, groups of eight rows
+// 512 bytes apart).
+__device__ __forceinline__ uint64_t sdesc_sw64(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
+         (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (4ull << 61);
+}
 
 template <int N>
 __device__ __forceinline__ void take_registers() {
@@ -271,6 +342,18 @@ __device__ __forceinline__ void take_registers() {
 template <int N>
 __device__ __forceinline__ void give_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Exchanges half of two 16-byte pieces with lane ^ bit: a 2 x 2 transpose.
+__device__ __forceinline__ void swap_pieces(uint4& x, uint4& y, int bit, int lane) {
+  const bool up = lane & bit;
+  uint32_t* a = &x.x;
+  uint32_t* b = &y.x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? a[i] : b[i], bit);
+    (up ? a[i] : b[i]) = got;
+  }
 }
 
 // Records of a cut unit: (CTA, piece, slot) holds (m, l) of 128 rows and their
@@ -299,6 +382,7 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
   auto bar = [&](int k) -> uint32_t { return bar0 + 8 * k; };
   TreeSeg* segs = reinterpret_cast<TreeSeg*>(smem + C::OFF_SEG);
   float2* xch = reinterpret_cast<float2*>(smem + C::OFF_XCH);
+  int8_t* exps = reinterpret_cast<int8_t*>(smem + C::OFF_EXP);
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC);
   volatile int* fail_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
   volatile int* n_k_issued = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 8);
@@ -317,10 +401,8 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
     for (int k = 0; k < C::NBAR; ++k) {
       int count = 1;
       if (k == C::PFULL || k == C::PFULL + 1) count = 4;
-      if (KV8 && ((k >= C::KFULL && k < C::KFULL + C::NK) || (k >= C::VFULL && k < C::VFULL + C::NV) ||
-                  k >= C::KRAWFREE))
-        count = 2;
-      if (k == C::OFREE || k == C::SYNC || k == C::QCONV) count = 8;
+      if (KV8 && ((k >= C::VFULL && k < C::VFULL + C::NV) || k == C::QCONV || k >= C::VRAWFREE)) count = 4;
+      if (k == C::OFREE || k == C::SYNC || (KV8 && k == C::EXPFREE)) count = 8;
       if ((k >= C::KFREE && k < C::KFREE + C::NK) || (k >= C::VFREE && k < C::VFREE + C::NV) || k == C::QFREE ||
           k == C::OFULL)
         count = 2;  // both slots
@@ -376,12 +458,13 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
     // Warps 0-3 serve slot 0, 4-7 slot 1; warp w owns TMEM lanes 32 (w % 4) .. + 31.
     const int b = warp >> 2;
     const int i_row = (warp & 3) * 32 + lane;
+    auto node_of = [&](int row) -> int { return row * a.group_inv >> 16; };  // row / group
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t tm_s = lane_base + b * C::BN;
     const uint32_t tm_o = lane_base + 256;
-    const float sl2 = a.scale_log2;
+    float sl2 = a.scale_log2;
     bool ok = true;
-    int sc = 0, g = 0, qn[2] = {0, 0};
+    int sc = 0, g = 0;
     uint32_t sync_phase = 0;
     for (int seg = 0; ok; ++seg) {
       const int slot = seg % C::SEGS;
@@ -392,20 +475,11 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
       const int nodes = sg.nodes, ctx = sg.ctx, n_new = sg.n_new;
       const bool two = nodes > NPS;
       if constexpr (KV8) {
-        // Q to f16 in place (same layout), before the segment's first S product.
-        for (int qb = 0; qb < (two ? 2 : 1) && ok; ++qb) {
-          if (!(ok = warp_wait(C::QFULL + qb, qn[qb]++ & 1, 79))) break;
-          const uint32_t qst = q_s + qb * C::QBYTES;
-          for (int i = tid; i < C::QBYTES / 16; i += 256) {
-            const uint4 w = ld_shared_v4(qst + i * 16);
-            st_shared_v4(qst + i * 16, make_uint4(bf16x2_to_f16x2(w.x), bf16x2_to_f16x2(w.y),
-                                                  bf16x2_to_f16x2(w.z), bf16x2_to_f16x2(w.w)));
-          }
-        }
-        if (!ok) break;
-        fence_proxy_async_smem();
+        // The row's scores carry 2^e of its q.
+        if (!(ok = warp_wait(C::QCONV, seg & 1, 79))) break;
+        sl2 = a.scale_log2 * __int_as_float((127 - exps[(two ? b * 128 : 0) + i_row]) << 23);
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(C::QCONV));
+        if (lane == 0) mbar_arrive(bar(C::EXPFREE));
       }
       // Rows of this slot; whether this warp has some.
       const bool live = (warp & 3) * 32 < (two ? (b ? nodes - NPS : NPS) : nodes) * G;
@@ -416,16 +490,17 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
       const int k0 = two ? 0 : (g ^ b) & 1;  // this slot's first step
       for (int k = k0; k < n; k += two ? 1 : 2) {
         const int key0 = (sg.j0 + k) * C::BN;
-        if (!(ok = warp_wait(C::SFULL + b, sc++ & 1, 82))) break;
-        tc_fence_after();
         const bool masked = key0 + C::BN > ctx;  // the step holds nodes, or ends behind the keys
-        const int off = key0 - ctx;
-        const int sh = off & 31, w0 = off >> 5;
-        if (live) {
-          uint32_t seen[4];
-          if (masked) {
+        // Before S is there: what the row sees of the step, and whether some row of the
+        // unit sees the key that this lane looks after.
+        uint32_t seen[4];
+        bool dead = false;
+        if (masked) {
+          const int off = key0 - ctx;
+          const int sh = off & 31, w0 = off >> 5;
+          if (live) {
             // (rows behind the slot's last take the unit's last node)
-            const int node = min((two && b ? NPS : 0) + i_row / G, nodes - 1);
+            const int node = min((two && b ? NPS : 0) + node_of(i_row), nodes - 1);
             const uint32_t* mask = a.masks + static_cast<size_t>(sg.q0 + sg.node0 + node) * a.words32;
             uint32_t w[5];
 #pragma unroll
@@ -433,15 +508,45 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
 #pragma unroll
             for (int i = 0; i < 4; ++i) seen[i] = __funnelshift_r(w[i], w[i + 1], sh);
           }
+          // (two words hold this warp's 32 keys)
+          const uint32_t* mk = a.masks + static_cast<size_t>(sg.q0 + sg.node0) * a.words32;
+          uint32_t lo = 0, hi = 0;
+          for (int i = lane; i < nodes; i += 32) {
+            lo |= view_word(mk + static_cast<size_t>(i) * a.words32, a.words32, n_new, w0 + (warp & 3));
+            hi |= view_word(mk + static_cast<size_t>(i) * a.words32, a.words32, n_new, w0 + (warp & 3) + 1);
+          }
+          lo = __reduce_or_sync(0xffffffffu, lo);
+          hi = __reduce_or_sync(0xffffffffu, hi);
+          dead = !(__funnelshift_r(lo, hi, sh) >> lane & 1u);
+        }
+        if (!(ok = warp_wait(C::SFULL + b, sc++ & 1, 82))) break;
+        tc_fence_after();
+        if (live) {
+          if (masked) {
+            // Scores of unseen keys become -inf in place, 32 columns at a time (a loop of
+            // its own: code that few steps run is fetched anew each time).
+#pragma unroll 1
+            for (int c = 0; c < C::BN; c += 32) {
+              const uint32_t w = seen[0];
+              seen[0] = seen[1];
+              seen[1] = seen[2];
+              seen[2] = seen[3];
+              if (__all_sync(0xffffffffu, w == 0xffffffffu)) continue;
+              uint32_t x[32];
+              tmem_ld32_async(tm_s + c, x);
+              tmem_wait_ld();
+              pin(x);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) x[e] = w >> e & 1u ? x[e] : 0xff800000u;
+              tmem_st32_async(tm_s + c, x);
+            }
+            tmem_wait_st();
+          }
           uint32_t sr[C::BN];
 #pragma unroll
           for (int i = 0; i < C::BN; i += 32) tmem_ld32_async(tm_s + i, sr + i);
           tmem_wait_ld();
           pin(sr);
-          if (masked) {
-#pragma unroll
-            for (int e = 0; e < C::BN; ++e) sr[e] = seen[e / 32] >> (e % 32) & 1u ? sr[e] : 0xff800000u;  // -inf
-          }
           // The row's maximum; the reference moves before any weight.
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -488,24 +593,13 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         // V of keys that no row of the unit sees may hold anything: zeros instead, before the
         // slot's product reads the step.  (Two tiles: by each slot, for its own product.)
         if (masked) {
-          uint32_t any[5] = {0, 0, 0, 0, 0};
-          const uint32_t* mk = a.masks + static_cast<size_t>(sg.q0 + sg.node0) * a.words32;
-          for (int i = lane; i < nodes; i += 32)
-#pragma unroll
-            for (int w = 0; w < 5; ++w) any[w] |= view_word(mk + static_cast<size_t>(i) * a.words32, a.words32, n_new, w0 + w);
-#pragma unroll
-          for (int w = 0; w < 5; ++w) any[w] = __reduce_or_sync(0xffffffffu, any[w]);
           const int stg = (g + k) % C::NV;
           if (!(ok = warp_wait(C::VFULL + stg, ((g + k) / C::NV) & 1, 83))) break;
-          uint32_t lo = any[0], hi = any[1];  // of this warp's 32 keys
-          if ((warp & 3) == 1) lo = any[1], hi = any[2];
-          if ((warp & 3) == 2) lo = any[2], hi = any[3];
-          if ((warp & 3) == 3) lo = any[3], hi = any[4];
-          if (!(__funnelshift_r(lo, hi, sh) >> lane & 1u)) {
+          if (dead) {
 #pragma unroll
-            for (int c = 0; c < C::HALVES * 8; ++c)
+            for (int c = 0; c < C::HALVES * 8; ++c)  // (eight lanes hit eight bank groups)
               st_shared_v4(v_s + stg * C::TBYTES + (i_row >> 4) * C::BLOCK_BYTES + ((i_row >> 3) & 1) * C::GSTRIDE +
-                               (c >> 3) * 1024 + (i_row & 7) * 128 + (c & 7) * 16,
+                               (c >> 3) * 1024 + (i_row & 7) * 128 + ((c ^ i_row) & 7) * 16,
                            make_uint4(0u, 0u, 0u, 0u));
           }
           fence_proxy_async_smem();
@@ -543,9 +637,10 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
       if ((warp & 3) * 32 < e_rows) {
         const bool mine = i_row < e_rows;
         const size_t rec = record_of(cta, kind == kTail ? 1 : 0, e_two ? b : 0);
-        const int i_node = i_row / G;
-        __nv_bfloat16* dst = a.out + (static_cast<size_t>(sg.q0 + sg.node0 + (e_two && b ? NPS : 0) + i_node) * a.num_heads +
-                                      sg.kvh * G + (i_row - i_node * G)) * D;
+        // A quad's lanes take 16 bytes each of one row at a time: whole sectors (kWhole).
+        __nv_bfloat16* dst = a.out + (static_cast<size_t>(sg.q0 + sg.node0 + (e_two && b ? NPS : 0)) * a.num_heads +
+                                      sg.kvh * G) * D + (lane & 3) * 8;
+        const int row0 = i_row & ~3;
         float4* part = reinterpret_cast<float4*>(a.part_o + rec * (D * 128)) + i_row;
         if (kind != kWhole && mine && (e_two || b == 0))
           *reinterpret_cast<float2*>(a.part_ml + (rec * 128 + i_row) * 2) = make_float2(m_ref, l_run);
@@ -569,15 +664,24 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
             if (has_other) v = fmaf(__uint_as_float(x[e]), f_other, v);
             o[e] = __float_as_uint(v);
           }
-          if (!mine) continue;
           auto f = [&](int e) { return __uint_as_float(o[e]); };
           if (kind == kWhole) {
+            uint4 p[4];
 #pragma unroll
             for (int e = 0; e < E; e += 8)
-              *reinterpret_cast<uint4*>(dst + c + e) =
-                  make_uint4(pack_bf16x2(f(e), f(e + 1)), pack_bf16x2(f(e + 2), f(e + 3)),
-                             pack_bf16x2(f(e + 4), f(e + 5)), pack_bf16x2(f(e + 6), f(e + 7)));
-          } else {
+              p[e / 8] = make_uint4(pack_bf16x2(f(e), f(e + 1)), pack_bf16x2(f(e + 2), f(e + 3)),
+                                    pack_bf16x2(f(e + 4), f(e + 5)), pack_bf16x2(f(e + 6), f(e + 7)));
+            swap_pieces(p[0], p[1], 1, lane);
+            swap_pieces(p[2], p[3], 1, lane);
+            swap_pieces(p[0], p[2], 2, lane);
+            swap_pieces(p[1], p[3], 2, lane);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int row = row0 + j, node = node_of(row);
+              if (row < e_rows)
+                *reinterpret_cast<uint4*>(dst + (node * a.num_heads + row - node * G) * D + c) = p[j];
+            }
+          } else if (mine) {
 #pragma unroll
             for (int e = 0; e < E; e += 4)
               part[((c + e) / 4) * 128] = make_float4(f(e), f(e + 1), f(e + 2), f(e + 3));
@@ -711,20 +815,17 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
           const int nblk = (p.len + kBlockSize - 1) / kBlockSize;
           int rowc = tile_rows(r, j0 * 8, nblk, true);
           for (int jj = j0; jj < j1; ++jj) {
-            constexpr int NS = KV8 ? C::NR : C::NK;
-            const int stg = g % NS;
-            if (g >= NS && !(ok = warp_wait((KV8 ? C::KRAWFREE : C::KFREE) + stg, ((g / NS) - 1) & 1, 62))) break;
+            const int stg = g % C::NK;
+            if (g >= C::NK && !(ok = warp_wait(C::KFREE + stg, ((g / C::NK) - 1) & 1, 62))) break;
             const int nb = min(8, nblk - jj * 8);
-            const int full = (KV8 ? C::KRAW : C::KFULL) + stg;
-            if (lane == 0) mbar_arrive_expect_tx(bar(full), nb * (KV8 ? C::RAW_BLOCK : C::BLOCK_BYTES));
+            if (lane == 0) mbar_arrive_expect_tx(bar(C::KFULL + stg), nb * C::K_BLOCK);
             __syncwarp();
             if (lane < nb) {
+              const uint32_t dst = k_s + stg * C::KBYTES + lane * C::K_BLOCK;
               if constexpr (KV8)
-                tma_load_3d(sbase + C::OFF_KRAW + stg * C::RAW_BYTES + lane * C::RAW_BLOCK, &kmap, bar(full), 0, kvh,
-                            rowc, policy);
+                tma_load_3d(dst, &kmap, bar(C::KFULL + stg), 0, kvh, rowc, policy);
               else
-                tma_load_5d(k_s + stg * C::TBYTES + lane * C::BLOCK_BYTES, &kmap, bar(full), 0, 0, 0, rowc / 8, kvh,
-                            policy);
+                tma_load_5d(dst, &kmap, bar(C::KFULL + stg), 0, 0, 0, rowc / 8, kvh, policy);
             }
             ++g;
             if (lane == 0) *n_k_issued = g;
@@ -797,27 +898,42 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         // Operand descriptors differ by their start addresses alone, the low word's low
         // bits: one is built for each operand, offsets are added.
         const uint64_t qd = sdesc_sw128(q_s, 16, 1024);
-        const uint64_t kd = sdesc_sw128(k_s, 16, C::GSTRIDE);
-        const uint64_t kd1 = sdesc_sw128(C::ALIAS ? q_s + C::QBYTES : k_s + C::TBYTES, 16, C::GSTRIDE);
-        KStages<C::ALIAS, C::NK> ks_of;
+        const uint64_t kd = !KV8 ? sdesc_sw128(k_s, 16, C::GSTRIDE)
+                                 : (D == 128 ? sdesc_sw128(k_s, 16, 1024) : sdesc_sw64(k_s, 16, 512));
         const uint64_t vd = sdesc_sw128(v_s, 1024, C::GSTRIDE);
         const uint32_t ts = tmem + b * C::BN, to = tmem + 256 + b * D;
-        // S = Q (buffer qb) K^T of K step gk, into the slot's columns.  `both`: the
-        // other slot reads the step as well; else this warp frees it for both.
-        auto issue_s = [&](int qb, int gk, bool both) -> bool {
-          const int st = ks_of.stage(gk, both);
-          if (!wait(C::KFULL + st, ks_of.uses(gk, g, both) & 1, 72)) return false;
+        // Whether K step gk has landed.
+        auto k_there = [&](int gk) -> bool {
+          return mbar_test(bar(C::KFULL + gk % C::NK), (gk / C::NK) & 1);
+        };
+        auto k_wait = [&](int gk) -> bool {
+          if (!wait(C::KFULL + gk % C::NK, (gk / C::NK) & 1, 72)) return false;
           tc_fence_after();
-          const uint64_t q0 = qd + qb * (C::QBYTES >> 4);
-          const uint64_t k0 = C::ALIAS ? (st ? kd1 : kd) : kd + st * (C::TBYTES >> 4);
-#pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks)
-            umma_bf16(ts, q0 + (((ks / 4) * C::CHUNK + (ks % 4) * 32) >> 4),
-                      k0 + (((ks / 4) * 1024 + (ks % 4) * 32) >> 4), C::IDESC_S, ks > 0);
-          umma_commit(bar(C::SFULL + b));
-          umma_commit(bar(C::KFREE + st));
-          if (!both) mbar_arrive(bar(C::KFREE + st));  // (the other slot never reads this stage)
           return true;
+        };
+        // S = Q (buffer qb) K^T of K step gk, into the slot's columns.  `pass_on`: the other
+        // slot's turn begins early enough that it wakes as the last products are issued.
+        auto issue_s = [&](int qb, int gk, bool pass_on) {
+          const uint64_t q0 = qd + qb * (C::QBYTES >> 4);
+          const uint64_t k0 = kd + (gk % C::NK) * (C::KBYTES >> 4);
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            if constexpr (KV8) {  // q's upper parts, then its lower ones
+              const int part = ks / (D / 32), k32 = ks % (D / 32) * 32;
+              umma_e4m3(ts, q0 + ((part * (D == 128 ? C::CHUNK : 64) + k32) >> 4), k0 + (k32 >> 4), C::IDESC_S, ks > 0);
+            } else {
+              umma_bf16(ts, q0 + (((ks / 4) * C::CHUNK + (ks % 4) * 32) >> 4),
+                        k0 + (((ks / 4) * 1024 + (ks % 4) * 32) >> 4), C::IDESC_S, ks > 0);
+            }
+            if (ks == 1 && pass_on) mbar_arrive(bar(C::TURN + (b ^ 1)));
+          }
+          umma_commit(bar(C::SFULL + b));
+        };
+        // The step's K stage is free when S is done; a step that only this slot takes
+        // is freed for the other one as well.
+        auto free_k = [&](int gk, bool both) {
+          umma_commit(bar(C::KFREE + gk % C::NK));
+          if (!both) mbar_arrive(bar(C::KFREE + gk % C::NK));
         };
         // O += P V of V step gv (P: 16 bits in the slot's S columns).
         auto issue_pv = [&](int gv, bool acc, bool in_turn) -> bool {
@@ -829,7 +945,6 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
 #pragma unroll
           for (int ks = 1; ks < C::BN / 16; ++ks)
             umma_tmem_a(to, ts + ks * 8, v0 + ((ks * C::BLOCK_BYTES) >> 4), C::IDESC_O, 1u);
-          umma_commit(bar(C::VFREE + gv % C::NV));
           return true;
         };
         for (int seg = 0; ok; ++seg) {
@@ -853,7 +968,11 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
           ++qc[0];
           if (two) ++qc[1];
           if (!ok) break;
-          if (k0 < n && !(ok = issue_s(qb, g + k0, two))) break;
+          if (k0 < n) {
+            if (!(ok = k_wait(g + k0))) break;
+            issue_s(qb, g + k0, false);
+            free_k(g + k0, two);
+          }
           if (k0 + dk >= n) {  // the last S of the segment
             if (k0 < n)
               umma_commit(bar(C::QFREE));
@@ -867,22 +986,30 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
               mbar_arrive(bar(C::VFREE + (g + k) % C::NV));
               continue;
             }
-            if (!(ok = issue_pv(g + k, k > k0, two))) break;
-            if (k + dk < n) {
-              if (!(ok = issue_s(qb, g + k + dk, two))) break;
-              if (k + 2 * dk >= n) umma_commit(bar(C::QFREE));
+            // The next step's K usually has landed: known before, S follows P V without a
+            // wait, and all commits come behind both (each takes as long as a product's part).
+            const int gv = g + k;
+            const bool more = k + dk < n;
+            const bool there = more && k_there(gv + dk);
+            if (!(ok = issue_pv(gv, k > k0, two))) break;
+            if (more) {
+              if (!there) {
+                umma_commit(bar(C::VFREE + gv % C::NV));
+                if (!(ok = k_wait(gv + dk))) break;
+              }
+              issue_s(qb, gv + dk, two);
             }
-            if (two) {
-              mbar_arrive(bar(C::TURN + (b ^ 1)));
-              ++turns;
-            }
+            if (two && !more) mbar_arrive(bar(C::TURN + (b ^ 1)));
+            turns += two;
+            if (more) free_k(gv + dk, two);
+            if (there || !more) umma_commit(bar(C::VFREE + gv % C::NV));
+            if (more && k + 2 * dk >= n) umma_commit(bar(C::QFREE));
           }
           if (!ok) break;
           if (k0 < n)
             umma_commit(bar(C::OFULL));
           else
             mbar_arrive(bar(C::OFULL));
-          ks_of.end_segment(g, n, two);
           g += n;
           mbar_arrive(bar(C::SEGFREE + slot));
         }
@@ -893,45 +1020,39 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
       }
       __syncwarp();
     } else if (warp >= 12) {
-      // =================================================== e4m3 -> f16 (KV8)
+      // ============================= e4m3: q split, V to f16 (a quarter of a step each)
       if constexpr (KV8) {
-        const bool is_v = warp >= 14;
-        const int half = warp & 1;
-        const int raw = is_v ? C::VRAW : C::KRAW, raw_free = is_v ? C::VRAWFREE : C::KRAWFREE;
-        const int full = is_v ? C::VFULL : C::KFULL, free = is_v ? C::VFREE : C::KFREE;
-        const uint32_t raw_base = sbase + (is_v ? C::OFF_VRAW : C::OFF_KRAW);
-        KStages<C::ALIAS, C::NK> ks_of;
-        bool ok = true, was_two = false;
-        int g = 0;
+        const int w4 = warp - 12;
+        bool ok = true;
+        int g = 0, qn[2] = {0, 0};
         for (int seg = 0; ok; ++seg) {
           const int slot = seg % C::SEGS;
           if (!(ok = warp_wait(C::SEGFULL + slot, (seg / C::SEGS) & 1, 68))) break;
           const TreeSeg sg = segs[slot];
           if (sg.kind == kEnd) break;
           const int nblk = (sg.ctx + sg.n_new + kBlockSize - 1) / kBlockSize, n = sg.j1 - sg.j0;
-          const bool two = sg.nodes > NPS;
-          // Slot 1's Q buffer becomes a K stage: its last reader is done first.
-          if (C::ALIAS && !is_v && was_two && !two && !(ok = warp_wait(C::QFREE, (seg - 1) & 1, 78))) break;
-          for (int k = 0; k < n; ++k) {
-            const int gk = g + k, rs = gk % C::NR;
-            const int st = is_v ? gk % C::NV : ks_of.stage(gk, two);
-            const int uses = is_v ? gk / C::NV : ks_of.uses(gk, g, two);
-            const uint32_t dst = is_v ? v_s + st * C::TBYTES
-                                      : (C::ALIAS && st ? q_s + C::QBYTES : k_s + st * C::TBYTES);
-            if (!(ok = warp_wait(raw + rs, (gk / C::NR) & 1, is_v ? 66 : 65))) break;
-            if (uses > 0 && !(ok = warp_wait(free + st, (uses - 1) & 1, 69))) break;
-            convert_half<D, KV8>(raw_base + rs * C::RAW_BYTES, dst, 4 * half,
-                                 min(4 * half + 4, nblk - (sg.j0 + k) * 8), lane);
+          const int nsl = sg.nodes > NPS ? 2 : 1;
+          if (seg > 0 && !(ok = warp_wait(C::EXPFREE, (seg - 1) & 1, 78))) break;
+          for (int qb = 0; qb < nsl && ok; ++qb)
+            if ((ok = warp_wait(C::QFULL + qb, qn[qb]++ & 1, 65)))
+              split_q<D, KV8>(q_s + qb * C::QBYTES, exps + qb * 128, w4, lane);
+          if (!ok) break;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(C::QCONV));
+          for (int k = 0; k < n; ++k, ++g) {
+            const int rs = g % C::NR, st = g % C::NV;
+            if (!(ok = warp_wait(C::VRAW + rs, (g / C::NR) & 1, 66))) break;
+            if (g >= C::NV && !(ok = warp_wait(C::VFREE + st, (g / C::NV - 1) & 1, 69))) break;
+            convert_v<D, KV8>(sbase + C::OFF_VRAW + rs * C::RAW_BYTES, v_s + st * C::TBYTES, 2 * w4,
+                              min(2 * w4 + 2, nblk - (sg.j0 + k) * 8), lane);
             fence_proxy_async_smem();  // the f16 step is read by the tensor core, the raw one overwritten by a copy
             __syncwarp();
             if (lane == 0) {
-              mbar_arrive(bar(full + st));
-              mbar_arrive(bar(raw_free + rs));
+              mbar_arrive(bar(C::VFULL + st));
+              mbar_arrive(bar(C::VRAWFREE + rs));
             }
           }
-          ks_of.end_segment(g, n, two);
-          g += n;
-          was_two = two;
           __syncwarp();
           if (ok && lane == 0) mbar_arrive(bar(C::SEGFREE + slot));
         }
@@ -944,9 +1065,9 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
   if (*fail_flag && tid == 0) {
     // Let copies still in flight land before TMEM is released and the CTA leaves (bounded).
     const int nk = *n_k_issued, nv = *n_v_issued;
-    const int kb = KV8 ? C::KRAW : C::KFULL, vb = KV8 ? C::VRAW : C::VFULL;
-    constexpr int SK = KV8 ? C::NR : C::NK, SV = KV8 ? C::NR : C::NV;
-    for (int i = max(0, nk - SK); i < nk; ++i) (void)mbar_wait(bar(kb + i % SK), (i / SK) & 1);
+    const int vb = KV8 ? C::VRAW : C::VFULL;
+    constexpr int SV = KV8 ? C::NR : C::NV;
+    for (int i = max(0, nk - C::NK); i < nk; ++i) (void)mbar_wait(bar(C::KFULL + i % C::NK), (i / C::NK) & 1);
     for (int i = max(0, nv - SV); i < nv; ++i) (void)mbar_wait(bar(vb + i % SV), (i / SV) & 1);
     for (int b = 0; b < 2; ++b)
       if (n_q_issued[b] > 0) (void)mbar_wait(bar(C::QFULL + b), (n_q_issued[b] - 1) & 1);
