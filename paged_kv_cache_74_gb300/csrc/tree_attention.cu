@@ -47,7 +47,7 @@ namespace {
 constexpr float kLowest = -1e30f;     // finite stand-in for -inf in running maxima
 constexpr float kRescaleSlack = 8.0f;  // log2 units: the reference of a row moves lazily
 constexpr long long kStepCost = 4;
-constexpr long long kUnitCost = 16;
+constexpr long long kUnitCost = 12;
 
 // How a segment's result is written.
 constexpr int kWhole = 0;  // the whole unit: bf16 output
@@ -115,17 +115,11 @@ struct TreeCfg {
   static constexpr int CONVERTERS = KV8 ? 4 : 0;    // a quarter of a V step each
   static constexpr int THREADS = (12 + CONVERTERS) * 32;
   static constexpr int SEG_USERS = 11 + CONVERTERS;  // 2 MMA, 8 softmax, V producer
-  // Registers of the softmax warps and of the others; their sum is within what a
-  // block is launched with (checked before the launch).
-  static constexpr int REGS_SOFTMAX = KV8 ? 184 : 200;
-  static constexpr int REGS_OTHER = KV8 ? 72 : 96;
-  static constexpr int REGS_SUM = 256 * REGS_SOFTMAX + (THREADS - 256) * REGS_OTHER;
   static constexpr uint32_t TMEM_COLS = 512;        // S0 0, S1 128, O0 256, O1 256 + D
   // (The descriptor bits of e4m3 in kind::f8f6f4 are those of f16 in kind::f16.)
   static constexpr uint32_t IDESC_S = KV8 ? idesc_f16_f32(BM, BN, 0) : idesc_bf16_f32(BM, BN, 0);
   static constexpr uint32_t IDESC_O = KV8 ? idesc_f16_f32(BM, D, 1) : idesc_bf16_f32(BM, D, 1);
   static_assert(SMEM <= 227 * 1024 && OFF_BAR % 8 == 0 && NK % 2 == 0, "shared memory");
-  static_assert(REGS_SUM <= 65536 && REGS_SOFTMAX % 8 == 0 && REGS_OTHER % 8 == 0, "registers");
 };
 
 // A request's rows, or tiles = 0 where it has none or a length is out of range.
@@ -216,8 +210,8 @@ __device__ __forceinline__ uint32_t view_word(const uint32_t* mask, int words32,
 
 // A part of an e4m3 V step (16-token blocks [b0, b1) of head_dim bytes a token at
 // `raw`) written as f16, exactly, in the operand layout of the bf16 copies ([8-key
-// group][head_dim half][8 keys][128 B], 128-byte swizzle).  Run by one warp, four
-// 8-key groups of loads in flight.  A raw 16-byte chunk becomes two f16 chunks; lanes
+// group][head_dim half][8 keys][128 B], 128-byte swizzle).  Run by one warp, an
+// 8-key group at a time.  A raw 16-byte chunk becomes two f16 chunks; lanes
 // of the upper head_dim half store them in the other order, so that the eight lanes
 // of a key hit eight bank groups.
 template <int D, bool KV8>
@@ -230,29 +224,23 @@ __device__ __forceinline__ void convert_v(uint32_t raw, uint32_t stage, int b0, 
   const uint32_t half = (c / 4) * 1024;
   const int cc = 2 * (c % 4), swap = c / 4;
 #pragma unroll 1
-  for (int g8 = 2 * b0; g8 < 2 * b1; g8 += 4) {
-    uint4 w[4][NLD];
+  for (int g8 = 2 * b0; g8 < 2 * b1; ++g8) {
+    uint4 w[NLD];
 #pragma unroll
-    for (int g = 0; g < 4; ++g)
+    for (int k = 0; k < NLD; ++k) w[k] = ld_shared_v4(raw + (g8 * 8 + lane / CPR + KPI * k) * D + c * 16);
 #pragma unroll
-      for (int k = 0; k < NLD; ++k)  // (an odd last block's second half: the stage's next bytes, unused)
-        if (g8 + g < 2 * b1) w[g][k] = ld_shared_v4(raw + ((g8 + g) * 8 + lane / CPR + KPI * k) * D + c * 16);
-#pragma unroll
-    for (int g = 0; g < 4; ++g)
-#pragma unroll
-      for (int k = 0; k < NLD; ++k) {
-        if (g8 + g >= 2 * b1) continue;
-        const int r = lane / CPR + KPI * k;
-        const uint32_t row = stage + (g8 + g) * C::GSTRIDE + half + r * 128;
-        const uint4 x = w[g][k];
-        const uint32_t a0 = swap ? x.z : x.x, a1 = swap ? x.w : x.y, b0w = swap ? x.x : x.z, b1w = swap ? x.y : x.w;
-        st_shared_v4(row + (((cc + swap) ^ r) * 16),
-                     make_uint4(e4m3x2_to_f16x2(a0), e4m3x2_to_f16x2(a0 >> 16), e4m3x2_to_f16x2(a1),
-                                e4m3x2_to_f16x2(a1 >> 16)));
-        st_shared_v4(row + (((cc + 1 - swap) ^ r) * 16),
-                     make_uint4(e4m3x2_to_f16x2(b0w), e4m3x2_to_f16x2(b0w >> 16), e4m3x2_to_f16x2(b1w),
-                                e4m3x2_to_f16x2(b1w >> 16)));
-      }
+    for (int k = 0; k < NLD; ++k) {
+      const int r = lane / CPR + KPI * k;
+      const uint32_t row = stage + g8 * C::GSTRIDE + half + r * 128;
+      const uint4 x = w[k];
+      const uint32_t a0 = swap ? x.z : x.x, a1 = swap ? x.w : x.y, b0w = swap ? x.x : x.z, b1w = swap ? x.y : x.w;
+      st_shared_v4(row + (((cc + swap) ^ r) * 16),
+                   make_uint4(e4m3x2_to_f16x2(a0), e4m3x2_to_f16x2(a0 >> 16), e4m3x2_to_f16x2(a1),
+                              e4m3x2_to_f16x2(a1 >> 16)));
+      st_shared_v4(row + (((cc + 1 - swap) ^ r) * 16),
+                   make_uint4(e4m3x2_to_f16x2(b0w), e4m3x2_to_f16x2(b0w >> 16), e4m3x2_to_f16x2(b1w),
+                              e4m3x2_to_f16x2(b1w >> 16)));
+    }
   }
 }
 
@@ -333,15 +321,6 @@ __device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t adesc, uint6
 __device__ __forceinline__ uint64_t sdesc_sw64(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
   return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
          (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (4ull << 61);
-}
-
-template <int N>
-__device__ __forceinline__ void take_registers() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void give_registers() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // Exchanges half of two 16-byte pieces with lane ^ bit: a 2 x 2 transpose.
@@ -451,9 +430,7 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
     return id * a.block_size + (t16 & ((1 << a.tile_shift) - 1)) * kBlockSize;
   };
 
-  // (The warps of a warpgroup change their registers together.)
   if (warp < 8) {
-    take_registers<C::REGS_SOFTMAX>();
     // ============================================================ softmax
     // Warps 0-3 serve slot 0, 4-7 slot 1; warp w owns TMEM lanes 32 (w % 4) .. + 31.
     const int b = warp >> 2;
@@ -542,16 +519,25 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
             }
             tmem_wait_st();
           }
-          uint32_t sr[C::BN];
-#pragma unroll
-          for (int i = 0; i < C::BN; i += 32) tmem_ld32_async(tm_s + i, sr + i);
-          tmem_wait_ld();
-          pin(sr);
+          // Two passes over the scores in TMEM, W columns at a time.  The loops' code is what
+          // counts: with all 128 scores of a row in registers and nothing rolled the warps'
+          // code outgrew the instruction caches (e4m3, five roles at once: 206 -> 154 us on a
+          // batch of 96 requests, W = 32; 64: 162.  bf16: 64 is the better one, 102 against 107
+          // us on 32 trees of 64 nodes).
+          constexpr int W = KV8 ? 32 : 64;
           // The row's maximum; the reference moves before any weight.
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+          for (int c = 0; c < C::BN; c += W) {
+            uint32_t sr[W];
 #pragma unroll
-          for (int e = 0; e < C::BN; e += 2)
-            mx[(e / 2) % 4] = fmax3(mx[(e / 2) % 4], __uint_as_float(sr[e]), __uint_as_float(sr[e + 1]));
+            for (int e = 0; e < W; e += 32) tmem_ld32_async(tm_s + c + e, sr + e);
+            tmem_wait_ld();
+            pin(sr);
+#pragma unroll
+            for (int e = 0; e < W; e += 2)
+              mx[(e / 2) % 4] = fmax3(mx[(e / 2) % 4], __uint_as_float(sr[e]), __uint_as_float(sr[e + 1]));
+          }
           const float m_tile = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
           const bool moved = m_tile > m_ref + kRescaleSlack;
           float alpha = 1.f;
@@ -563,23 +549,28 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
           // The weights, 16 bits each, over the scores' columns.
           const float2 sl = make_float2(sl2, sl2), mm = make_float2(-m_ref, -m_ref);
           float2 sum[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+          for (int c = 0; c < C::BN; c += W) {
+            uint32_t sr[W], pk[W / 2];
 #pragma unroll
-          for (int c = 0; c < C::BN; c += 32) {
-            uint32_t pk[16];
+            for (int e = 0; e < W; e += 32) tmem_ld32_async(tm_s + c + e, sr + e);
+            tmem_wait_ld();
+            pin(sr);
 #pragma unroll
-            for (int e = c; e < c + 32; e += 2) {
+            for (int e = 0; e < W; e += 2) {
               const float2 x = __ffma2_rn(make_float2(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])), sl, mm);
               const float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
-              pk[(e - c) / 2] = KV8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+              pk[e / 2] = KV8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
               sum[(e / 2) % 4] = __fadd2_rn(sum[(e / 2) % 4], make_float2(p0, p1));
             }
-            tmem_st16_async(tm_s + c / 2, pk);
+#pragma unroll
+            for (int e = 0; e < W / 2; e += 16) tmem_st16_async(tm_s + c / 2 + e, pk + e);
           }
           const float2 ps = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
           l_run += ps.x + ps.y;
           if (__any_sync(0xffffffffu, moved) && !first) {
             // S of this step is done, so the slot's P V before it is too.
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D / 16; ++c) {
               float ov[16];
               tmem_ld16(tm_o + b * D + c * 16, ov);
@@ -596,7 +587,7 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
           const int stg = (g + k) % C::NV;
           if (!(ok = warp_wait(C::VFULL + stg, ((g + k) / C::NV) & 1, 83))) break;
           if (dead) {
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < C::HALVES * 8; ++c)  // (eight lanes hit eight bank groups)
               st_shared_v4(v_s + stg * C::TBYTES + (i_row >> 4) * C::BLOCK_BYTES + ((i_row >> 3) & 1) * C::GSTRIDE +
                                (c >> 3) * 1024 + (i_row & 7) * 128 + ((c ^ i_row) & 7) * 16,
@@ -697,7 +688,6 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
     }
     if (!ok && lane == 0) *fail_flag = 1;
   } else {
-    give_registers<C::REGS_OTHER>();
     if (warp == 8) {
       // ====================================== range walk, Q and K producer
       if (cta == 0) report_bad_requests(a, lane);
@@ -1143,10 +1133,6 @@ cudaError_t launch_impl(const TreeArgs& a, const CUtensorMap& qmap, const CUtens
     const cudaError_t err =
         cudaFuncSetAttribute(tree_attention_kernel<D, KV8>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (err != cudaSuccess) return err;
-    cudaFuncAttributes fa;
-    if (cudaFuncGetAttributes(&fa, tree_attention_kernel<D, KV8>) != cudaSuccess ||
-        fa.numRegs * C::THREADS < C::REGS_SUM)
-      return cudaErrorInvalidConfiguration;
     attr_set[dev] = true;
   }
   const cudaError_t err = launch_overlapped(tree_attention_kernel<D, KV8>, dim3(a.num_ctas), dim3(C::THREADS), C::SMEM,
