@@ -1071,10 +1071,13 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
 }
 
 // Merges the units that range boundaries cut.  Block (c, b, z): slot b of the unit
-// that CTA c began and did not finish.  A warp takes 8 rows x 16 columns at a time,
-// a thread 4 columns, over the contributors in order.
+// that CTA c began and did not finish.  A warp takes 8 rows x 32 columns, a thread two
+// groups of 4 columns, over the contributors in order, four at a time with all their loads
+// in flight: a unit mostly has two, and what counts is the chain of round trips.
 constexpr int kMergeWarps = 8;
-constexpr int kMergeBlocks = 4;
+constexpr int kMergeBatch = 4;
+template <int D>
+constexpr int merge_blocks() { return 16 * (D / 32) / kMergeWarps; }  // a task a warp
 template <int D>
 __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const TreeArgs a) {
   griddep_launch_dependents();
@@ -1088,38 +1091,52 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const Tree
   if (b == 1 && !two) return;
   const int rows = (two ? (b ? nodes - NPS : NPS) : nodes) * G;
   const int lane = threadIdx.x & 31;
-  constexpr int kCols = D / 16;
-  const int tasks = (rows + 7) / 8 * kCols;
-  for (int t = blockIdx.z * kMergeWarps + (threadIdx.x >> 5); t < tasks; t += kMergeBlocks * kMergeWarps) {
-    const int i = t / kCols * 8 + (lane & 7);
-    const int c4 = t % kCols * 4 + (lane >> 3);  // column group of 4
-    if (i >= rows) continue;
-    auto ml_of = [&](int c) -> float2 {
-      return __ldcg(reinterpret_cast<const float2*>(a.part_ml + (record_of(c, c == c0 ? 1 : 0, b) * 128 + i) * 2));
-    };
-    float m = kLowest;
-#pragma unroll 4
-    for (int c = c0; c <= c1; ++c) m = fmaxf(m, ml_of(c).x);
-    float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int c = c0; c <= c1; ++c) {
-      const float2 ml = ml_of(c);
-      const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part_o + record_of(c, c == c0 ? 1 : 0, b) * (D * 128)) +
-                              c4 * 128 + i);
-      const float w = fast_exp2(ml.x - m);
-      l = fmaf(ml.y, w, l);
-      o.x = fmaf(x.x, w, o.x);
-      o.y = fmaf(x.y, w, o.y);
-      o.z = fmaf(x.z, w, o.z);
-      o.w = fmaf(x.w, w, o.w);
+  const int t = blockIdx.z * kMergeWarps + (threadIdx.x >> 5);
+  const int i = t / (D / 32) * 8 + (lane & 7);
+  const int c4 = t % (D / 32) * 8 + (lane >> 3);  // column groups of 4: this one and the fourth from it
+  if (i >= rows) return;
+  float m = kLowest, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f), o2 = o;
+  auto add = [](float4& s, const float4& x, float w) {
+    s = make_float4(fmaf(x.x, w, s.x), fmaf(x.y, w, s.y), fmaf(x.z, w, s.z), fmaf(x.w, w, s.w));
+  };
+  for (int c = c0; c <= c1; c += kMergeBatch) {
+    float2 ml[kMergeBatch];
+    float4 x[kMergeBatch], x2[kMergeBatch];
+#pragma unroll
+    for (int u = 0; u < kMergeBatch; ++u) {
+      ml[u] = make_float2(kLowest, 0.f);
+      x[u] = x2[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (c + u > c1) continue;
+      const size_t rid = record_of(c + u, c + u == c0 ? 1 : 0, b);
+      const float4* part = reinterpret_cast<const float4*>(a.part_o + rid * (D * 128)) + c4 * 128 + i;
+      ml[u] = __ldcg(reinterpret_cast<const float2*>(a.part_ml + (rid * 128 + i) * 2));
+      x[u] = __ldcg(part);
+      x2[u] = __ldcg(part + 4 * 128);
     }
-    const float inv = l > 0.f ? a.o_scale / l : 0.f;
-    const int node = i / G;
-    __nv_bfloat16* dst = a.out + (static_cast<size_t>(row0 + (two && b ? NPS : 0) + node) * a.num_heads + kvh * G +
-                                  (i - node * G)) * D + c4 * 4;
-    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    float top = m;
+#pragma unroll
+    for (int u = 0; u < kMergeBatch; ++u) top = fmaxf(top, ml[u].x);
+    const float w0 = fast_exp2(m - top);
+    m = top;
+    l *= w0;
+    o = make_float4(o.x * w0, o.y * w0, o.z * w0, o.w * w0);
+    o2 = make_float4(o2.x * w0, o2.y * w0, o2.z * w0, o2.w * w0);
+#pragma unroll
+    for (int u = 0; u < kMergeBatch; ++u) {
+      const float w = fast_exp2(ml[u].x - m);
+      l = fmaf(ml[u].y, w, l);
+      add(o, x[u], w);
+      add(o2, x2[u], w);
+    }
   }
+  const float inv = l > 0.f ? a.o_scale / l : 0.f;
+  const int node = i * a.group_inv >> 16;
+  __nv_bfloat16* dst = a.out + (static_cast<size_t>(row0 + (two && b ? NPS : 0) + node) * a.num_heads + kvh * G +
+                                (i - node * G)) * D + c4 * 4;
+  *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+  *reinterpret_cast<uint2*>(dst + 16) =
+      make_uint2(pack_bf16x2(o2.x * inv, o2.y * inv), pack_bf16x2(o2.z * inv, o2.w * inv));
 }
 
 template <int D, bool KV8>
@@ -1139,7 +1156,7 @@ cudaError_t launch_impl(const TreeArgs& a, const CUtensorMap& qmap, const CUtens
                                             stream, qmap, kmap, vmap, a);
   // Units of one step are never cut.
   if (err != cudaSuccess || a.max_seq_len <= 128) return err;
-  return launch_overlapped(tree_merge_kernel<D>, dim3(a.num_ctas, 2, kMergeBlocks), dim3(kMergeWarps * 32), 0, stream,
+  return launch_overlapped(tree_merge_kernel<D>, dim3(a.num_ctas, 2, merge_blocks<D>()), dim3(kMergeWarps * 32), 0, stream,
                            a);
 }
 
