@@ -33,8 +33,8 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kMaxCluster = 8;
-constexpr int kOffsetsInShared = 8192;  // row offsets bisected in shared memory, 32 KB
-constexpr int kAlone = 4;               // blocks of a request that one thread handles by itself
+constexpr int kInShared = 4096;  // requests whose row offsets and contexts are kept in shared memory, 32 KB
+constexpr int kRows = 4;         // rows of a thread that are in flight together
 
 // Sums over the block of two non-negative values per thread, exclusive prefixes
 // in *ea, *eb, totals in *ta, *tb.  (64 bits: lengths come from device data.)
@@ -104,17 +104,23 @@ __device__ __forceinline__ void exchange(cg::cluster_group& cluster, Exchange* e
   *blocks_all = ba;
 }
 
-// Runs f(r, j, base + j) for entries j = 0 .. n - 1 of each lane's request: a few by
-// the lane itself, more by the whole warp.
+// Runs f(i, j, e) for the entries e = 0 .. total - 1 of the block's kThreads requests, entry
+// j of request i: spread evenly over the threads whatever the requests' counts.
+// `before`: entries of the requests before this thread's; `start`: shared.
 template <typename F>
-__device__ __forceinline__ void for_entries(int r, int n, long long base, int lane, F f) {
-  if (n <= kAlone)
-    for (int j = 0; j < n; ++j) f(r, j, base + j);
-  for (unsigned large = __ballot_sync(0xffffffffu, n > kAlone); large != 0; large &= large - 1) {
-    const int src = __ffs(large) - 1;
-    const int wr = __shfl_sync(0xffffffffu, r, src), wn = __shfl_sync(0xffffffffu, n, src);
-    const long long wb = __shfl_sync(0xffffffffu, base, src);
-    for (int j = lane; j < wn; j += 32) f(wr, j, wb + j);
+__device__ __forceinline__ void for_entries(int before, int total, int* start, F f) {
+  start[threadIdx.x] = before;
+  __syncthreads();
+  for (int e = threadIdx.x; e < total; e += kThreads) {
+    int lo = 0, hi = kThreads;  // the last request that starts at or before e
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (start[mid] <= e)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    f(lo, e - start[lo], e);
   }
 }
 
@@ -153,28 +159,30 @@ __device__ __forceinline__ StepNeed step_need(const PlanStepArgs& a, int r, bool
 __global__ void __launch_bounds__(kThreads) plan_step_kernel(const PlanStepArgs a) {
   __shared__ long long warp_sums[kThreads / 32][2];
   __shared__ Exchange ex;
-  __shared__ int offsets[kOffsetsInShared];
+  __shared__ int start[kThreads], first[kThreads];
+  __shared__ int offsets[kInShared + 1], contexts[kInShared];
   cg::cluster_group cluster = cg::this_cluster();
   griddep_launch_dependents();
   griddep_wait();
   const int rank = static_cast<int>(cluster.block_rank()), ctas = static_cast<int>(cluster.num_blocks());
-  const int tid = threadIdx.x, lane = tid & 31;
+  const int tid = threadIdx.x;
   const int S = a.num_seqs;
   const int per = (S + ctas - 1) / ctas;
   const int r0 = min(S, rank * per), r1 = min(S, r0 + per);
+  const bool one = r1 - r0 <= kThreads;  // (the slice's state is read and summed once)
+  const int count = __ldcg(a.free_count);
 
   // Sums of this CTA's slice.
-  long long rows = 0, blocks = 0, e0, e1;
+  long long rows = 0, blocks = 0, e0, e1, ta, tb;
+  StepNeed s{0, 0, 0, 0, 0, false};
   for (int base = r0; base < r1; base += kThreads) {
     const int r = base + tid;
-    StepNeed s{0, 0, 0, 0, 0, false};
+    s = StepNeed{0, 0, 0, 0, 0, false};
     if (r < r1) s = step_need(a, r, true);
-    long long ta, tb;
     block_scan2(s.rows, s.blocks, warp_sums, &e0, &e1, &ta, &tb);
     rows += ta;
     blocks += tb;
   }
-  const int count = __ldcg(a.free_count);
   long long row, block, all_rows, all_blocks;
   exchange(cluster, &ex, rows, blocks, &row, &block, &all_rows, &all_blocks);
   // All or nothing: a batch that does not fit leaves tables, counts and stack alone.
@@ -189,19 +197,19 @@ __global__ void __launch_bounds__(kThreads) plan_step_kernel(const PlanStepArgs 
   // Tables, offsets and lengths.  (The slices' state has been read.)
   for (int base = r0; base < r1; base += kThreads) {
     const int r = base + tid;
-    StepNeed s{0, 0, 0, 0, 0, false};
-    if (r < r1) s = step_need(a, r, false);
-    long long ta, tb;
-    block_scan2(s.rows, s.blocks, warp_sums, &e0, &e1, &ta, &tb);
+    if (!one) {
+      s = StepNeed{0, 0, 0, 0, 0, false};
+      if (r < r1) s = step_need(a, r, false);
+      block_scan2(s.rows, s.blocks, warp_sums, &e0, &e1, &ta, &tb);
+    }
     const bool go = fits && s.ok;
-    for_entries(r, go ? s.blocks : 0, block + e1, lane, [&](int wr, int j, long long i) {
-      const int id = __ldcg(a.free_blocks + (count - 1 - i));
-      const int h = __ldcg(a.held_blocks + wr);
+    first[tid] = s.held;
+    for_entries(static_cast<int>(fits ? e1 : 0), static_cast<int>(fits ? tb : 0), start, [&](int i, int j, int e) {
+      const int id = __ldcg(a.free_blocks + (count - 1 - (static_cast<int>(block) + e)));
       if (static_cast<unsigned>(id) >= static_cast<unsigned>(a.num_blocks))
-        record_error(a.status, PA_DEV_BAD_BLOCK_ID, wr, id);
-      a.block_tables[static_cast<size_t>(wr) * a.max_blocks_per_seq + h + j] = id;
+        record_error(a.status, PA_DEV_BAD_BLOCK_ID, base + i, id);
+      a.block_tables[static_cast<size_t>(base + i) * a.max_blocks_per_seq + first[i] + j] = id;
     });
-    __syncwarp();  // the warp has read its requests' held counts
     if (r < r1) {
       a.query_start_loc[r] = static_cast<int>(min(row + e0, 0x7fffffffll));
       a.seq_lens[r] = go ? s.len : 0;
@@ -211,25 +219,37 @@ __global__ void __launch_bounds__(kThreads) plan_step_kernel(const PlanStepArgs 
     block += tb;
   }
   if (rank == ctas - 1 && tid == 0) a.query_start_loc[S] = static_cast<int>(min(all_rows, 0x7fffffffll));
-  __threadfence();
-  cluster.sync();
+  if (ctas > 1) {
+    __threadfence();
+    cluster.sync();
+  } else {
+    __syncthreads();
+  }
   if (rank == 0 && tid == 0 && fits) *a.free_count = count - static_cast<int>(all_blocks);
 
   // The rows: slots, positions, masks.
-  const bool cached = S < kOffsetsInShared;
+  const bool cached = S <= kInShared;
   if (cached) {
-    for (int r = tid; r <= S; r += kThreads) offsets[r] = __ldcg(a.query_start_loc + r);
+    for (int r = tid; r <= S; r += kThreads) {
+      offsets[r] = __ldcg(a.query_start_loc + r);
+      if (r < S) contexts[r] = __ldcg(a.seq_lens + r) > 0 ? __ldcg(a.context_lens + r) : -1;  // -1: refused
+    }
     __syncthreads();
   }
   auto first_row = [&](int r) -> int { return cached ? offsets[r] : __ldcg(a.query_start_loc + r); };
+  auto context = [&](int r) -> int {
+    return cached ? contexts[r] : (__ldcg(a.seq_lens + r) > 0 ? __ldcg(a.context_lens + r) : -1);
+  };
   const int live = fits ? static_cast<int>(all_rows) : 0;
+  const int stride = ctas * kThreads;
   for (long long t64 = static_cast<long long>(rank) * kThreads + tid; t64 < a.max_tokens;
-       t64 += static_cast<long long>(ctas) * kThreads) {
-    const int t = static_cast<int>(t64);
-    long long slot = -1;
-    int pos = 0;
-    unsigned long long mask[kMaxMaskWords] = {0, 0, 0, 0};
-    if (t < live) {
+       t64 += static_cast<long long>(kRows) * stride) {
+    int req[kRows], row_in[kRows], pos[kRows], id[kRows];
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      const long long t = t64 + static_cast<long long>(u) * stride;
+      req[u] = -1;
+      if (t >= live) continue;
       int lo = 0, hi = S;  // the last request whose first row is at or before t
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -238,36 +258,45 @@ __global__ void __launch_bounds__(kThreads) plan_step_kernel(const PlanStepArgs 
         else
           hi = mid;
       }
-      const int r = lo;
-      const int f = first_row(r);
-      const int i = t - f;
-      const int len = __ldcg(a.seq_lens + r);
-      if (len > 0) {  // 0: the request was refused
-        const int ctx = __ldcg(a.context_lens + r);
-        const int p = ctx + i;
-        const int id = __ldcg(a.block_tables + static_cast<size_t>(r) * a.max_blocks_per_seq + p / a.block_size);
-        if (static_cast<unsigned>(id) < static_cast<unsigned>(a.num_blocks))
-          slot = static_cast<long long>(id) * a.block_size + p % a.block_size;
+      const int ctx = context(lo);
+      if (ctx < 0) continue;
+      req[u] = lo;
+      row_in[u] = static_cast<int>(t) - first_row(lo);
+      pos[u] = ctx + row_in[u];
+      id[u] = __ldcg(a.block_tables + static_cast<size_t>(lo) * a.max_blocks_per_seq + pos[u] / a.block_size);
+    }
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      const long long t = t64 + static_cast<long long>(u) * stride;
+      if (t >= a.max_tokens) break;
+      long long slot = -1;
+      int place = 0;
+      unsigned long long mask[kMaxMaskWords] = {0, 0, 0, 0};
+      if (req[u] >= 0) {
+        const int i = row_in[u];
+        if (static_cast<unsigned>(id[u]) < static_cast<unsigned>(a.num_blocks))
+          slot = static_cast<long long>(id[u]) * a.block_size + pos[u] % a.block_size;
         else
-          record_error(a.status, PA_DEV_BAD_BLOCK_ID, r, id);
-        pos = p;
+          record_error(a.status, PA_DEV_BAD_BLOCK_ID, req[u], id[u]);
+        place = pos[u];
         if (a.parents != nullptr) {
           // Up the tree: every parent comes before its child, so the walk ends.
+          const int32_t* parents = a.parents + (t - i);
           int depth = 0, node = i;
           while (true) {
 #pragma unroll
             for (int w = 0; w < kMaxMaskWords; ++w)
               if (node >> 6 == w) mask[w] |= 1ull << (node & 63);
-            const int up = __ldg(a.parents + f + node);
+            const int up = __ldg(parents + node);
             if (up < -1 || up >= node) {
-              record_error(a.status, PA_DEV_BAD_PARENT, r, up);
+              record_error(a.status, PA_DEV_BAD_PARENT, req[u], up);
               break;
             }
             if (up < 0) break;
             node = up;
             ++depth;
           }
-          pos = ctx + depth;
+          place += depth - i;
         } else {
           // A chain: row i sees rows 0 .. i.
 #pragma unroll
@@ -277,12 +306,12 @@ __global__ void __launch_bounds__(kThreads) plan_step_kernel(const PlanStepArgs 
           }
         }
       }
-    }
-    a.slot_mapping[t] = slot;
-    a.positions[t] = pos;
+      a.slot_mapping[t] = slot;
+      a.positions[t] = place;
 #pragma unroll
-    for (int w = 0; w < kMaxMaskWords; ++w)
-      if (w < a.words) a.tree_masks[static_cast<size_t>(t) * a.words + w] = mask[w];
+      for (int w = 0; w < kMaxMaskWords; ++w)
+        if (w < a.words) a.tree_masks[static_cast<size_t>(t) * a.words + w] = mask[w];
+    }
   }
 }
 
@@ -305,22 +334,25 @@ __device__ __forceinline__ int release_need(const ReleaseArgs& a, int r, bool re
 __global__ void __launch_bounds__(kThreads) release_blocks_kernel(const ReleaseArgs a) {
   __shared__ long long warp_sums[kThreads / 32][2];
   __shared__ Exchange ex;
+  __shared__ int start[kThreads], first[kThreads];
   cg::cluster_group cluster = cg::this_cluster();
   griddep_launch_dependents();
   griddep_wait();
   const int rank = static_cast<int>(cluster.block_rank()), ctas = static_cast<int>(cluster.num_blocks());
-  const int tid = threadIdx.x, lane = tid & 31;
+  const int tid = threadIdx.x;
   const int S = a.num_seqs;
   const int per = (S + ctas - 1) / ctas;
   const int r0 = min(S, rank * per), r1 = min(S, r0 + per);
+  const bool one = r1 - r0 <= kThreads;
+  const int count = __ldcg(a.free_count);
   long long blocks = 0, e0, e1, ta, tb;
-  int keep = 0;
+  int keep = 0, n = 0;
   for (int base = r0; base < r1; base += kThreads) {
     const int r = base + tid;
-    block_scan2(0, r < r1 ? release_need(a, r, true, &keep) : 0, warp_sums, &e0, &e1, &ta, &tb);
+    n = r < r1 ? release_need(a, r, true, &keep) : 0;
+    block_scan2(0, n, warp_sums, &e0, &e1, &ta, &tb);
     blocks += tb;
   }
-  const int count = __ldcg(a.free_count);
   long long row, block, all_rows, all;
   exchange(cluster, &ex, 0, blocks, &row, &block, &all_rows, &all);
   if (count < 0 || count + all > a.capacity) {  // more blocks than there are: given back twice
@@ -330,14 +362,16 @@ __global__ void __launch_bounds__(kThreads) release_blocks_kernel(const ReleaseA
   }
   for (int base = r0; base < r1; base += kThreads) {
     const int r = base + tid;
-    const int n = r < r1 ? release_need(a, r, false, &keep) : 0;
-    block_scan2(0, n, warp_sums, &e0, &e1, &ta, &tb);
-    for_entries(r, n, block + e1, lane, [&](int wr, int j, long long i) {
-      const int first = (__ldcg(a.keep_lens + wr) + a.block_size - 1ll) / a.block_size;
-      const int id = __ldcg(a.block_tables + static_cast<size_t>(wr) * a.max_blocks_per_seq + first + j);
+    if (!one) {
+      n = r < r1 ? release_need(a, r, false, &keep) : 0;
+      block_scan2(0, n, warp_sums, &e0, &e1, &ta, &tb);
+    }
+    first[tid] = keep;
+    for_entries(static_cast<int>(e1), static_cast<int>(tb), start, [&](int i, int j, int e) {
+      const int id = __ldcg(a.block_tables + static_cast<size_t>(base + i) * a.max_blocks_per_seq + first[i] + j);
       if (static_cast<unsigned>(id) >= static_cast<unsigned>(a.num_blocks))
-        record_error(a.status, PA_DEV_BAD_BLOCK_ID, wr, id);
-      a.free_blocks[count + all - 1 - i] = id;
+        record_error(a.status, PA_DEV_BAD_BLOCK_ID, base + i, id);
+      a.free_blocks[count + all - 1 - block - e] = id;
     });
     if (n > 0) a.held_blocks[r] = keep;
     block += tb;
