@@ -344,6 +344,7 @@ struct CommitArgs {
   int32_t* status;
   int64_t layer_chunks;
   int row_chunks, num_layers, num_seqs, max_accepted, max_blocks_per_seq, block_size, num_blocks;
+  int warp_layers;                  // layers a warp moves (set by the launcher)
 };
 cudaError_t launch_commit_tokens(const CommitArgs& a, cudaStream_t stream);
 
