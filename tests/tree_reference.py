@@ -13,8 +13,11 @@ output by 2.1 delta (sum w |v| + |O|) while delta < 0.02:
 f16 numbers below 2^-14 are multiples of 2^-24: over e4m3 caches a small weight is
 off by up to 2^-25 instead, relative to a sum of weights that is at least 1 in the piece
 whose reference is the largest, so the output by 2^-25 sum |v| over the seen keys for each
-of the two halves of a piece's keys, which have references of their own: 2^-24; a small q by
-2^-25, the score by 2^-25 scale sum_i |k_ij|."""
+of the two halves of a piece's keys, which have references of their own: 2^-24.  There q is the
+sum of two e4m3 numbers in units in which its row's largest lies in [128, 256): the second is a
+multiple of 2^-9, so a q that the first leaves finer bits of is off by up to 2^-10, that is 2^-17
+of the row's largest, the score by 2^-17 scale max_i |q_i| sum_i |k_ij|; the products are twice as
+many, 17/16 as large in all."""
 import math
 
 import torch
@@ -45,7 +48,9 @@ def attend(q, k, v, seen, scale, u):
         delta = 2.0 ** -17 * mag + 2.0 ** -19 * top + 2.0 ** -20
         small = 0.0
         if u == 2.0 ** -11:
-            delta = delta + 2.0 ** -25 * scale * kh.abs().sum(1)[None, :].masked_fill(~seen, 0).amax(1, keepdim=True)
+            k_sum = kh.abs().sum(1)[None, :].masked_fill(~seen, 0).amax(1, keepdim=True)
+            delta = delta + (2.0 ** -16 * 17 / 16 - 2.0 ** -17) * mag
+            delta = delta + 2.0 ** -17 * scale * qh.abs().amax(1, keepdim=True) * k_sum
             small = 2.0 ** -24 * (seen.double() @ vh.abs())
         assert float(delta.max()) < 0.02
         out[:, h] = o
