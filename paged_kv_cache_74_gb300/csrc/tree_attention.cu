@@ -27,10 +27,12 @@
 //   cuts leaves its pieces as fp32 records, which a second kernel merges with the whole
 //   device: the last contributor alone would read up to 152 records of 64 KB by itself
 //   where few long contexts are split over every SM.
-// * Warps: 0-3 softmax of slot 0, 4-7 of slot 1 (thread = row, its 128 scores of a
-//   step in registers, which the other warps give up: setmaxnreg); 8 range walk, Q
-//   and K copies (TMA); 9 and 11 MMA issue of a slot each; 10 V copies; over e4m3 caches 12-13 turn landed
-//   K steps into f16, 14-15 V steps.
+// * Warps: 0-3 softmax of slot 0, 4-7 of slot 1 (thread = row, two passes over its scores
+//   in TMEM); 8 range walk, Q and K copies (TMA); 9 and 11 MMA issue of a slot each; 10 V
+//   copies; over e4m3 caches 12-15 split q and turn landed V steps into f16.
+// * e4m3 keys are the operand as they lie in the cache: q is the exact sum of two e4m3
+//   operands (split_q), two products at twice the f16 rate.  V has to become f16: the
+//   weights need more bits than an e4m3 number or two have.
 // A step that holds nodes takes its mask from the row's words; V of keys that no
 // row of the unit sees is zeroed before the product (a zero weight does not
 // cancel a NaN inside the MMA).  Every wait is bounded; a timeout records
