@@ -692,7 +692,6 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
   } else {
     if (warp == 8) {
       // ====================================== range walk, Q and K producer
-      if (cta == 0) report_bad_requests(a, lane);
       const uint64_t policy = l2_policy_evict_first();
       if (lane == 0) {
         tma_prefetch_desc(&qmap);
@@ -700,11 +699,24 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         a.splits[cta].c1 = -1;  // no unit cut at the end of this range so far
       }
       const int H = a.num_kv_heads;
+      // 128 requests at a time, their loads in flight together.
+      int tiles[4], steps[4];
+      auto load_requests = [&](int rc) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const TreeReq p = tree_req(a, rc + 32 * i + lane);
+          tiles[i] = p.tiles;
+          steps[i] = req_steps(p);
+        }
+      };
       long long st = 0, un = 0;
-      for (int r = lane; r < a.num_seqs; r += 32) {
-        const TreeReq p = tree_req(a, r);
-        un += p.tiles;
-        st += static_cast<long long>(p.tiles) * req_steps(p);
+      for (int rc = 0; rc < a.num_seqs; rc += 128) {
+        load_requests(rc);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          un += tiles[i];
+          st += static_cast<long long>(tiles[i]) * steps[i];
+        }
       }
       const long long n_steps = warp_sum64(st) * H, n_units = warp_sum64(un) * H;
       const long long Cw = kStepCost * n_steps + kUnitCost * n_units;
@@ -725,22 +737,26 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         // The request that holds x0, and the cost before it.
         int r = -1;
         long long cb = 0;
-        for (int rc = 0; rc < a.num_seqs && r < 0; rc += 32) {
-          const TreeReq p = tree_req(a, rc + lane);
-          const long long cost = (CS + CT * req_steps(p)) * p.tiles * H;
-          long long incl = cost;
+        for (int rc = 0; rc < a.num_seqs && r < 0; rc += 128) {
+          if (a.num_seqs > 128) load_requests(rc);
 #pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += v;
-          }
-          const unsigned hit = __ballot_sync(0xffffffffu, cb + incl > x0);
-          if (hit != 0) {
-            const int first = __ffs(hit) - 1;
-            cb += __shfl_sync(0xffffffffu, incl - cost, first);
-            r = rc + first;
-          } else {
-            cb += __shfl_sync(0xffffffffu, incl, 31);
+          for (int i = 0; i < 4; ++i) {
+            if (r >= 0) continue;
+            const long long cost = (CS + CT * steps[i]) * tiles[i] * H;
+            long long incl = cost;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+              const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+              if (lane >= o) incl += v;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, cb + incl > x0);
+            if (hit != 0) {
+              const int first = __ffs(hit) - 1;
+              cb += __shfl_sync(0xffffffffu, incl - cost, first);
+              r = rc + 32 * i + first;
+            } else {
+              cb += __shfl_sync(0xffffffffu, incl, 31);
+            }
           }
         }
         TreeReq p = tree_req(a, r);
@@ -834,6 +850,7 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         mbar_arrive(bar(C::SEGFULL + seg % C::SEGS));
       }
       if (!ok && lane == 0) *fail_flag = 1;
+      if (cta == 0) report_bad_requests(a, lane);
     } else if (warp == 10) {
       // =========================================================== V producer
       const uint64_t policy = l2_policy_evict_first();
