@@ -13,6 +13,11 @@
 // n * group query rows.  A 128-key step reads 64 KB at head_dim 128 in bf16 (1.47 us of an SM's
 // share of the copy bandwidth) and takes 0.33 us of the SM's tensor core per 128 rows for each
 // of the two products: up to 256 rows a kv head the keys' bytes are the bound.
+// That holds to one tile of rows; what two tiles take in practice is the exponentials, maxima
+// and conversions of 256 x 128 scores a step (1.75 us with the products, not hidden by each other
+// entirely) and a unit's end.  Measured, bf16 in us a call: 64 requests x 16 nodes, 32 / 8 heads,
+// 512 to 4096 keys 117 (0.83 of the copy peak), 32 x 64 nodes 90 (809 TFLOP/s), 8 x 32768 keys
+// 174 (0.91); e4m3, 96 x up to 16 nodes, 64 / 8 heads, up to 4099 keys 142.
 // So the design reads the keys once for all rows:
 // * The rows of a kv head are packed, row = node * group + head: one TMA box
 //   {64, group, 128 / group} of q lands as the 128-row operand of the products.  A
@@ -31,7 +36,7 @@
 //   in TMEM); 8 range walk, Q and K copies (TMA); 9 and 11 MMA issue of a slot each; 10 V
 //   copies; over e4m3 caches 12-15 split q and turn landed V steps into f16.
 // * e4m3 keys are the operand as they lie in the cache: q is the exact sum of two e4m3
-//   operands (split_q), two products at twice the f16 rate.  V has to become f16: the
+//   operands (split_q), two products.  V has to become f16: the
 //   weights need more bits than an e4m3 number or two have.
 // A step that holds nodes takes its mask from the row's words; V of keys that no
 // row of the unit sees is zeroed before the product (a zero weight does not
@@ -48,6 +53,8 @@ namespace {
 
 constexpr float kLowest = -1e30f;     // finite stand-in for -inf in running maxima
 constexpr float kRescaleSlack = 8.0f;  // log2 units: the reference of a row moves lazily
+// What a step and a unit's start and end take, relative to each other.  10 to 16 per unit are
+// alike; 24 and 32 cost 2 and 5 % on 32 trees of 64 nodes, 5 % each on ragged trees.
 constexpr long long kStepCost = 4;
 constexpr long long kUnitCost = 12;
 
@@ -257,7 +264,8 @@ __device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
 // bf16 has eight significant bits, h takes four and what it leaves has at most four.  e is
 // the row's own, its largest value lands in [128, 256); so l is exact for all values down to
 // 2^-9 of the row's largest, and off by at most 2^-10 (2^-17 of the largest) below.  S = h K^T
-// + l K^T then takes K as it lies in the cache, at twice the f16 rate each: K is not converted.
+// + l K^T then takes K as it lies in the cache: K is not converted (and has no second place in
+// shared memory, and all converting warps work on V).
 // In place: h takes the place of the rows' first halves, l of the second (head_dim 64:
 // within the row).  Warp w4 of four, a row by four lanes.
 template <int D, bool KV8>
@@ -966,11 +974,11 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
           // Two tiles: both slots take every step; one: those of their parity (of the
           // CTA's step count g + k, so that a K stage always has the same owner).  Both
           // slots wait for and free every V step, in order: a barrier's parity names a
-          // phase only to who has seen the one before.  With two tiles they issue in turn: at
-          // the same time their products share the tensor core, both softmaxes start
-          // together when they are done, and the core idles meanwhile.  A slot without a step still waits
-          // for the segment's Q and the end of the one before, so that its arrivals
-          // count for this one.
+          // phase only to who has seen the one before.  With two tiles they issue in
+          // turn: at the same time their products share the tensor core, both softmaxes start
+          // together when they are done, and the core idles meanwhile (32 trees of 64 nodes:
+          // 127 us without, 106 with turns).  A slot without a step still waits for the segment's Q
+          // and the end of the one before, so that its arrivals count for this one.
           const int k0 = two ? 0 : (g ^ b) & 1, dk = two ? 1 : 2;
           const int qb = two ? b : 0;
           ok = KV8 ? wait(C::QCONV, seg & 1, 71) : wait(C::QFULL + qb, qc[qb] & 1, 71);
@@ -1089,7 +1097,8 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
   }
 }
 
-// Merges the units that range boundaries cut.  Block (c, b, z): slot b of the unit
+// Merges the units that range boundaries cut (151 of them: 8 us over 64 requests x 16 nodes,
+// 13 over two tiles a unit, 40 MB, caches cold).  Block (c, b, z): slot b of the unit
 // that CTA c began and did not finish.  A warp takes 8 rows x 32 columns, a thread two
 // groups of 4 columns, over the contributors in order, four at a time with all their loads
 // in flight: a unit mostly has two, and what counts is the chain of round trips.
