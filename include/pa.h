@@ -735,7 +735,7 @@ pa_status pa_release_blocks(const int32_t* block_tables, int32_t max_blocks_per_
 /*
  * pa_tree_workspace_size -- bytes of workspace pa_tree_attention needs (status
  * record and the partial records of units cut between CTAs), on the current device.
- * No part of it needs initialising.  Returns 0 for invalid arguments.
+ * Beside the status record no part of it needs initialising.  Returns 0 for invalid arguments.
  */
 size_t pa_tree_workspace_size(int32_t num_seqs, int32_t total_q, int32_t num_heads,
                               int32_t num_kv_heads, int32_t head_dim, int32_t max_seq_len);
