@@ -107,7 +107,8 @@ struct TreeCfg {
   static constexpr int QFREE = QFULL + 2;        // the last S product of a segment is done
   static constexpr int SFULL = QFREE + 1;        // [2] S of a slot in TMEM
   static constexpr int PFULL = SFULL + 2;        // [2] P of a slot in TMEM (4 warps)
-  static constexpr int OFULL = PFULL + 2;        // the last P.V product of a segment is done
+  static constexpr int PHALF = PFULL + 2;        // [2] P of its first 64 keys, O rescaled
+  static constexpr int OFULL = PHALF + 2;        // the last P.V product of a segment is done
   static constexpr int OFREE = OFULL + 1;        // O read at a segment's end (8 warps)
   static constexpr int SEGFULL = OFREE + 1;      // [SEGS]
   static constexpr int SEGFREE = SEGFULL + SEGS; // [SEGS] every role is done with it
@@ -389,7 +390,7 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
   if (tid == 0) {
     for (int k = 0; k < C::NBAR; ++k) {
       int count = 1;
-      if (k == C::PFULL || k == C::PFULL + 1) count = 4;
+      if (k >= C::PFULL && k < C::PHALF + 2) count = 4;
       if (KV8 && ((k >= C::VFULL && k < C::VFULL + C::NV) || k == C::QCONV || k >= C::VRAWFREE)) count = 4;
       if (k == C::OFREE || k == C::SYNC || (KV8 && k == C::EXPFREE)) count = 8;
       if ((k >= C::KFREE && k < C::KFREE + C::NK) || (k >= C::VFREE && k < C::VFREE + C::NV) || k == C::QFREE ||
@@ -508,6 +509,7 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         }
         if (!(ok = warp_wait(C::SFULL + b, sc++ & 1, 82))) break;
         tc_fence_after();
+        constexpr int W = KV8 ? 32 : 64;
         if (live) {
           if (masked) {
             // Scores of unseen keys become -inf in place, 32 columns at a time (a loop of
@@ -534,7 +536,6 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
           // code outgrew the instruction caches (e4m3, five roles at once: 206 -> 154 us on a
           // batch of 96 requests, W = 32; 64: 162.  bf16: 64 is the better one, 102 against 107
           // us on 32 trees of 64 nodes).
-          constexpr int W = KV8 ? 32 : 64;
           // The row's maximum; the reference moves before any weight.
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
@@ -556,28 +557,6 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
             l_run *= alpha;
             m_ref = m_tile;
           }
-          // The weights, 16 bits each, over the scores' columns.
-          const float2 sl = make_float2(sl2, sl2), mm = make_float2(-m_ref, -m_ref);
-          float2 sum[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll 1
-          for (int c = 0; c < C::BN; c += W) {
-            uint32_t sr[W], pk[W / 2];
-#pragma unroll
-            for (int e = 0; e < W; e += 32) tmem_ld32_async(tm_s + c + e, sr + e);
-            tmem_wait_ld();
-            pin(sr);
-#pragma unroll
-            for (int e = 0; e < W; e += 2) {
-              const float2 x = __ffma2_rn(make_float2(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])), sl, mm);
-              const float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
-              pk[e / 2] = KV8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
-              sum[(e / 2) % 4] = __fadd2_rn(sum[(e / 2) % 4], make_float2(p0, p1));
-            }
-#pragma unroll
-            for (int e = 0; e < W / 2; e += 16) tmem_st16_async(tm_s + c / 2 + e, pk + e);
-          }
-          const float2 ps = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
-          l_run += ps.x + ps.y;
           if (__any_sync(0xffffffffu, moved) && !first) {
             // S of this step is done, so the slot's P V before it is too.
 #pragma unroll 1
@@ -604,6 +583,40 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
                            make_uint4(0u, 0u, 0u, 0u));
           }
           fence_proxy_async_smem();
+        }
+        // The first half of P V starts while the second half of P is worked out.
+        auto half_done = [&]() {
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(C::PHALF + b));
+        };
+        if (live) {
+          // The weights, 16 bits each, over the scores' columns.
+          const float2 sl = make_float2(sl2, sl2), mm = make_float2(-m_ref, -m_ref);
+          float2 sum[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+          for (int c = 0; c < C::BN; c += W) {
+            uint32_t sr[W], pk[W / 2];
+#pragma unroll
+            for (int e = 0; e < W; e += 32) tmem_ld32_async(tm_s + c + e, sr + e);
+            tmem_wait_ld();
+            pin(sr);
+#pragma unroll
+            for (int e = 0; e < W; e += 2) {
+              const float2 x = __ffma2_rn(make_float2(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])), sl, mm);
+              const float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
+              pk[e / 2] = KV8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+              sum[(e / 2) % 4] = __fadd2_rn(sum[(e / 2) % 4], make_float2(p0, p1));
+            }
+#pragma unroll
+            for (int e = 0; e < W / 2; e += 16) tmem_st16_async(tm_s + c / 2 + e, pk + e);
+            if (c + W == C::BN / 2) half_done();
+          }
+          const float2 ps = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
+          l_run += ps.x + ps.y;
+        } else {
+          half_done();
         }
         tmem_wait_st();
         tc_fence_before();  // P and O precede the next products
@@ -954,13 +967,18 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         };
         // O += P V of V step gv (P: 16 bits in the slot's S columns).
         auto issue_pv = [&](int gv, bool acc, bool in_turn) -> bool {
-          if (!wait(C::VFULL + gv % C::NV, (gv / C::NV) & 1, 73) || !wait(C::PFULL + b, pc++ & 1, 75)) return false;
+          if (!wait(C::VFULL + gv % C::NV, (gv / C::NV) & 1, 73) || !wait(C::PHALF + b, pc & 1, 75)) return false;
           if (in_turn && (b == 1 || turns > 0) && !wait(C::TURN + b, (b == 1 ? turns : turns - 1) & 1, 77)) return false;
           tc_fence_after();
           const uint64_t v0 = vd + (gv % C::NV) * (C::TBYTES >> 4);
           umma_tmem_a(to, ts, v0, C::IDESC_O, acc ? 1u : 0u);
 #pragma unroll
-          for (int ks = 1; ks < C::BN / 16; ++ks)
+          for (int ks = 1; ks < C::BN / 32; ++ks)
+            umma_tmem_a(to, ts + ks * 8, v0 + ((ks * C::BLOCK_BYTES) >> 4), C::IDESC_O, 1u);
+          if (!wait(C::PFULL + b, pc++ & 1, 75)) return false;
+          tc_fence_after();
+#pragma unroll
+          for (int ks = C::BN / 32; ks < C::BN / 16; ++ks)
             umma_tmem_a(to, ts + ks * 8, v0 + ((ks * C::BLOCK_BYTES) >> 4), C::IDESC_O, 1u);
           return true;
         };
