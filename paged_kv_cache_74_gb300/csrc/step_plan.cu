@@ -173,6 +173,8 @@ __global__ void __launch_bounds__(kThreads) plan_step_kernel(const PlanStepArgs 
   const int per = (S + ctas - 1) / ctas;
   const int r0 = min(S, rank * per), r1 = min(S, r0 + per);
   const bool one = r1 - r0 <= kThreads;  // (the slice's state is read and summed once)
+  const bool cached = S <= kInShared;
+  const bool local = ctas == 1 && one;   // all requests are this CTA's, each a thread's
   const int count = __ldcg(a.free_count);
 
   // Sums of this CTA's slice.
@@ -214,14 +216,22 @@ __global__ void __launch_bounds__(kThreads) plan_step_kernel(const PlanStepArgs 
       a.block_tables[static_cast<size_t>(base + i) * a.max_blocks_per_seq + first[i] + j] = id;
     });
     if (r < r1) {
-      a.query_start_loc[r] = static_cast<int>(min(row + e0, 0x7fffffffll));
+      const int at = static_cast<int>(min(row + e0, 0x7fffffffll));
+      a.query_start_loc[r] = at;
       a.seq_lens[r] = go ? s.len : 0;
       if (go && s.blocks > 0) a.held_blocks[r] = s.held + s.blocks;
+      if (local) {
+        offsets[r] = at;
+        contexts[r] = go && s.len > 0 ? s.ctx : -1;
+      }
     }
     row += ta;
     block += tb;
   }
-  if (rank == ctas - 1 && tid == 0) a.query_start_loc[S] = static_cast<int>(min(all_rows, 0x7fffffffll));
+  if (rank == ctas - 1 && tid == 0) {
+    a.query_start_loc[S] = static_cast<int>(min(all_rows, 0x7fffffffll));
+    if (local) offsets[S] = static_cast<int>(min(all_rows, 0x7fffffffll));
+  }
   if (ctas > 1) {
     __threadfence();
     cluster.sync();
@@ -231,8 +241,7 @@ __global__ void __launch_bounds__(kThreads) plan_step_kernel(const PlanStepArgs 
   if (rank == 0 && tid == 0 && fits) *a.free_count = count - static_cast<int>(all_blocks);
 
   // The rows: slots, positions, masks.
-  const bool cached = S <= kInShared;
-  if (cached) {
+  if (cached && !local) {
     for (int r = tid; r <= S; r += kThreads) {
       offsets[r] = __ldcg(a.query_start_loc + r);
       if (r < S) contexts[r] = __ldcg(a.seq_lens + r) > 0 ? __ldcg(a.context_lens + r) : -1;  // -1: refused
