@@ -20,8 +20,8 @@
 // spread evenly over the CTAs whatever the requests' lengths (the request of a
 // token by bisection of the row offsets).  Blocks are spread over a CTA's threads the
 // same way: with a request's blocks on a warp 67 requests, four of them prompts of up to
-// 11000 tokens, took 26.8 + 20.5 us (plan, release), now 16.6 + 5.8; 256 requests with trees of
-// 8 to 24 rows 14.2 + 5.6, four small requests 9.2 + 5.1, each alone with cold caches.
+// 11000 tokens, took 26.8 + 20.5 us (plan, release), now 16.8 + 6.2; 256 requests with trees of
+// 8 to 24 rows 14.2 + 5.4, four small requests 8.3 + 4.9, each alone with cold caches.
 #include <cooperative_groups.h>
 
 #include <algorithm>

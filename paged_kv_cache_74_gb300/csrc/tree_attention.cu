@@ -14,10 +14,10 @@
 // share of the copy bandwidth) and takes 0.33 us of the SM's tensor core per 128 rows for each
 // of the two products: up to 256 rows a kv head the keys' bytes are the bound.
 // That holds to one tile of rows; what two tiles take in practice is the exponentials, maxima
-// and conversions of 256 x 128 scores a step (1.75 us with the products, not hidden by each other
+// and conversions of 256 x 128 scores a step (1.7 us with the products, not hidden by each other
 // entirely) and a unit's end.  Measured, bf16 in us a call: 64 requests x 16 nodes, 32 / 8 heads,
-// 512 to 4096 keys 117 (0.83 of the copy peak), 32 x 64 nodes 90 (809 TFLOP/s), 8 x 32768 keys
-// 174 (0.91); e4m3, 96 x up to 16 nodes, 64 / 8 heads, up to 4099 keys 142.
+// 512 to 4096 keys 114 (0.85 of the copy peak), 32 x 64 nodes 87 (832 TFLOP/s), 8 x 32768 keys
+// 172 (0.92); e4m3, 96 x up to 16 nodes, 64 / 8 heads, up to 4099 keys 142.
 // So the design reads the keys once for all rows:
 // * The rows of a kv head are packed, row = node * group + head: one TMA box
 //   {64, group, 128 / group} of q lands as the 128-row operand of the products.  A
@@ -584,7 +584,8 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
           }
           fence_proxy_async_smem();
         }
-        // The first half of P V starts while the second half of P is worked out.
+        // The first half of P V starts while the second half of P is worked out (32 trees
+        // of 64 nodes: 89.9 -> 87.5 us).
         auto half_done = [&]() {
           tmem_wait_st();
           tc_fence_before();
