@@ -799,25 +799,32 @@ def tree_workspace_size(num_seqs, total_q, num_heads, num_kv_heads, head_dim, ma
 
 def _tree_attention(fn, cache_dtype, scales, q, key_cache, value_cache, query_start_loc, seq_lens,
                     block_tables, tree_masks, max_query_len, max_seq_len, scale, out, workspace):
-    dev, out = _attention_args(q, key_cache, value_cache, cache_dtype, block_tables, seq_lens, out, None,
-                               None, None, workspace, query_start_loc)
-    if not isinstance(tree_masks, torch.Tensor) or tree_masks.dtype is not torch.int64 or \
-            tree_masks.get_device() != dev or not tree_masks.is_contiguous():
-        _refuse("tree_masks", tree_masks, torch.int64, dev)
-    tq, hq, d = q.shape
-    nb, bs, hkv, _ = key_cache.shape
-    S = seq_lens.shape[0]
-    if query_start_loc is None or query_start_loc.numel() != S + 1:
-        raise ValueError(f"query_start_loc must be [{S + 1}]")
-    if tree_masks.dim() not in (1, 2) or tree_masks.shape[0] != tq:
-        raise ValueError(f"tree_masks must be [{tq}, words]")
-    words = tree_masks.shape[1] if tree_masks.dim() == 2 else 1
+    dev = _device_of("q", q)
+    bf16, i32 = torch.bfloat16, torch.int32
+    _check_all(dev, (("q", q, bf16), ("key_cache", key_cache, cache_dtype),
+                     ("value_cache", value_cache, cache_dtype), ("query_start_loc", query_start_loc, i32),
+                     ("seq_lens", seq_lens, i32), ("block_tables", block_tables, i32),
+                     ("tree_masks", tree_masks, torch.int64)),
+               (("out", out, bf16), ("workspace", workspace, torch.uint8)))
+    q_shape, shape = q.shape, key_cache.shape
+    if len(q_shape) != 3 or len(shape) != 4 or shape[3] != q_shape[2] or value_cache.shape != shape:
+        raise ValueError("cache shapes do not match q")
+    tq, hq, d = q_shape
+    nb, bs, hkv, _ = shape
+    S, width = _table_shape(block_tables)
+    if seq_lens.numel() != S or query_start_loc.numel() != S + 1:
+        raise ValueError(f"seq_lens must be [{S}] and query_start_loc [{S + 1}]")
+    words = _mask_words(tree_masks, tq)
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != q_shape:
+        raise ValueError("out must have q's shape")
     if workspace is None:
         with torch.cuda.device(dev):
             workspace = new_workspace(tree_workspace_size(S, tq, hq, hkv, d, max_seq_len), q.device)
     _launch(fn, dev, out.data_ptr(), q.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
             query_start_loc.data_ptr(), seq_lens.data_ptr(), S, tq, int(max_query_len), int(max_seq_len),
-            block_tables.data_ptr(), block_tables.shape[1], tree_masks.data_ptr(), words, hq, hkv, d, bs, nb,
+            block_tables.data_ptr(), width, tree_masks.data_ptr(), words, hq, hkv, d, bs, nb,
             float(scale), *scales, workspace.data_ptr(), workspace.numel())
     return out
 
@@ -848,8 +855,22 @@ def _lens(S, *named):
 
 
 def _status4(status):
-    if status is not None and status.numel() < 4:
+    if status.numel() < 4:
         raise ValueError("status must hold 4 values")
+
+
+def _table_shape(block_tables):
+    shape = block_tables.shape
+    if len(shape) != 2:
+        raise ValueError("block_tables must be [num_seqs, max_blocks]")
+    return shape
+
+
+def _mask_words(tree_masks, rows):
+    shape = tree_masks.shape
+    if len(shape) not in (1, 2) or shape[0] != rows:
+        raise ValueError(f"tree_masks must be [{rows}, words]")
+    return shape[1] if len(shape) == 2 else 1
 
 
 def plan_step(block_tables, held_blocks, context_lens, query_lens, free_blocks, free_count, block_size,
@@ -870,23 +891,21 @@ def plan_step(block_tables, held_blocks, context_lens, query_lens, free_blocks, 
                      ("query_start_loc", query_start_loc, i32), ("seq_lens", seq_lens, i32),
                      ("slot_mapping", slot_mapping, i64), ("positions", positions, i32)),
                (("parents", parents, i32), ("tree_masks", tree_masks, i64), ("status", status, i32)))
-    if block_tables.dim() != 2:
-        raise ValueError("block_tables must be [num_seqs, max_blocks]")
-    S, T = block_tables.shape[0], slot_mapping.numel()
-    _lens(S, ("held_blocks", held_blocks), ("context_lens", context_lens), ("query_lens", query_lens),
-          ("seq_lens", seq_lens))
-    _lens(T, ("positions", positions))
+    S, width = _table_shape(block_tables)
+    T = slot_mapping.numel()
+    if not held_blocks.numel() == context_lens.numel() == query_lens.numel() == seq_lens.numel() == S:
+        _lens(S, ("held_blocks", held_blocks), ("context_lens", context_lens), ("query_lens", query_lens),
+              ("seq_lens", seq_lens))
+    if positions.numel() != T:
+        raise ValueError(f"positions must be [{T}]")
     if query_start_loc.numel() != S + 1 or free_count.numel() != 1:
         raise ValueError(f"query_start_loc must be [{S + 1}] and free_count [1]")
     if parents is not None and parents.numel() != T:
         raise ValueError(f"parents must be [{T}]")
-    words = 0
-    if tree_masks is not None:
-        words = tree_masks.shape[1] if tree_masks.dim() == 2 else 1
-        if tree_masks.dim() not in (1, 2) or tree_masks.shape[0] != T:
-            raise ValueError(f"tree_masks must be [{T}, words]")
-    _status4(status)
-    _launch("pa_plan_step", dev, block_tables.data_ptr(), block_tables.shape[1], held_blocks.data_ptr(),
+    words = _mask_words(tree_masks, T) if tree_masks is not None else 0
+    if status is not None:
+        _status4(status)
+    _launch("pa_plan_step", dev, block_tables.data_ptr(), width, held_blocks.data_ptr(),
             context_lens.data_ptr(), query_lens.data_ptr(), S, free_blocks.data_ptr(), free_blocks.numel(),
             free_count.data_ptr(), int(block_size), int(num_blocks), query_start_loc.data_ptr(),
             seq_lens.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(), T, _addr(parents),
@@ -903,13 +922,14 @@ def release_blocks(block_tables, held_blocks, keep_lens, free_blocks, free_count
     _check_all(dev, (("block_tables", block_tables, i32), ("held_blocks", held_blocks, i32),
                      ("keep_lens", keep_lens, i32), ("free_blocks", free_blocks, i32),
                      ("free_count", free_count, i32)), (("status", status, i32),))
-    if block_tables.dim() != 2:
-        raise ValueError("block_tables must be [num_seqs, max_blocks]")
-    S = block_tables.shape[0]
-    _lens(S, ("held_blocks", held_blocks), ("keep_lens", keep_lens))
-    _lens(1, ("free_count", free_count))
-    _status4(status)
-    _launch("pa_release_blocks", dev, block_tables.data_ptr(), block_tables.shape[1], held_blocks.data_ptr(),
+    S, width = _table_shape(block_tables)
+    if not held_blocks.numel() == keep_lens.numel() == S:
+        _lens(S, ("held_blocks", held_blocks), ("keep_lens", keep_lens))
+    if free_count.numel() != 1:
+        raise ValueError("free_count must be [1]")
+    if status is not None:
+        _status4(status)
+    _launch("pa_release_blocks", dev, block_tables.data_ptr(), width, held_blocks.data_ptr(),
             keep_lens.data_ptr(), S, free_blocks.data_ptr(), free_blocks.numel(), free_count.data_ptr(),
             int(block_size), int(num_blocks), _addr(status))
 
@@ -927,22 +947,25 @@ def commit_tokens(key_cache, value_cache, block_tables, context_lens, query_lens
                      ("block_tables", block_tables, i32), ("context_lens", context_lens, i32),
                      ("query_lens", query_lens, i32), ("accepted", accepted, i32),
                      ("accept_lens", accept_lens, i32)), (("new_lens", new_lens, i32), ("status", status, i32)))
-    if key_cache.dim() not in (4, 5) or value_cache.shape != key_cache.shape:
+    shape = key_cache.shape
+    if len(shape) not in (4, 5) or value_cache.shape != shape:
         raise ValueError("key_cache and value_cache must be [(layers,) num_blocks, block, kv_heads, head_dim]")
-    layers = key_cache.shape[0] if key_cache.dim() == 5 else 1
-    nb, bs, hkv, d = key_cache.shape[-4:]
-    if block_tables.dim() != 2 or accepted.dim() != 2 or accepted.shape[0] != block_tables.shape[0]:
-        raise ValueError("block_tables must be [num_seqs, max_blocks] and accepted [num_seqs, max_accepted]")
-    S = block_tables.shape[0]
-    _lens(S, ("context_lens", context_lens), ("query_lens", query_lens), ("accept_lens", accept_lens))
+    layers, nb, bs, hkv, d = shape if len(shape) == 5 else (1, *shape)
+    S, width = _table_shape(block_tables)
+    path = accepted.shape
+    if len(path) != 2 or path[0] != S:
+        raise ValueError(f"accepted must be [{S}, max_accepted]")
     if new_lens is None:
         new_lens = torch.empty_like(context_lens)
-    _lens(S, ("new_lens", new_lens))
-    _status4(status)
+    if not context_lens.numel() == query_lens.numel() == accept_lens.numel() == new_lens.numel() == S:
+        _lens(S, ("context_lens", context_lens), ("query_lens", query_lens), ("accept_lens", accept_lens),
+              ("new_lens", new_lens))
+    if status is not None:
+        _status4(status)
     _launch("pa_commit_tokens", dev, key_cache.data_ptr(), value_cache.data_ptr(), layers, block_tables.data_ptr(),
-            block_tables.shape[1], context_lens.data_ptr(), query_lens.data_ptr(), accepted.data_ptr(),
-            accepted.shape[1], accept_lens.data_ptr(), new_lens.data_ptr(), S, hkv, d, bs, nb,
-            key_cache.element_size(), _addr(status))
+            width, context_lens.data_ptr(), query_lens.data_ptr(), accepted.data_ptr(),
+            path[1], accept_lens.data_ptr(), new_lens.data_ptr(), S, hkv, d, bs, nb,
+            1 if dtype is torch.uint8 else 2, _addr(status))
     return new_lens
 
 
