@@ -90,12 +90,19 @@ def test_scores_far_apart(cuda_lib, fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
-@pytest.mark.parametrize("count,nodes", [(300, 1), (77, 3), (40, 0)])
+@pytest.mark.parametrize("count,nodes", [(1100, 1), (300, 1), (77, 3), (40, 0)])
 def test_many_requests(cuda_lib, count, nodes, fp8):
     rng = random.Random(count)
     requests = [(nodes or rng.choice([0, 0, 1, 9]), rng.randint(0, 200)) for _ in range(count)]
     requests = [(n, c if n + c else 1) for n, c in requests]
     Batch(requests, 4, 2, 64, fp8=fp8, seed=count, pad_rows=2).check(cuda_lib)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_requests_that_share_their_context_blocks(cuda_lib, fp8):
+    b = Batch([(12, 320), (30, 320), (1, 320)], 8, 2, 128, fp8=fp8, seed=13)
+    b.tables[1:, :20] = b.tables[0, :20]
+    b.check(cuda_lib)
 
 
 def test_chains_agree_with_prefill(cuda_lib):
