@@ -80,12 +80,20 @@ struct Exchange {
   long long rows[kMaxCluster], blocks[kMaxCluster];  // sums of each CTA's slice
 };
 
+// Shared memory of a CTA that has not started may not be written: every CTA arrives on the
+// cluster's barrier first thing and waits there before its first remote store, so that the
+// loads and the scan between them cover the wait.
+__device__ __forceinline__ void cluster_started(cg::cluster_group& cluster) {
+  if (cluster.num_blocks() > 1) cluster_arrive();
+}
+
 // This CTA's sums to every CTA of the cluster; returns the sums of the slices
 // before this one and of all.  Ends in a cluster barrier.
 __device__ __forceinline__ void exchange(cg::cluster_group& cluster, Exchange* ex, long long rows, long long blocks,
                                          long long* rows_before, long long* blocks_before, long long* rows_all,
                                          long long* blocks_all) {
   const int rank = static_cast<int>(cluster.block_rank()), n = static_cast<int>(cluster.num_blocks());
+  if (n > 1) cluster_wait();  // for cluster_started(): every CTA's shared memory is there
   if (static_cast<int>(threadIdx.x) < n) {
     Exchange* to = cluster.map_shared_rank(ex, threadIdx.x);
     to->rows[rank] = rows;
@@ -165,6 +173,7 @@ __global__ void __launch_bounds__(kThreads) plan_step_kernel(const PlanStepArgs 
   __shared__ int start[kThreads], first[kThreads];
   __shared__ int offsets[kInShared + 1], contexts[kInShared];
   cg::cluster_group cluster = cg::this_cluster();
+  cluster_started(cluster);
   griddep_launch_dependents();
   griddep_wait();
   const int rank = static_cast<int>(cluster.block_rank()), ctas = static_cast<int>(cluster.num_blocks());
@@ -348,6 +357,7 @@ __global__ void __launch_bounds__(kThreads) release_blocks_kernel(const ReleaseA
   __shared__ Exchange ex;
   __shared__ int start[kThreads], first[kThreads];
   cg::cluster_group cluster = cg::this_cluster();
+  cluster_started(cluster);
   griddep_launch_dependents();
   griddep_wait();
   const int rank = static_cast<int>(cluster.block_rank()), ctas = static_cast<int>(cluster.num_blocks());
