@@ -808,9 +808,12 @@ pa_status pa_tree_attention_fp8(void* out, const void* q, const void* key_cache,
  *                  may not overlap an input (PA_ERR_INVALID)
  * The row at position context_lens[r] + i becomes the one at context_lens[r] +
  * accepted[r][i].  Requests whose path, lengths or block ids are out of range
- * are recorded and skipped (new_lens = context_lens).  num_kv_heads * head_dim *
+ * are recorded and skipped (new_lens = context_lens).  Each request with accepted rows
+ * holds blocks for context_lens + query_lens tokens: one that pa_plan_step refused does not,
+ * and what its table has behind the held blocks may be another request's by now.  Its accept_lens
+ * is 0 here; pa_commit_planned_tokens sees to that itself.  num_kv_heads * head_dim *
  * element_bytes a multiple of 16, any positive block_size; num_seqs == 0 or
- * num_layers == 0 is a no-op.  Requests that move into a shared block race.
+ * num_layers == 0 is a no-op (new_lens is not written).  Requests that move into a shared block race.
  */
 pa_status pa_commit_tokens(void* key_cache, void* value_cache, int32_t num_layers,
                            const int32_t* block_tables, int32_t max_blocks_per_seq,
@@ -820,6 +823,24 @@ pa_status pa_commit_tokens(void* key_cache, void* value_cache, int32_t num_layer
                            int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
                            int32_t num_blocks, int32_t element_bytes, int32_t* device_status,
                            void* stream);
+
+/*
+ * pa_commit_planned_tokens -- pa_commit_tokens behind a pa_plan_step whose outcome the host
+ * does not know (a captured step).
+ *
+ *   seq_lens       [num_seqs] int32, as the plan wrote them
+ * A request whose entry is not context_lens + query_lens (0: the plan refused it, or the whole
+ * batch) is left alone, new_lens = context_lens, and recorded as PA_DEV_BAD_SEQ_LEN if its
+ * accept_lens is not 0.  Everything else as in pa_commit_tokens.
+ */
+pa_status pa_commit_planned_tokens(void* key_cache, void* value_cache, int32_t num_layers,
+                                   const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                   const int32_t* context_lens, const int32_t* query_lens,
+                                   const int32_t* seq_lens, const int32_t* accepted,
+                                   int32_t max_accepted, const int32_t* accept_lens, int32_t* new_lens,
+                                   int32_t num_seqs, int32_t num_kv_heads, int32_t head_dim,
+                                   int32_t block_size, int32_t num_blocks, int32_t element_bytes,
+                                   int32_t* device_status, void* stream);
 
 #ifdef __cplusplus
 }

@@ -32,6 +32,7 @@ ABI_SYMBOLS = ("pa_status_string", "pa_abi_version", "pa_reshape_and_cache",
                "pa_qk_norm_rope_append", "pa_qk_norm_rope_append_fp8", "pa_decode_masked",
                "pa_decode_masked_fp8", "pa_prefill_masked_workspace_size", "pa_prefill_varlen_masked",
                "pa_prefill_varlen_masked_fp8", "pa_plan_step", "pa_release_blocks", "pa_commit_tokens",
+               "pa_commit_planned_tokens",
                "pa_tree_workspace_size", "pa_tree_attention", "pa_tree_attention_fp8")
 
 
@@ -121,6 +122,9 @@ def _declare(lib):
     lib.pa_release_blocks.argtypes = [_vp, _i32, _vp, _vp, _i32, _vp, _i32, _vp, _i32, _i32, _vp, _vp]
     lib.pa_commit_tokens.restype = ctypes.c_int
     lib.pa_commit_tokens.argtypes = [_vp, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _i32, _vp, _vp] + [_i32] * 6 + [_vp, _vp]
+    lib.pa_commit_planned_tokens.restype = ctypes.c_int
+    lib.pa_commit_planned_tokens.argtypes = [_vp, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _vp] + \
+        [_i32] * 6 + [_vp, _vp]
     lib.pa_tree_workspace_size.restype = _sz
     lib.pa_tree_workspace_size.argtypes = [_i32] * 6
     tree = [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _i32, _vp] + [_i32] * 6 + [_f32]
@@ -935,18 +939,21 @@ def release_blocks(block_tables, held_blocks, keep_lens, free_blocks, free_count
 
 
 def commit_tokens(key_cache, value_cache, block_tables, context_lens, query_lens, accepted, accept_lens,
-                  new_lens=None, status=None):
+                  new_lens=None, status=None, seq_lens=None):
     """Moves K and V of the accepted rows (accepted int32 [S, max_accepted], ascending,
     the first accept_lens [S] of them) to the slots behind context_lens [S], in caches
     [num_blocks, block, kv_heads, head_dim] or [layers, num_blocks, ..] (bf16 or
-    uint8).  Returns new_lens [S] = context_lens + accept_lens."""
+    uint8).  Returns new_lens [S] = context_lens + accept_lens.  With seq_lens [S], as
+    plan_step wrote them, requests that the plan refused are left alone (new_lens =
+    context_lens); without, their accept_lens must be 0."""
     dev = _device_of("key_cache", key_cache)
     i32 = torch.int32
     dtype = torch.uint8 if key_cache.dtype is torch.uint8 else torch.bfloat16
     _check_all(dev, (("key_cache", key_cache, dtype), ("value_cache", value_cache, dtype),
                      ("block_tables", block_tables, i32), ("context_lens", context_lens, i32),
                      ("query_lens", query_lens, i32), ("accepted", accepted, i32),
-                     ("accept_lens", accept_lens, i32)), (("new_lens", new_lens, i32), ("status", status, i32)))
+                     ("accept_lens", accept_lens, i32)), (("new_lens", new_lens, i32), ("status", status, i32),
+                                                        ("seq_lens", seq_lens, i32)))
     shape = key_cache.shape
     if len(shape) not in (4, 5) or value_cache.shape != shape:
         raise ValueError("key_cache and value_cache must be [(layers,) num_blocks, block, kv_heads, head_dim]")
@@ -962,8 +969,12 @@ def commit_tokens(key_cache, value_cache, block_tables, context_lens, query_lens
               ("new_lens", new_lens))
     if status is not None:
         _status4(status)
-    _launch("pa_commit_tokens", dev, key_cache.data_ptr(), value_cache.data_ptr(), layers, block_tables.data_ptr(),
-            width, context_lens.data_ptr(), query_lens.data_ptr(), accepted.data_ptr(),
+    fn, planned = "pa_commit_tokens", ()
+    if seq_lens is not None:
+        _lens(S, ("seq_lens", seq_lens))
+        fn, planned = "pa_commit_planned_tokens", (seq_lens.data_ptr(),)
+    _launch(fn, dev, key_cache.data_ptr(), value_cache.data_ptr(), layers, block_tables.data_ptr(),
+            width, context_lens.data_ptr(), query_lens.data_ptr(), *planned, accepted.data_ptr(),
             path[1], accept_lens.data_ptr(), new_lens.data_ptr(), S, hkv, d, bs, nb,
             1 if dtype is torch.uint8 else 2, _addr(status))
     return new_lens

@@ -38,6 +38,7 @@ __global__ void __launch_bounds__(kWarps * 32) commit_tokens_kernel(const Commit
   const int part = rest % (2 * segs);
   const bool first = rest == 0;  // reports, and writes the new length
   const int ctx = __ldg(a.context_lens + r), rows = __ldg(a.query_lens + r), n = __ldg(a.accept_lens + r);
+  const bool planned = a.seq_lens == nullptr || __ldg(a.seq_lens + r) == static_cast<long long>(ctx) + rows;
   const int32_t* path = a.accepted + static_cast<size_t>(r) * a.max_accepted;
   const int first_node = lane < a.max_accepted ? __ldg(path + lane) : -1;  // (before the lengths are known)
   const int32_t* table = a.block_tables + static_cast<size_t>(r) * a.max_blocks_per_seq;
@@ -58,6 +59,10 @@ __global__ void __launch_bounds__(kWarps * 32) commit_tokens_kernel(const Commit
   } else if (n < 0 || n > a.max_accepted || n > rows) {
     bad = PA_DEV_BAD_PATH;
     what = n;
+  } else if (!planned && n > 0) {
+    // The plan refused the request: the table's entries behind the held blocks are not its own.
+    bad = PA_DEV_BAD_SEQ_LEN;
+    what = __ldg(a.seq_lens + r);
   }
   long long src = -1, dst = -1;
   for (int base = 0; bad == PA_DEV_OK && base < n; base += 32) {

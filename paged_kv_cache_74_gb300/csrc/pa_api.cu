@@ -722,6 +722,63 @@ bool ranges_clash(const Range (&r)[N]) {
   return false;
 }
 
+// seq_lens: optional, as pa_plan_step wrote them.
+pa_status commit_tokens_impl(void* key_cache, void* value_cache, int32_t num_layers, const int32_t* block_tables,
+                             int32_t max_blocks_per_seq, const int32_t* context_lens, const int32_t* query_lens,
+                             const int32_t* seq_lens, const int32_t* accepted, int32_t max_accepted,
+                             const int32_t* accept_lens, int32_t* new_lens, int32_t num_seqs, int32_t num_kv_heads,
+                             int32_t head_dim, int32_t block_size, int32_t num_blocks, int32_t element_bytes,
+                             int32_t* device_status, void* stream) {
+  if (num_seqs < 0 || num_layers < 0 || max_blocks_per_seq < 1 || max_accepted < 1 || num_kv_heads < 1 ||
+      head_dim < 1 || block_size < 1 || num_blocks < 1)
+    return PA_ERR_INVALID;
+  const int64_t row_elems = static_cast<int64_t>(num_kv_heads) * head_dim;
+  if ((element_bytes != 1 && element_bytes != 2) || row_elems > (1 << 20) || row_elems * element_bytes % 16 != 0 ||
+      num_seqs > 65535 || num_layers > 65535)
+    return PA_ERR_UNSUPPORTED;
+  if (num_seqs == 0 || num_layers == 0) return PA_OK;
+  if (!key_cache || !value_cache || !block_tables || !context_lens || !query_lens || !accepted || !accept_lens)
+    return PA_ERR_INVALID;
+  if (!aligned(key_cache, 16) || !aligned(value_cache, 16)) return PA_ERR_INVALID;
+  const void* words[] = {block_tables, context_lens, query_lens, seq_lens, accepted, accept_lens, new_lens, device_status};
+  for (const void* p : words)
+    if (!aligned(p, 4)) return PA_ERR_INVALID;
+  const int64_t layer_chunks = row_elems * element_bytes / 16 * block_size * num_blocks;
+  const size_t s = static_cast<size_t>(num_seqs);
+  const size_t cache_bytes = static_cast<size_t>(layer_chunks) * 16 * num_layers;
+  const Range ranges[] = {{key_cache, cache_bytes, true},
+                          {value_cache, cache_bytes, true},
+                          {block_tables, s * max_blocks_per_seq * 4, false},
+                          {context_lens, s * 4, false},
+                          {query_lens, s * 4, false},
+                          {seq_lens, s * 4, false},
+                          {accepted, s * max_accepted * 4, false},
+                          {accept_lens, s * 4, false},
+                          {new_lens, s * 4, true},
+                          {device_status, 16, true}};
+  if (ranges_clash(ranges)) return PA_ERR_INVALID;
+  CommitArgs a;
+  a.key_cache = static_cast<uint4*>(key_cache);
+  a.value_cache = static_cast<uint4*>(value_cache);
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.query_lens = query_lens;
+  a.seq_lens = seq_lens;
+  a.accepted = accepted;
+  a.accept_lens = accept_lens;
+  a.new_lens = new_lens;
+  a.status = device_status;
+  a.layer_chunks = layer_chunks;
+  a.row_chunks = static_cast<int>(row_elems * element_bytes / 16);
+  a.num_layers = num_layers;
+  a.num_seqs = num_seqs;
+  a.max_accepted = max_accepted;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.block_size = block_size;
+  a.num_blocks = num_blocks;
+  return launch_commit_tokens(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
 }  // namespace
 }  // namespace pa
 
@@ -1443,52 +1500,23 @@ pa_status pa_commit_tokens(void* key_cache, void* value_cache, int32_t num_layer
                            int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
                            int32_t num_blocks, int32_t element_bytes, int32_t* device_status,
                            void* stream) {
-  if (num_seqs < 0 || num_layers < 0 || max_blocks_per_seq < 1 || max_accepted < 1 || num_kv_heads < 1 ||
-      head_dim < 1 || block_size < 1 || num_blocks < 1)
-    return PA_ERR_INVALID;
-  const int64_t row_elems = static_cast<int64_t>(num_kv_heads) * head_dim;
-  if ((element_bytes != 1 && element_bytes != 2) || row_elems > (1 << 20) || row_elems * element_bytes % 16 != 0 ||
-      num_seqs > 65535 || num_layers > 65535)
-    return PA_ERR_UNSUPPORTED;
-  if (num_seqs == 0 || num_layers == 0) return PA_OK;
-  if (!key_cache || !value_cache || !block_tables || !context_lens || !query_lens || !accepted || !accept_lens)
-    return PA_ERR_INVALID;
-  if (!aligned(key_cache, 16) || !aligned(value_cache, 16)) return PA_ERR_INVALID;
-  const void* words[] = {block_tables, context_lens, query_lens, accepted, accept_lens, new_lens, device_status};
-  for (const void* p : words)
-    if (!aligned(p, 4)) return PA_ERR_INVALID;
-  const int64_t layer_chunks = row_elems * element_bytes / 16 * block_size * num_blocks;
-  const size_t s = static_cast<size_t>(num_seqs);
-  const size_t cache_bytes = static_cast<size_t>(layer_chunks) * 16 * num_layers;
-  const Range ranges[] = {{key_cache, cache_bytes, true},
-                          {value_cache, cache_bytes, true},
-                          {block_tables, s * max_blocks_per_seq * 4, false},
-                          {context_lens, s * 4, false},
-                          {query_lens, s * 4, false},
-                          {accepted, s * max_accepted * 4, false},
-                          {accept_lens, s * 4, false},
-                          {new_lens, s * 4, true},
-                          {device_status, 16, true}};
-  if (ranges_clash(ranges)) return PA_ERR_INVALID;
-  CommitArgs a;
-  a.key_cache = static_cast<uint4*>(key_cache);
-  a.value_cache = static_cast<uint4*>(value_cache);
-  a.block_tables = block_tables;
-  a.context_lens = context_lens;
-  a.query_lens = query_lens;
-  a.accepted = accepted;
-  a.accept_lens = accept_lens;
-  a.new_lens = new_lens;
-  a.status = device_status;
-  a.layer_chunks = layer_chunks;
-  a.row_chunks = static_cast<int>(row_elems * element_bytes / 16);
-  a.num_layers = num_layers;
-  a.num_seqs = num_seqs;
-  a.max_accepted = max_accepted;
-  a.max_blocks_per_seq = max_blocks_per_seq;
-  a.block_size = block_size;
-  a.num_blocks = num_blocks;
-  return launch_commit_tokens(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  return commit_tokens_impl(key_cache, value_cache, num_layers, block_tables, max_blocks_per_seq, context_lens,
+                            query_lens, nullptr, accepted, max_accepted, accept_lens, new_lens, num_seqs,
+                            num_kv_heads, head_dim, block_size, num_blocks, element_bytes, device_status, stream);
+}
+
+pa_status pa_commit_planned_tokens(void* key_cache, void* value_cache, int32_t num_layers,
+                                   const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                   const int32_t* context_lens, const int32_t* query_lens,
+                                   const int32_t* seq_lens, const int32_t* accepted,
+                                   int32_t max_accepted, const int32_t* accept_lens, int32_t* new_lens,
+                                   int32_t num_seqs, int32_t num_kv_heads, int32_t head_dim,
+                                   int32_t block_size, int32_t num_blocks, int32_t element_bytes,
+                                   int32_t* device_status, void* stream) {
+  if (num_seqs > 0 && !seq_lens) return PA_ERR_INVALID;
+  return commit_tokens_impl(key_cache, value_cache, num_layers, block_tables, max_blocks_per_seq, context_lens,
+                            query_lens, seq_lens, accepted, max_accepted, accept_lens, new_lens, num_seqs,
+                            num_kv_heads, head_dim, block_size, num_blocks, element_bytes, device_status, stream);
 }
 
 size_t pa_tree_workspace_size(int32_t num_seqs, int32_t total_q, int32_t num_heads,

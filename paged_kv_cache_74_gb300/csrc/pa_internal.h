@@ -338,6 +338,7 @@ struct CommitArgs {
   const int32_t* block_tables;
   const int32_t* context_lens;
   const int32_t* query_lens;
+  const int32_t* seq_lens;          // as plan_step wrote them, or nullptr
   const int32_t* accepted;          // [num_seqs, max_accepted]
   const int32_t* accept_lens;       // [num_seqs]
   int32_t* new_lens;                // optional output
