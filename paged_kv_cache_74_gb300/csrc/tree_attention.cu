@@ -204,8 +204,8 @@ __device__ __forceinline__ void pin(uint32_t (&r)[N]) {
 struct TreeSeg {
   int r, q0, node0, nodes;  // q0: the request's first row; the unit's nodes
   int ctx, n_new, j0, j1;
-  int kvh, kind, c0, c1;
-  int pad[4];
+  int kvh, kind;
+  int pad[6];
 };
 static_assert(sizeof(TreeSeg) == 64, "segment record");
 
@@ -731,6 +731,19 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
           steps[i] = req_steps(p);
         }
       };
+      // The first request with rows behind request r, or num_seqs: idle ones may be most of a
+      // batch of fixed slots.
+      auto next_request = [&](int r) -> int {
+        for (int rc = r + 1; rc < a.num_seqs; rc += 128) {
+          load_requests(rc);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const unsigned hit = __ballot_sync(0xffffffffu, tiles[i] > 0);
+            if (hit != 0) return rc + 32 * i + __ffs(hit) - 1;
+          }
+        }
+        return a.num_seqs;
+      };
       long long st = 0, un = 0;
       for (int rc = 0; rc < a.num_seqs; rc += 128) {
         load_requests(rc);
@@ -790,12 +803,15 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
           if (j >= n_u) {  // no step of this unit starts in the range: the next one
             cb += CS + CT * n_u;
             j = 0;
+            if (cb + CS >= x1) break;  // (before looking for a unit that the range does not reach)
             if (++u == H * p.tiles) {
               u = 0;
-              do {
-                p = tree_req(a, ++r);
-              } while (p.tiles == 0 && r < a.num_seqs);
-              if (p.tiles == 0) break;  // no more work
+              p = tree_req(a, ++r);
+              if (p.tiles == 0) {
+                r = next_request(r);
+                p = tree_req(a, r);
+                if (p.tiles == 0) break;  // no more work
+              }
               n_u = req_steps(p);
             }
           }
