@@ -731,19 +731,6 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
           steps[i] = req_steps(p);
         }
       };
-      // The first request with rows behind request r, or num_seqs: idle ones may be most of a
-      // batch of fixed slots.
-      auto next_request = [&](int r) -> int {
-        for (int rc = r + 1; rc < a.num_seqs; rc += 128) {
-          load_requests(rc);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const unsigned hit = __ballot_sync(0xffffffffu, tiles[i] > 0);
-            if (hit != 0) return rc + 32 * i + __ffs(hit) - 1;
-          }
-        }
-        return a.num_seqs;
-      };
       long long st = 0, un = 0;
       for (int rc = 0; rc < a.num_seqs; rc += 128) {
         load_requests(rc);
@@ -806,12 +793,22 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
             if (cb + CS >= x1) break;  // (before looking for a unit that the range does not reach)
             if (++u == H * p.tiles) {
               u = 0;
-              p = tree_req(a, ++r);
-              if (p.tiles == 0) {
-                r = next_request(r);
-                p = tree_req(a, r);
-                if (p.tiles == 0) break;  // no more work
-              }
+              // The next request with rows (idle ones may be most of a batch of fixed slots), 32 at a
+              // time: 30000 idle ones behind four live requests 3.35 ms one by one, 0.73 ms so.  (128 at a
+              // time, unrolled: 1 to 3 % slower on batches without idle ones, code.)
+              TreeReq c;
+              unsigned hit;
+              do {
+                c = tree_req(a, r + 1 + lane);
+                hit = __ballot_sync(0xffffffffu, c.tiles > 0);
+                r += hit != 0 ? __ffs(hit) : 32;
+              } while (hit == 0 && r < a.num_seqs);
+              if (hit == 0) break;  // no more work
+              const int from = __ffs(hit) - 1;
+              p.q0 = __shfl_sync(0xffffffffu, c.q0, from);
+              p.n = __shfl_sync(0xffffffffu, c.n, from);
+              p.len = __shfl_sync(0xffffffffu, c.len, from);
+              p.tiles = __shfl_sync(0xffffffffu, c.tiles, from);
               n_u = req_steps(p);
             }
           }
