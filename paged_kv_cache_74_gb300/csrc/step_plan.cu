@@ -167,6 +167,68 @@ __device__ __forceinline__ StepNeed step_need(const PlanStepArgs& a, int r, bool
   return s;
 }
 
+// Whether `mine` holds for a thread of the cluster.  What a thread has written before is there
+// for the others behind it.
+__device__ __forceinline__ bool cluster_any(cg::cluster_group& cluster, Exchange* ex, bool mine) {
+  __threadfence();
+  const int any = __syncthreads_or(mine);
+  cluster_started(cluster);  // (every thread has read the sums of the exchange before)
+  long long before[2], all[2];
+  exchange(cluster, ex, any, 0, &before[0], &before[1], &all[0], &all[1]);
+  return all[0] != 0;
+}
+
+// Depths of the rows in their trees, which may be long ones (no masks): row t's, shifted
+// up by 32 bits, into slot_mapping[t], which has its slots only later.  A row walks up
+// kWalk parents by itself.  Where that does not end in a root, rows double what they have
+// walked: with (ancestor a, steps d) of each row, (a, d) becomes (a's ancestor, d + a's
+// steps), until every row has come to its root, ceil(log2(depth / kWalk)) rounds.  A
+// pair is one 64-bit word, true at any time, so rows may read each other's while they change.
+// Walked to the end by each row a chain of 120000 rows took 264 ms, now 0.29.
+// request_of(t): the request of row t and its first row, or -1 where it was refused.
+constexpr int kWalk = 64;
+template <typename F>
+__device__ void tree_depths(cg::cluster_group& cluster, Exchange* ex, const PlanStepArgs& a, int live, F request_of) {
+  const int stride = static_cast<int>(cluster.num_blocks()) * kThreads;
+  const int t0 = static_cast<int>(cluster.block_rank()) * kThreads + threadIdx.x;
+  auto pair_of = [](int ancestor, int steps) -> long long {
+    return static_cast<long long>(steps) << 32 | static_cast<unsigned>(ancestor);
+  };
+  bool on = false;
+  for (long long t = t0; t < live; t += stride) {
+    int first = 0;
+    const int r = request_of(t, &first);
+    int ancestor = -1, steps = 0;
+    if (r >= 0) {
+      int node = static_cast<int>(t) - first;
+      while (true) {
+        const int up = __ldg(a.parents + first + node);
+        if (up < -1 || up >= node) record_error(a.status, PA_DEV_BAD_PARENT, r, up);
+        if (up < 0 || up >= node) break;
+        node = up;
+        if (++steps == kWalk) {
+          ancestor = first + node;
+          on = true;
+          break;
+        }
+      }
+    }
+    __stcg(reinterpret_cast<long long*>(a.slot_mapping) + t, pair_of(ancestor, steps));
+  }
+  while (cluster_any(cluster, ex, on)) {
+    on = false;
+    for (long long t = t0; t < live; t += stride) {
+      const long long mine = __ldcg(reinterpret_cast<const long long*>(a.slot_mapping) + t);
+      const int ancestor = static_cast<int>(mine);
+      if (ancestor < 0) continue;
+      const long long other = __ldcg(reinterpret_cast<const long long*>(a.slot_mapping) + ancestor);
+      __stcg(reinterpret_cast<long long*>(a.slot_mapping) + t,
+             pair_of(static_cast<int>(other), static_cast<int>((mine >> 32) + (other >> 32))));
+      on = on || static_cast<int>(other) >= 0;
+    }
+  }
+}
+
 __global__ void __launch_bounds__(kThreads) plan_step_kernel(const PlanStepArgs a) {
   __shared__ long long warp_sums[kThreads / 32][2];
   __shared__ Exchange ex;
@@ -261,8 +323,26 @@ __global__ void __launch_bounds__(kThreads) plan_step_kernel(const PlanStepArgs 
   auto context = [&](int r) -> int {
     return cached ? contexts[r] : (__ldcg(a.seq_lens + r) > 0 ? __ldcg(a.context_lens + r) : -1);
   };
+  auto request_of = [&](long long t) -> int {  // the last one whose first row is at or before t
+    int lo = 0, hi = S;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (first_row(mid) <= t)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    return lo;
+  };
   const int live = fits ? static_cast<int>(all_rows) : 0;
   const int stride = ctas * kThreads;
+  const bool long_trees = a.parents != nullptr && a.words == 0;
+  if (long_trees)
+    tree_depths(cluster, &ex, a, live, [&](long long t, int* first) -> int {
+      const int r = request_of(t);
+      *first = first_row(r);
+      return context(r) < 0 ? -1 : r;
+    });
   for (long long t64 = static_cast<long long>(rank) * kThreads + tid; t64 < a.max_tokens;
        t64 += static_cast<long long>(kRows) * stride) {
     int req[kRows], row_in[kRows], pos[kRows], id[kRows];
@@ -271,14 +351,7 @@ __global__ void __launch_bounds__(kThreads) plan_step_kernel(const PlanStepArgs 
       const long long t = t64 + static_cast<long long>(u) * stride;
       req[u] = -1;
       if (t >= live) continue;
-      int lo = 0, hi = S;  // the last request whose first row is at or before t
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (first_row(mid) <= t)
-          lo = mid;
-        else
-          hi = mid;
-      }
+      const int lo = request_of(t);
       const int ctx = context(lo);
       if (ctx < 0) continue;
       req[u] = lo;
@@ -300,8 +373,10 @@ __global__ void __launch_bounds__(kThreads) plan_step_kernel(const PlanStepArgs 
         else
           record_error(a.status, PA_DEV_BAD_BLOCK_ID, req[u], id[u]);
         place = pos[u];
-        if (a.parents != nullptr) {
-          // Up the tree: every parent comes before its child, so the walk ends.
+        if (long_trees) {
+          place += static_cast<int>(__ldcg(reinterpret_cast<const long long*>(a.slot_mapping) + t) >> 32) - i;
+        } else if (a.parents != nullptr) {
+          // Up the tree, 64 * words parents at most: every one comes before its child.
           const int32_t* parents = a.parents + (t - i);
           int depth = 0, node = i;
           while (true) {
