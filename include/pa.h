@@ -781,7 +781,8 @@ pa_status pa_tree_attention(void* out, const void* q, const void* key_cache,
  * pa_tree_attention_fp8 -- pa_tree_attention over e4m3 caches, as pa_prefill_varlen_fp8
  * is to pa_prefill_varlen.  The scores are e4m3 products, q the sum of two e4m3 numbers in
  * units of its row: exact for every q down to 2^-9 of the row's largest, off by at most 2^-17 of the
- * largest below; q beyond +-2^48 saturates.  Weights are rounded to f16, V is exact.
+ * largest below; finite q beyond +-2^48 saturates, a row with an infinity or a NaN gives NaNs.
+ * Weights are rounded to f16, V is exact.
  */
 pa_status pa_tree_attention_fp8(void* out, const void* q, const void* key_cache,
                                 const void* value_cache, const int32_t* query_start_loc,

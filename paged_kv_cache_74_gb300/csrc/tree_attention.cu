@@ -291,7 +291,8 @@ __device__ __forceinline__ void split_q(uint32_t q, int8_t* exps, int w4, int la
     m2 = max(m2, __shfl_xor_sync(0xffffffffu, m2, 16));  // (all of the warp's rows are read)
     // (Beyond 2^47 a row saturates; rows of zeros and of values below 2^-93 take the last step.)
     const int e = min(max(134 - static_cast<int>(m2 >> 7), -40), 100);
-    const float s = __int_as_float((e + 127) << 23);
+    // (A row with an infinity or a NaN becomes NaNs: e4m3 numbers saturate, so it would come out finite.)
+    const float s = __int_as_float(m2 >= 0x7f80u ? 0x7fffffff : (e + 127) << 23);
     if (part == 0) exps[r] = static_cast<int8_t>(e);
     __syncwarp();
 #pragma unroll
