@@ -466,7 +466,9 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
       if constexpr (KV8) {
         // The row's scores carry 2^e of its q.
         if (!(ok = warp_wait(C::QCONV, seg & 1, 79))) break;
-        sl2 = a.scale_log2 * __int_as_float((127 - exps[(two ? b * 128 : 0) + i_row]) << 23);
+        // (Not 0 for tiny scales: unseen scores are -inf.  Seen ones are below 2^27, so at the
+        // smallest normal number they are 0 as good as exactly.)
+        sl2 = fmaxf(a.scale_log2 * __int_as_float((127 - exps[(two ? b * 128 : 0) + i_row]) << 23), 1.17549435e-38f);
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(C::EXPFREE));
       }
