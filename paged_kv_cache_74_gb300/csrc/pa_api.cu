@@ -1405,7 +1405,8 @@ pa_status pa_plan_step(int32_t* block_tables, int32_t max_blocks_per_seq, int32_
                        int32_t mask_words, int32_t* device_status, void* stream) {
   if (num_seqs < 0 || max_blocks_per_seq < 1 || capacity < 1 || block_size < 1 || num_blocks < 1 || max_tokens < 0)
     return PA_ERR_INVALID;
-  if (tree_masks ? mask_words < 1 : mask_words != 0) return PA_ERR_INVALID;
+  // (Masks of no rows have no address.)
+  if (mask_words < 0 || (tree_masks ? mask_words < 1 : mask_words != 0 && max_tokens > 0)) return PA_ERR_INVALID;
   if (num_seqs > 65535 || mask_words > kMaxMaskWords) return PA_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(max_blocks_per_seq) * block_size > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
   if (!free_blocks || !free_count || !query_start_loc) return PA_ERR_INVALID;
