@@ -823,6 +823,8 @@ def _tree_attention(fn, cache_dtype, scales, q, key_cache, value_cache, query_st
         out = torch.empty_like(q)
     elif out.shape != q_shape:
         raise ValueError("out must have q's shape")
+    if tq == 0 or S == 0:
+        return out
     if workspace is None:
         with torch.cuda.device(dev):
             workspace = new_workspace(tree_workspace_size(S, tq, hq, hkv, d, max_seq_len), q.device)

@@ -3,6 +3,7 @@ import pytest
 import torch
 
 from test_gpu_step_plan import i32
+from test_gpu_tree import Batch
 
 pytestmark = pytest.mark.gpu
 
@@ -25,6 +26,18 @@ def test_plan_of_no_rows(cuda_lib, S, words):
     assert t["qsl"].tolist() == [0] * (S + 1) and t["seq"].tolist() == [16, 0, 20][:S]
     assert t["held"].tolist() == [1, 0, 2][:S] and t["count"].tolist() == [5 - 3 * (S > 0)]
     assert t["tables"].tolist() == [[9, 0, 0, 0], [0, 0, 0, 0], [8, 7, 0, 0]][:S] and not t["status"].any()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_attention_of_no_rows(cuda_lib, fp8):
+    b = Batch([(3, 40), (2, 0)], 4, 2, 64, fp8=fp8, seed=1)
+    scales = (1.0, 1.0) if fp8 else ()
+    call = cuda_lib.tree_attention_fp8 if fp8 else cuda_lib.tree_attention
+    got = call(b.q[:0], b.kc, b.vc, rows(3), b.sl, b.tables, b.m[:0], 3, 43, 0.125, *scales)
+    assert got.shape == (0, 4, 64)
+    out = torch.full_like(b.q, 3.5)
+    assert call(b.q, b.kc, b.vc, rows(1), rows(0), b.tables[:0], b.m, 3, 43, 0.125, *scales, out=out) is out
+    assert (out == 3.5).all()
 
 
 def test_commit_and_release_of_no_requests(cuda_lib):
