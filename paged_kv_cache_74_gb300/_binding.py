@@ -960,6 +960,8 @@ def commit_tokens(key_cache, value_cache, block_tables, context_lens, query_lens
     if len(shape) not in (4, 5) or value_cache.shape != shape:
         raise ValueError("key_cache and value_cache must be [(layers,) num_blocks, block, kv_heads, head_dim]")
     layers, nb, bs, hkv, d = shape if len(shape) == 5 else (1, *shape)
+    if layers == 0:
+        raise ValueError("key_cache and value_cache must hold a layer")
     S, width = _table_shape(block_tables)
     path = accepted.shape
     if len(path) != 2 or path[0] != S:

@@ -47,3 +47,10 @@ def test_commit_and_release_of_no_requests(cuda_lib):
     count = i32([2])
     cuda_lib.release_blocks(rows(0, 2), rows(0), rows(0), i32([1, 2, 0]), count, 16, 4)
     assert count.tolist() == [2]
+
+
+def test_commit_without_layers_is_refused(cuda_lib):
+    """(It would return lengths that nothing has written.)"""
+    kc = torch.ones(0, 4, 16, 1, 64, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError):
+        cuda_lib.commit_tokens(kc, kc, rows(1, 2), rows(1), rows(1), rows(1, 3), rows(1))
