@@ -762,7 +762,9 @@ size_t pa_tree_workspace_size(int32_t num_seqs, int32_t total_q, int32_t num_hea
  * tcgen05 products, weights rounded to bf16, one rounding of the result.  Up to 256 query
  * rows (q_len * num_heads / num_kv_heads) share each read of the keys.
  * Two kernels on `stream`: the attention, and the merge of what it has cut between
- * CTAs (not when max_seq_len <= 128).  Results depend on the batch alone.
+ * CTAs (not when max_seq_len <= 128).  A batch's results are the same bit for bit in every run with the
+ * same num_seqs, total_q and max_seq_len on the same kind of device; these also decide where work is cut
+ * and in what order its pieces are summed.
  * Block tables, sizes, workspace alignment and errors as pa_prefill_varlen; a request with
  * q_len > max_query_len, > seq_len or > 64 * mask_words is skipped with
  * PA_DEV_BAD_QUERY_LEN.

@@ -13,8 +13,10 @@
 // follow from it: nothing to compute and little to move, so what counts is the
 // chain of round trips.  One cluster does all of it in one launch: its CTAs sum
 // their slices of the requests, exchange the sums through distributed shared
-// memory, and write; the cluster barrier orders every read of the lengths, the
-// held counts and the stack before the first write, so that the state can be
+// memory, and write.  The cluster barrier of the exchange puts the sums and the stack's
+// count, which all CTAs need, before the first write; behind it a CTA reads only
+// the state of its own slice (again, where that has more requests than a CTA has
+// threads) and arrays that the call does not write.  So the state can be
 // updated in place without a workspace, a ticket or a second launch.  A second
 // cluster barrier puts the block tables before the tokens' slots, which are
 // spread evenly over the CTAs whatever the requests' lengths (the request of a
@@ -270,7 +272,7 @@ __global__ void __launch_bounds__(kThreads) plan_step_kernel(const PlanStepArgs 
       record_error(a.status, PA_DEV_OUT_OF_BLOCKS, S, static_cast<int>(min(all_blocks, 0x7fffffffll)));
   }
 
-  // Tables, offsets and lengths.  (The slices' state has been read.)
+  // Tables, offsets and lengths.
   for (int base = r0; base < r1; base += kThreads) {
     const int r = base + tid;
     if (!one) {
