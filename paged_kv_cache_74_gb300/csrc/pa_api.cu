@@ -6,6 +6,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstring>
+#include <limits>
 #include <mutex>  // std::call_once
 
 #include "pa_internal.h"
@@ -699,6 +700,10 @@ pa_status tree_attention_impl(void* out, const void* q, const void* key_cache, c
   a.total_q = total_q;
   a.num_ctas = L.num_ctas;
   a.scale_log2 = scale * k_scale * 1.4426950408889634f;
+  // Over e4m3 a row's scores, below 2^27, are multiplied by scale_log2 2^-e: for tiny scales that
+  // must not become 0, as unseen scores are -inf.  At the smallest normal number seen ones are as good as 0.
+  if (kv8) a.scale_log2 = std::max(a.scale_log2, std::numeric_limits<float>::min());
+  a.exp_max = std::min(std::ilogb(a.scale_log2), -26) + 126;
   a.o_scale = v_scale;
   return launch_tree_attention(a, qmap, kmap, vmap, head_dim, kv8, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? PA_OK

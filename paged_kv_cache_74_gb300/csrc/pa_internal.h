@@ -326,6 +326,7 @@ struct TreeArgs {
   int group_inv;                    // ceil(2^16 / group): row / group = row * group_inv >> 16 for 128 rows
   int max_seq_len, max_query_len, num_blocks, block_size, tile_shift, total_q, num_ctas;
   float scale_log2, o_scale;        // as PrefillArgs
+  int exp_max;                      // e4m3: largest power of two that a row of q is scaled by, <= 100
 };
 size_t tree_record_floats(int head_dim);  // of part_o, per CTA
 cudaError_t launch_tree_attention(const TreeArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,

@@ -270,7 +270,7 @@ __device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
 // In place: h takes the place of the rows' first halves, l of the second (head_dim 64:
 // within the row).  Warp w4 of four, a row by four lanes.
 template <int D, bool KV8>
-__device__ __forceinline__ void split_q(uint32_t q, int8_t* exps, int w4, int lane) {
+__device__ __forceinline__ void split_q(uint32_t q, int8_t* exps, int exp_max, int w4, int lane) {
   using C = TreeCfg<D, KV8>;
   constexpr int NCH = D / 32;  // 16-byte chunks of a lane
   const int part = lane >> 3;
@@ -289,8 +289,9 @@ __device__ __forceinline__ void split_q(uint32_t q, int8_t* exps, int w4, int la
     m2 = max(m2 & 0xffffu, m2 >> 16);
     m2 = max(m2, __shfl_xor_sync(0xffffffffu, m2, 8));
     m2 = max(m2, __shfl_xor_sync(0xffffffffu, m2, 16));  // (all of the warp's rows are read)
-    // (Beyond 2^47 a row saturates; rows of zeros and of values below 2^-93 take the last step.)
-    const int e = min(max(134 - static_cast<int>(m2 >> 7), -40), 100);
+    // (Beyond 2^47 a row saturates; rows of zeros and of values below 2^-93 take the last step,
+    // or exp_max, which keeps scale 2^-e a normal number.)
+    const int e = min(max(134 - static_cast<int>(m2 >> 7), -40), exp_max);
     // (A row with an infinity or a NaN becomes NaNs: e4m3 numbers saturate, so it would come out finite.)
     const float s = __int_as_float(m2 >= 0x7f80u ? 0x7fffffff : (e + 127) << 23);
     if (part == 0) exps[r] = static_cast<int8_t>(e);
@@ -466,9 +467,7 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
       if constexpr (KV8) {
         // The row's scores carry 2^e of its q.
         if (!(ok = warp_wait(C::QCONV, seg & 1, 79))) break;
-        // (Not 0 for tiny scales: unseen scores are -inf.  Seen ones are below 2^27, so at the
-        // smallest normal number they are 0 as good as exactly.)
-        sl2 = fmaxf(a.scale_log2 * __int_as_float((127 - exps[(two ? b * 128 : 0) + i_row]) << 23), 1.17549435e-38f);
+        sl2 = a.scale_log2 * __int_as_float((127 - exps[(two ? b * 128 : 0) + i_row]) << 23);
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(C::EXPFREE));
       }
@@ -1087,7 +1086,7 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
           if (seg > 0 && !(ok = warp_wait(C::EXPFREE, (seg - 1) & 1, 78))) break;
           for (int qb = 0; qb < nsl && ok; ++qb)
             if ((ok = warp_wait(C::QFULL + qb, qn[qb]++ & 1, 65)))
-              split_q<D, KV8>(q_s + qb * C::QBYTES, exps + qb * 128, w4, lane);
+              split_q<D, KV8>(q_s + qb * C::QBYTES, exps + qb * 128, a.exp_max, w4, lane);
           if (!ok) break;
           fence_proxy_async_smem();
           __syncwarp();
