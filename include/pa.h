@@ -700,7 +700,8 @@ pa_status pa_prefill_varlen_masked_fp8(void* out, const void* q, const void* key
  * batch, when its rows exceed max_tokens (PA_DEV_BAD_QUERY_LEN, request index
  * num_seqs) or its blocks *free_count (PA_DEV_OUT_OF_BLOCKS): every seq_lens 0,
  * every slot -1, tables, held_blocks and the list as they were.  Attention calls
- * then skip the rows (q_len > seq_len).
+ * then skip the rows (q_len > seq_len), as does pa_commit_planned_tokens.  A block id of the list that is
+ * out of range is recorded and entered as it is; its rows get slot -1.
  * num_seqs up to 65535 and max_tokens >= 0; num_seqs == 0 still fills the rows.
  * No output may overlap an input or another output (PA_ERR_INVALID).
  */

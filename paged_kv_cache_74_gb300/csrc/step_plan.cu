@@ -22,8 +22,8 @@
 // spread evenly over the CTAs whatever the requests' lengths (the request of a
 // token by bisection of the row offsets).  Blocks are spread over a CTA's threads the
 // same way: with a request's blocks on a warp 67 requests, four of them prompts of up to
-// 11000 tokens, took 26.8 + 20.5 us (plan, release), now 16.8 + 6.2; 256 requests with trees of
-// 8 to 24 rows 14.2 + 5.4, four small requests 8.3 + 4.9, each alone with cold caches.
+// 11000 tokens, took 26.8 + 20.5 us (plan, release), now 17.1 + 5.7; 256 requests with trees of
+// 8 to 24 rows 14.5 + 5.5, four small requests 8.4 + 5.0, each alone with cold caches.
 #include <cooperative_groups.h>
 
 #include <algorithm>
