@@ -80,6 +80,7 @@ __device__ __forceinline__ void block_scan2(long long a, long long b, long long 
 
 struct Exchange {
   long long rows[kMaxCluster], blocks[kMaxCluster];  // sums of each CTA's slice
+  int flags[kMaxCluster];
 };
 
 // Shared memory of a CTA that has not started may not be written: every CTA arrives on the
@@ -89,20 +90,22 @@ __device__ __forceinline__ void cluster_started(cg::cluster_group& cluster) {
   if (cluster.num_blocks() > 1) cluster_arrive();
 }
 
-// This CTA's sums to every CTA of the cluster; returns the sums of the slices
-// before this one and of all.  Ends in a cluster barrier.
-__device__ __forceinline__ void exchange(cg::cluster_group& cluster, Exchange* ex, long long rows, long long blocks,
-                                         long long* rows_before, long long* blocks_before, long long* rows_all,
-                                         long long* blocks_all) {
+// This CTA's sums and flag to every CTA of the cluster; gives the sums of the slices
+// before this one and of all, and whether any flag is set.  Ends in a cluster barrier.
+__device__ __forceinline__ bool exchange(cg::cluster_group& cluster, Exchange* ex, long long rows, long long blocks,
+                                         int flag, long long* rows_before, long long* blocks_before,
+                                         long long* rows_all, long long* blocks_all) {
   const int rank = static_cast<int>(cluster.block_rank()), n = static_cast<int>(cluster.num_blocks());
   if (n > 1) cluster_wait();  // for cluster_started(): every CTA's shared memory is there
   if (static_cast<int>(threadIdx.x) < n) {
     Exchange* to = cluster.map_shared_rank(ex, threadIdx.x);
     to->rows[rank] = rows;
     to->blocks[rank] = blocks;
+    to->flags[rank] = flag;
   }
   cluster.sync();
   long long rb = 0, bb = 0, ra = 0, ba = 0;
+  int any = 0;
   for (int c = 0; c < n; ++c) {
     if (c < rank) {
       rb += ex->rows[c];
@@ -110,11 +113,13 @@ __device__ __forceinline__ void exchange(cg::cluster_group& cluster, Exchange* e
     }
     ra += ex->rows[c];
     ba += ex->blocks[c];
+    any |= ex->flags[c];
   }
   *rows_before = rb;
   *blocks_before = bb;
   *rows_all = ra;
   *blocks_all = ba;
+  return any != 0;
 }
 
 // Runs f(i, j, e) for the entries e = 0 .. total - 1 of the block's kThreads requests, entry
@@ -176,11 +181,11 @@ __device__ __forceinline__ bool cluster_any(cg::cluster_group& cluster, Exchange
   const int any = __syncthreads_or(mine);
   cluster_started(cluster);  // (every thread has read the sums of the exchange before)
   long long before[2], all[2];
-  exchange(cluster, ex, any, 0, &before[0], &before[1], &all[0], &all[1]);
-  return all[0] != 0;
+  return exchange(cluster, ex, 0, 0, any, &before[0], &before[1], &all[0], &all[1]);
 }
 
-// Depths of the rows in their trees, which may be long ones (no masks): row t's, shifted
+// Depths of the rows in their trees where some are longer than kShortTree (without masks; up
+// to there a row walks to its root where its slot is written, 2 to 4 us less): row t's, shifted
 // up by 32 bits, into slot_mapping[t], which has its slots only later.  A row walks up
 // kWalk parents by itself.  Where that does not end in a root, rows double what they have
 // walked: with (ancestor a, steps d) of each row, (a, d) becomes (a's ancestor, d + a's
@@ -188,6 +193,7 @@ __device__ __forceinline__ bool cluster_any(cg::cluster_group& cluster, Exchange
 // pair is one 64-bit word, true at any time, so rows may read each other's while they change.
 // Walked to the end by each row a chain of 120000 rows took 264 ms, now 0.29.
 // request_of(t): the request of row t and its first row, or -1 where it was refused.
+constexpr int kShortTree = 64 * kMaxMaskWords;
 constexpr int kWalk = 64;
 template <typename F>
 __device__ void tree_depths(cg::cluster_group& cluster, Exchange* ex, const PlanStepArgs& a, int live, F request_of) {
@@ -253,16 +259,20 @@ __global__ void __launch_bounds__(kThreads) plan_step_kernel(const PlanStepArgs 
   // Sums of this CTA's slice.
   long long rows = 0, blocks = 0, e0, e1, ta, tb;
   StepNeed s{0, 0, 0, 0, 0, false};
+  bool long_tree = false;
   for (int base = r0; base < r1; base += kThreads) {
     const int r = base + tid;
     s = StepNeed{0, 0, 0, 0, 0, false};
     if (r < r1) s = step_need(a, r, true);
+    long_tree = long_tree || s.rows > kShortTree;
     block_scan2(s.rows, s.blocks, warp_sums, &e0, &e1, &ta, &tb);
     rows += ta;
     blocks += tb;
   }
   long long row, block, all_rows, all_blocks;
-  exchange(cluster, &ex, rows, blocks, &row, &block, &all_rows, &all_blocks);
+  int flag = 0;
+  if (a.parents != nullptr && a.words == 0) flag = __syncthreads_or(long_tree);
+  const bool long_trees = exchange(cluster, &ex, rows, blocks, flag, &row, &block, &all_rows, &all_blocks);
   // All or nothing: a batch that does not fit leaves tables, counts and stack alone.
   const bool fits = all_rows <= a.max_tokens && count >= 0 && count <= a.capacity && all_blocks <= count;
   if (!fits && rank == 0 && tid == 0) {
@@ -338,7 +348,6 @@ __global__ void __launch_bounds__(kThreads) plan_step_kernel(const PlanStepArgs 
   };
   const int live = fits ? static_cast<int>(all_rows) : 0;
   const int stride = ctas * kThreads;
-  const bool long_trees = a.parents != nullptr && a.words == 0;
   if (long_trees)
     tree_depths(cluster, &ex, a, live, [&](long long t, int* first) -> int {
       const int r = request_of(t);
@@ -378,7 +387,7 @@ __global__ void __launch_bounds__(kThreads) plan_step_kernel(const PlanStepArgs 
         if (long_trees) {
           place += static_cast<int>(__ldcg(reinterpret_cast<const long long*>(a.slot_mapping) + t) >> 32) - i;
         } else if (a.parents != nullptr) {
-          // Up the tree, 64 * words parents at most: every one comes before its child.
+          // Up the tree, kShortTree parents at most: every one comes before its child.
           const int32_t* parents = a.parents + (t - i);
           int depth = 0, node = i;
           while (true) {
@@ -453,7 +462,7 @@ __global__ void __launch_bounds__(kThreads) release_blocks_kernel(const ReleaseA
     blocks += tb;
   }
   long long row, block, all_rows, all;
-  exchange(cluster, &ex, 0, blocks, &row, &block, &all_rows, &all);
+  exchange(cluster, &ex, 0, blocks, 0, &row, &block, &all_rows, &all);
   if (count < 0 || count + all > a.capacity) {  // more blocks than there are: given back twice
     if (rank == 0 && tid == 0)
       record_error(a.status, PA_DEV_OUT_OF_BLOCKS, S, static_cast<int>(min(count + all, 0x7fffffffll)));

@@ -51,6 +51,7 @@ def trees(new, kind, seed):
 @pytest.mark.parametrize("kind", ["chain", "near", "random", "two"])
 @pytest.mark.parametrize("new", [
     [64], [65], [66], [129], [1000], [300, 0, 1, 700],           # one CTA; at and behind 64 parents
+    [256], [257], [321], [256] * 20, [256] * 19 + [257],         # at and behind 256 rows
     [4097], [64, 65, 4000, 1, 0, 8191], [70000], [5] * 1200 + [20000, 3],
 ])
 def test_depths(cuda_lib, new, kind):
